@@ -1,4 +1,4 @@
-"""ctypes mirror of include/gdn.h and the loader of libgdn.so.
+"""ctypes mirror of include/gdn.h and include/gdn_train.h and the loader of libgdn.so.
 
 The library is loaded after torch so that it binds to the HIP runtime torch
 already holds (both answer to the soname libamdhip64.so.7).  There is no
@@ -22,11 +22,15 @@ GDN_PATH_TOKEN, GDN_PATH_CHUNKED = 0, 1
 GDN_PREFILL_MAX_DEFAULT = -1
 GDN_MIXED_AUTO, GDN_MIXED_ONE_LAUNCH, GDN_MIXED_TWO_LAUNCHES = 0, 1, 2
 GDN_NOALLOC_SYNC_WORDS = 65536
+GDNT_SCAN_BLOCK, GDNT_CKPT_ROWS, GDNT_CKPT_CHANNELS = 256, 16, 4
+GDNT_DEVERR_TIMEOUT = 32
 
 SYMBOLS = ("gdn_abi_version", "gdn_status_str", "gdn_spec_page_layout", "gdn_chunked_workspace_bytes",
            "gdn_conv_update", "gdn_recurrent_seq", "gdn_recurrent_seq_noalloc", "gdn_chunked_prefill", "gdn_prefill_path", "gdn_prefill",
            "gdn_spec_verify", "gdn_spec_verify_cached", "gdn_prefix_restore", "gdn_mixed_step",
-           "gdn_mixed_launches", "gdn_mixed_step_launches")
+           "gdn_mixed_launches", "gdn_mixed_step_launches",
+           "gdnt_scan_workspace_bytes", "gdnt_scan_saved_bytes", "gdnt_conv_workspace_bytes",
+           "gdnt_scan_forward", "gdnt_scan_backward", "gdnt_conv_backward")
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -77,6 +81,14 @@ class GdnVerifyPart(ctypes.Structure):
                 ("n_req", _i32), ("n_cand", _i32), ("req_page", _vp), ("num_accepted", _vp),
                 ("step_parity", _vp), ("pages", _vp), ("page_bytes", _i64), ("n_pages", _i32),
                 ("conv", GdnConvPool), ("o", _vp)]
+
+
+class GdntScanDims(ctypes.Structure):
+    _fields_ = [("channels", _i32), ("act_dtype", _i32), ("state_dtype", _i32)]
+
+
+class GdntScanParams(ctypes.Structure):
+    _fields_ = [("a_log", _vp), ("dt_bias", _vp)]
 
 
 _lib = None
@@ -144,5 +156,24 @@ def load() -> ctypes.CDLL:
     L.gdn_mixed_step_launches.restype = _i32
     L.gdn_mixed_step_launches.argtypes = [ctypes.POINTER(GdnDims), ctypes.POINTER(GdnParams),
                                           ctypes.POINTER(GdnSeqPart), ctypes.POINTER(GdnVerifyPart), _i32, _vp, _vp]
+    sz, szp = ctypes.c_size_t, ctypes.POINTER(ctypes.c_size_t)
+    L.gdnt_scan_workspace_bytes.restype = _i32
+    L.gdnt_scan_workspace_bytes.argtypes = [ctypes.POINTER(GdntScanDims), _i32, _i64, szp]
+    L.gdnt_scan_saved_bytes.restype = _i32
+    L.gdnt_scan_saved_bytes.argtypes = [ctypes.POINTER(GdntScanDims), _i64, szp, szp]
+    L.gdnt_conv_workspace_bytes.restype = _i32
+    L.gdnt_conv_workspace_bytes.argtypes = [ctypes.POINTER(GdnDims), _i32, _i64, szp]
+    L.gdnt_scan_forward.restype = _i32
+    L.gdnt_scan_forward.argtypes = [ctypes.POINTER(GdntScanDims), ctypes.POINTER(GdntScanParams), _vp, _i64, _vp, _vp,
+                                    _i64, ctypes.POINTER(GdnBatch), GdnStatePool, GdnStatePool, _vp, _i64, _vp, _vp,
+                                    _vp, sz, _vp, _vp]
+    L.gdnt_scan_backward.restype = _i32
+    L.gdnt_scan_backward.argtypes = [ctypes.POINTER(GdntScanDims), ctypes.POINTER(GdntScanParams), _vp, _i64, _vp, _vp,
+                                     _i64, _vp, ctypes.POINTER(GdnBatch), GdnStatePool, _vp, _vp, _i64, _vp,
+                                     _vp, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _vp, sz, _vp, _vp]
+    L.gdnt_conv_backward.restype = _i32
+    L.gdnt_conv_backward.argtypes = [ctypes.POINTER(GdnDims), _vp, _vp, _i64, _vp, _i32, _i64,
+                                     ctypes.POINTER(GdnBatch), GdnConvPool, _i32, _vp, _vp, _i64, _vp, _vp,
+                                     _vp, sz, _vp, _vp]
     _lib = L
     return L

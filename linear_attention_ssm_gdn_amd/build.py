@@ -2,7 +2,7 @@
 
 Every translation unit is compiled by hipcc for gfx950 only, in parallel,
 then linked into one shared library that exports the gdn_* symbols of
-include/gdn.h and nothing else.
+include/gdn.h, the gdnt_* symbols of include/gdn_train.h and nothing else.
 """
 import concurrent.futures as cf
 import os
@@ -17,7 +17,7 @@ OBJ = os.path.join(HERE, "_build")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["gdn_api.cpp", "gdn_seq.hip", "gdn_conv.hip", "gdn_verify.hip", "gdn_chunked.hip", "gdn_mixed.hip",
-           "gdn_noalloc.hip"]
+           "gdn_noalloc.hip", "gdnt_api.cpp", "gdnt_map.hip", "gdnt_scan.hip", "gdnt_conv.hip"]
 FLAGS = [
     "--offload-arch=gfx950", "-mcode-object-version=5", "-O3", "-std=c++17", "-fPIC",
     "-fvisibility=hidden", "-ffp-contract=off", "-Wall", "-Wno-unused-function",

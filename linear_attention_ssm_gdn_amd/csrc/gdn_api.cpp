@@ -8,6 +8,7 @@
 
 #include "../../include/gdn.h"
 #include "gdn_kernels.h"
+#include "gdnt_kernels.h"
 
 #define GDN_EXPORT extern "C" __attribute__((visibility("default")))
 
@@ -137,6 +138,9 @@ gdn::VerifyArgs verify_args(const gdn_dims* dims, const gdn_params* params, cons
 }  // namespace
 
 namespace gdn {
+// The structural checks, for the entry points of gdnt_api.cpp that take gdn_dims.
+int32_t dims_status(const gdn_dims* d) { return check_dims(d); }
+
 // Validation and argument block of a token-by-token call whose sync words
 // the caller does not supply (conv.sync may be NULL): used by the entry
 // point that keeps them in the library's own device array.

@@ -1,0 +1,137 @@
+// gdnt_device.hpp -- device helpers of the training-side operators: rows of
+// four channels, the row map, the gates of the vector-state recurrence.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gdn_device.hpp"
+#include "gdnt_kernels.h"
+#include "../../include/gdn_train.h"
+
+namespace gdnt {
+
+using gdn::bf16_t;
+using gdn::from_f32;
+using gdn::to_f32;
+
+// Four channels of a row as they are stored.
+template <typename T> struct Raw4;
+template <> struct Raw4<bf16_t> {
+    uint2 v;
+    __device__ __forceinline__ float get(int i) const {
+        const uint32_t w = (i & 2) ? v.y : v.x;
+        return __uint_as_float((i & 1) ? (w & 0xffff0000u) : (w << 16));
+    }
+    __device__ __forceinline__ void set(int i, bf16_t e) {
+        uint32_t& w = (i & 2) ? v.y : v.x;
+        w = (i & 1) ? ((w & 0xffffu) | ((uint32_t)e << 16)) : ((w & 0xffff0000u) | e);
+    }
+};
+template <> struct Raw4<float> {
+    float4 v;
+    __device__ __forceinline__ float get(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+    __device__ __forceinline__ void set(int i, float e) { (i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w) = e; }
+};
+
+template <typename T> __device__ __forceinline__ Raw4<T> zero4() {
+    Raw4<T> r;
+    __builtin_memset(&r, 0, sizeof(r));
+    return r;
+}
+
+// p: the first of the four channels; nc: how many of them exist (VEC: 4).
+template <typename T, bool VEC> __device__ __forceinline__ Raw4<T> load4(const T* p, int nc) {
+    Raw4<T> r = zero4<T>();
+    if constexpr (VEC) {
+        r.v = *reinterpret_cast<const decltype(r.v)*>(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < nc) r.set(i, p[i]);
+    }
+    return r;
+}
+template <bool VEC> __device__ __forceinline__ void store4(bf16_t* p, const float (&f)[4], int nc) {
+    if constexpr (VEC) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(gdn::f32x2_to_bf16x2(f[0], f[1]), gdn::f32x2_to_bf16x2(f[2], f[3]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < nc) p[i] = from_f32<bf16_t>(f[i]);
+    }
+}
+template <bool VEC> __device__ __forceinline__ void store4(float* p, const float (&f)[4], int nc) {
+    if constexpr (VEC) {
+        *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i < nc) p[i] = f[i];
+    }
+}
+
+// State pages and per-sequence gradients: touched once per sequence, so one
+// value at a time serves.
+__device__ __forceinline__ float load_state(const void* base, int64_t at, int32_t dtype) {
+    return dtype == GDN_BF16 ? to_f32(static_cast<const bf16_t*>(base)[at]) : static_cast<const float*>(base)[at];
+}
+__device__ __forceinline__ void store_state(void* base, int64_t at, int32_t dtype, float v) {
+    if (dtype == GDN_BF16) static_cast<bf16_t*>(base)[at] = from_f32<bf16_t>(v);
+    else static_cast<float*>(base)[at] = v;
+}
+
+__device__ __forceinline__ void raise(int32_t* err, uint32_t bit) {
+    if (err) atomicOr(reinterpret_cast<unsigned int*>(err), bit);
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTiny = 1.17549435e-38f;  // smallest normal number
+
+__device__ __forceinline__ float rcp(float v) { return __builtin_amdgcn_rcpf(v); }
+__device__ __forceinline__ float exp2_hw(float v) { return __builtin_amdgcn_exp2f(v); }
+
+// softplus(z) = max(z, 0) + log1p(t), t = e^{-|z|}, and log1p(t) =
+// 2 atanh(s), s = t / (2 + t) <= 1/3, by its series: the terms left out are
+// below 2e-8 of it.  Relative accuracy holds for small softplus too, where
+// log(1 + t) would lose it: a decay near 1 is raised to long powers.
+__device__ __forceinline__ float softplus_t(float z, float& t) {
+    t = exp2_hw(-fabsf(z) * kLog2e);
+    const float s = t * rcp(2.0f + t);
+    const float w = s * s;
+    float p = fmaf(w, 1.0f / 13.0f, 1.0f / 11.0f);
+    p = fmaf(w, p, 1.0f / 9.0f);
+    p = fmaf(w, p, 1.0f / 7.0f);
+    p = fmaf(w, p, 1.0f / 5.0f);
+    p = fmaf(w, p, 1.0f / 3.0f);
+    p = fmaf(w, p, 1.0f);
+    return fmaf(s + s, p, fmaxf(z, 0.0f));
+}
+// sigmoid(b); the hardware exponential and reciprocal, about an ulp each.
+__device__ __forceinline__ float sigmoid_hw(float b) { return rcp(1.0f + exp2_hw(-b * kLog2e)); }
+
+// Per-channel constants: dt_bias and -exp(A_log) log2(e), so that
+// e^{g} = 2^{k softplus(z)}.
+struct ChanP {
+    float dt[4], k[4];
+};
+__device__ __forceinline__ ChanP load_params(const float* a_log, const float* dt_bias, int64_t c0, int nc) {
+    ChanP p;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        p.dt[i] = i < nc ? dt_bias[c0 + i] : 0.0f;
+        p.k[i] = i < nc ? -expf(a_log[c0 + i]) * kLog2e : 0.0f;
+    }
+    return p;
+}
+
+// A run of rows as a map of the state before it: h -> a h + u, or u alone
+// where a sequence starts inside (f).  `a` stays a normal number, so a state
+// that is Inf passes through a run whose decays underflow as Inf and not as
+// NaN; a finite one is changed by less than 1e-38 of it.
+struct Run {
+    float a, u;
+};
+__device__ __forceinline__ float through(const Run& r, bool f, float h) { return f ? r.u : fmaf(r.a, h, r.u); }
+
+}  // namespace gdnt

@@ -1,0 +1,82 @@
+// gdnt_kernels.h -- argument blocks and launchers of the training-side
+// operators (the C ABI in gdnt_api.cpp validates arguments and calls these).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+struct gdn_dims;
+
+namespace gdn {
+// The checks of gdn_api.cpp on gdn_dims (GDN_OK, GDN_ERR_ARG or GDN_ERR_UNSUPPORTED).
+int32_t dims_status(const struct gdn_dims* d);
+}  // namespace gdn
+
+namespace gdnt {
+
+constexpr int kTileRows = 256;  // packed rows of a tile: also the distance of the kept states
+constexpr int kTileCols = 64;   // channels of a tile
+
+// The row map: for each packed row -1 (no sequence, or a padding or skipped
+// one) or sequence * 4 + 2 * (last row) + (first row).
+struct MapArgs {
+    const int32_t* cu; const int32_t* page_idx; int32_t n_seqs;
+    int64_t n_rows, n_map;         // rows, and rows rounded up to the tile
+    int32_t page_limit, max_len;   // 0 <= page < page_limit; max_len 0: any length
+    int32_t* map;
+    uint32_t* zero; int64_t n_zero;  // words to clear for the kernel that follows
+    // a backward pass hands the final gradient of empty sequences through:
+    // rows of `width` values, NULL src: zeros, NULL dst: nothing to do
+    const float* pass_src; float* pass_dst; int64_t pass_width;
+    int32_t* err;
+};
+
+struct ScanArgs {
+    const void* x; const void* a; const void* b; int64_t x_stride, ab_stride;
+    int64_t n_rows;
+    const int32_t* cu; const int32_t* page_idx; const uint8_t* has_init; int32_t n_seqs, max_len;
+    const float* a_log; const float* dt_bias;
+    const void* st_in; int64_t st_in_stride; void* st_out; int64_t st_out_stride; int32_t page_limit;
+    void* h; int64_t h_stride;
+    float* states;                       // kept states [n_tiles][C]
+    int8_t* q; float* q_scale;           // 8-bit checkpoint
+    // backward pass
+    const void* dh; int64_t dh_stride; const float* d_state;
+    void* dx; int64_t dx_stride; void* da; void* db; int64_t dab_stride;
+    float* d_a_log; float* d_dt_bias; float* d_state0;
+    // workspace
+    int32_t* map; uint32_t* ticket; uint64_t* chain; float* part;
+    int32_t C, act_dtype, state_dtype;
+    bool vec;                            // every row starts aligned for 4-channel vectors and C % 4 == 0
+    int32_t* err;
+};
+
+struct ConvBwdArgs {
+    const void* x; int64_t x_stride; const void* dy; int64_t dy_stride;
+    int64_t n_rows;
+    const int32_t* cu; const int32_t* page_idx; const uint8_t* has_init; int32_t n_seqs, max_len;
+    const void* conv_w; const void* window; int64_t window_stride; int32_t page_limit;
+    const float* d_window;
+    void* dx; int64_t dx_stride; float* d_conv_w; float* d_window0;
+    int32_t* map; float* part;
+    int32_t C, activation, act_dtype, dy_dtype;
+    bool vec;
+    int32_t* err;
+};
+
+inline int64_t n_tiles(int64_t n_rows) { return (n_rows + kTileRows - 1) / kTileRows; }
+inline int64_t padded_channels(int64_t C) { return (C + kTileCols - 1) / kTileCols * kTileCols; }
+
+hipError_t launch_map(const MapArgs& a, hipStream_t s);
+hipError_t launch_scan_rows(const ScanArgs& a, hipStream_t s);
+hipError_t launch_scan_forward(const ScanArgs& a, hipStream_t s);
+hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t s);
+hipError_t launch_conv_backward(const ConvBwdArgs& a, hipStream_t s);
+// out[j][c] = sum over tiles of part[tile][j][c], j < n_out, in fp64 and in tile order; out is
+// out0 (j = 0), out1 (j = 1), or out0 [C][n_out] when out1 is NULL.
+hipError_t launch_sum_tiles(const float* part, int64_t n_tiles, int32_t C, int n_out, float* out0, float* out1,
+                            hipStream_t s);
+// Chain words and partial sums of the scan's workspace (gdnt_api.cpp lays it out).
+size_t scan_chain_bytes(int64_t n_rows, int32_t C);
+
+}  // namespace gdnt

@@ -1,0 +1,129 @@
+// gdnt_map.hip -- the row map of a packed ragged batch, and the sum of
+// per-tile partial gradients.
+#include "gdnt_device.hpp"
+
+namespace gdnt {
+
+constexpr int kMapThreads = 256;
+
+// Bounds of sequence s are in range and not decreasing.
+__device__ __forceinline__ bool bounds_ok(const MapArgs& A, int c0, int c1) {
+    return c0 >= 0 && c1 >= c0 && (int64_t)c1 <= A.n_rows;
+}
+
+// Is sequence `s` free of bad bounds, given that some sequence is not?  The
+// running end of the valid sequences before it decides, so rows have one owner.
+__device__ bool valid_slow(const MapArgs& A, int s) {
+    int end = 0;
+    for (int j = 0; j <= s; ++j) {
+        const int c0 = A.cu[j], c1 = A.cu[j + 1];
+        const bool ok = c0 >= end && bounds_ok(A, c0, c1);
+        if (j == s) return ok;
+        if (ok) end = c1;
+    }
+    return false;
+}
+
+// One thread per row finds its sequence by bisection of cu_seqlens; every
+// workgroup first looks all of cu_seqlens over (n_seqs / 256 loads a thread)
+// and takes the slow scan where a bound is bad.  The first workgroup raises
+// the error bits.
+__global__ __launch_bounds__(kMapThreads) void k_row_map(const MapArgs A) {
+    const int tid = threadIdx.x;
+    const int64_t gid = (int64_t)blockIdx.x * kMapThreads + tid;
+    const int64_t stride = (int64_t)gridDim.x * kMapThreads;
+    for (int64_t i = gid; i < A.n_zero; i += stride) A.zero[i] = 0;
+
+    bool bad = false;
+    for (int s = tid; s < A.n_seqs; s += kMapThreads) bad |= !bounds_ok(A, A.cu[s], A.cu[s + 1]);
+    bad = __syncthreads_or(bad) != 0;
+
+    for (int64_t r = gid; r < A.n_map; r += stride) {
+        int seq = -1;
+        if (r < A.n_rows) {
+            if (!bad) {
+                int lo = 0, hi = A.n_seqs;  // the last s with cu[s] <= r, or -1
+                while (lo < hi) {
+                    const int mid = (lo + hi) >> 1;
+                    if ((int64_t)A.cu[mid] <= r) lo = mid + 1;
+                    else hi = mid;
+                }
+                seq = lo - 1;
+                if (seq >= 0 && (int64_t)A.cu[seq + 1] <= r) seq = -1;
+            } else {
+                int end = 0;
+                for (int s = 0; s < A.n_seqs; ++s) {
+                    const int c0 = A.cu[s], c1 = A.cu[s + 1];
+                    if (c0 < end || !bounds_ok(A, c0, c1)) continue;
+                    if ((int64_t)c0 <= r && r < (int64_t)c1) { seq = s; break; }
+                    end = c1;
+                }
+            }
+        }
+        int32_t m = -1;
+        if (seq >= 0) {
+            const int c0 = A.cu[seq], c1 = A.cu[seq + 1], page = A.page_idx[seq];
+            if (page >= 0 && page < A.page_limit && (A.max_len == 0 || c1 - c0 <= A.max_len))
+                m = seq * 4 + (r == (int64_t)c1 - 1 ? 2 : 0) + (r == (int64_t)c0 ? 1 : 0);
+        }
+        A.map[r] = m;
+    }
+
+    if (blockIdx.x == 0) {
+        for (int s = tid; s < A.n_seqs; s += kMapThreads) {
+            const int page = A.page_idx[s];
+            if (page < 0) continue;
+            if (page >= A.page_limit) raise(A.err, GDN_DEVERR_PAGE);
+            else if (bad && !valid_slow(A, s)) raise(A.err, GDN_DEVERR_BATCH);
+            else if (A.max_len > 0 && A.cu[s + 1] - A.cu[s] > A.max_len) raise(A.err, GDN_DEVERR_BATCH);
+        }
+    }
+    if (A.pass_dst) {
+        for (int s = blockIdx.x; s < A.n_seqs; s += gridDim.x) {
+            const int page = A.page_idx[s];
+            if (page < 0 || page >= A.page_limit || A.cu[s] != A.cu[s + 1]) continue;
+            if (bad && !valid_slow(A, s)) continue;
+            const int64_t at = (int64_t)s * A.pass_width;
+            for (int64_t i = tid; i < A.pass_width; i += kMapThreads)
+                A.pass_dst[at + i] = A.pass_src ? A.pass_src[at + i] : 0.0f;
+        }
+    }
+}
+
+hipError_t launch_map(const MapArgs& a, hipStream_t s) {
+    // a workgroup clears up to 16 words a thread
+    int64_t grid = (a.n_map + kMapThreads - 1) / kMapThreads;
+    const int64_t by_zero = (a.n_zero + kMapThreads * 16 - 1) / (kMapThreads * 16);
+    grid = grid > by_zero ? grid : by_zero;
+    grid = grid < 1 ? 1 : grid > 4096 ? 4096 : grid;
+    hipLaunchKernelGGL(k_row_map, dim3((unsigned)grid), dim3(kMapThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+// 64 channels by 4 groups of tiles to a workgroup; fp64, every order fixed.
+__global__ __launch_bounds__(256) void k_sum_tiles(const float* part, int64_t n_tiles, int32_t C, int64_t Cp,
+                                                   int n_out, float* out0, float* out1) {
+    __shared__ double sum[4][64];
+    const int lane = threadIdx.x & 63, group = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * 64 + lane;  // < Cp
+    const int j = blockIdx.y;
+    double acc = 0.0;
+    for (int64_t t = group; t < n_tiles; t += 4) acc += (double)part[(t * n_out + j) * Cp + c];
+    sum[group][lane] = acc;
+    __syncthreads();
+    if (group == 0 && c < C) {
+        const float v = (float)((sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]));
+        if (out1) (j == 0 ? out0 : out1)[c] = v;
+        else out0[c * n_out + j] = v;
+    }
+}
+
+hipError_t launch_sum_tiles(const float* part, int64_t n_tiles, int32_t C, int n_out, float* out0, float* out1,
+                            hipStream_t s) {
+    const int64_t Cp = padded_channels(C);
+    hipLaunchKernelGGL(k_sum_tiles, dim3((unsigned)(Cp / 64), (unsigned)n_out), dim3(256), 0, s, part, n_tiles, C, Cp,
+                       n_out, out0, out1);
+    return hipGetLastError();
+}
+
+}  // namespace gdnt
