@@ -3,162 +3,192 @@
 //   z_t = sum_j w_j X_{t-3+j},  dz_t = dy_t silu'(z_t),
 //   dX_t = sum_j w_j dz_{t+3-j},  dw_j = sum_t dz_t X_{t-3+j}.
 //
-// A tile is 256 packed rows by 64 channels: 16 lanes side by side hold four
-// channels each, 16 row groups hold 16 consecutive rows each.  A thread walks
-// its rows and the three behind them (their dz reach back into its rows)
-// with the last four X and dz in registers; the rows before and behind come
-// from the caches, where the neighbouring row groups read them too.
+// Sixteen lanes side by side hold four channels each, sixteen row groups of a
+// workgroup hold `own` consecutive rows each.  A thread walks its rows and the
+// three behind them, whose dz reach back into its rows, four rows at a time
+// with the next four already loading; the rows around its own come from the
+// caches, where the neighbouring row groups read them too.  Walking down, row
+// t completes dX of row t-3 and adds to the three after it, so seen from row
+// t there are three open sums.  The rows before a sequence's first are its
+// window: their sums are d_window0, and where a sequence ends the open sums
+// are the rows of its rolled window, where d_window joins.
 #include "gdnt_device.hpp"
 
 namespace gdnt {
 
-constexpr int CR = 16;              // rows of a thread
 constexpr int kConvThreads = 256;
 constexpr int kConvWaves = kConvThreads / 64;
-static_assert(kConvThreads / 16 * CR == kTileRows && 16 * 4 == kTileCols, "tile shape");
+constexpr int kConvGroups = kConvThreads / 16;
+
+template <typename T, typename YT> struct ConvRows {  // four rows as loaded
+    Raw4<T> x[4];
+    Raw4<YT> y[4];
+};
 
 template <typename T, typename YT, bool VEC>
-__global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArgs A, int n_cols) {
+__global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArgs A, int n_cols, int own) {
     __shared__ float s_w[kConvWaves][4][kTileCols];
     const int64_t tile = blockIdx.x / n_cols;
     const int col = (int)(blockIdx.x % n_cols);
     const int lane = threadIdx.x & 63, cl = threadIdx.x & 15, rg = threadIdx.x >> 4, wave = threadIdx.x >> 6;
     const int64_t Cp = (int64_t)n_cols * kTileCols;
-    const int64_t r0 = tile * kTileRows + rg * CR, c0 = (int64_t)col * kTileCols + cl * 4;
+    const int64_t r0 = (tile * kConvGroups + rg) * own, c0 = (int64_t)col * kTileCols + cl * 4;
     const int64_t left = (int64_t)A.C - c0;
     const int nc = left >= 4 ? 4 : left > 0 ? (int)left : 0;
-
-    // row map of r0-3 .. r0+CR+2 (entry k is row r0-3+k); the map is padded
-    // to whole tiles, rows outside it belong to nothing
-    int32_t m[CR + 6];
     const int64_t n_map = (A.n_rows + kTileRows - 1) / kTileRows * kTileRows;
+
+    // bit k + 3 stands for row r0 + k, k = -3 .. own + 2 < 61: is it a
+    // sequence's, and is it not the successor of the row above it
+    uint64_t in = 0, cut = 0;
 #pragma unroll
-    for (int k = 0; k < CR + 6; ++k) {
-        const int64_t r = r0 - 3 + k;
-        m[k] = r >= 0 && r < n_map ? A.map[r] : -1;
+    for (int q = 0; q < 4; ++q) {
+        const int64_t r = r0 - 3 + q * 16 + cl;
+        const int32_t m = r >= 0 && r < n_map ? A.map[r] : -1;
+        in |= ((__ballot(m >= 0) >> (lane & 48)) & 0xffffull) << (q * 16);
+        cut |= ((__ballot(m < 0 || (m & 1)) >> (lane & 48)) & 0xffffull) << (q * 16);
     }
-    float wt[4][4];  // [tap][channel]
+
+    float wt[4][4], dw[4][4];  // [tap][channel]
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) wt[j][i] = i < nc ? to_f32(static_cast<const T*>(A.conv_w)[(c0 + i) * 4 + j]) : 0.0f;
+        for (int j = 0; j < 4; ++j) {
+            wt[j][i] = i < nc ? to_f32(static_cast<const T*>(A.conv_w)[(c0 + i) * 4 + j]) : 0.0f;
+            dw[j][i] = 0.0f;
+        }
 
-    const T* px = static_cast<const T*>(A.x) + c0;
-    const YT* py = static_cast<const YT*>(A.dy) + c0;
-    T* pdx = static_cast<T*>(A.dx) + c0;
-    Raw4<T> rx[CR + 6];
-    Raw4<YT> ry[CR + 3];
-#pragma unroll
-    for (int k = 0; k < CR + 6; ++k) {
-        rx[k] = zero4<T>();
-        if (m[k] >= 0 && nc > 0) rx[k] = load4<T, VEC>(px + (r0 - 3 + k) * A.x_stride, nc);
-    }
-#pragma unroll
-    for (int k = 0; k < CR + 3; ++k) {
-        ry[k] = zero4<YT>();
-        if (m[k + 3] >= 0 && nc > 0) ry[k] = load4<YT, VEC>(py + (r0 + k) * A.dy_stride, nc);
-    }
+    const T* px = static_cast<const T*>(A.x) + r0 * A.x_stride + c0;
+    const YT* py = static_cast<const YT*>(A.dy) + r0 * A.dy_stride + c0;
+    T* pdx = static_cast<T*>(A.dx) + r0 * A.dx_stride + c0;
 
-    // X of the three rows before the current one, dz of the last four rows
-    float X[3][4], dz[4][4], dw[4][4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) { dz[j][i] = 0.0f; dw[j][i] = 0.0f; }
-
-    // before row r0: where it continues a sequence, the rows above it that do
-    // too; further up, the sequence's window
-    auto window = [&](int32_t mr, int row, float (&v)[4]) {
-        const int seq = mr >> 2;
-        const bool init = A.window && (A.has_init ? A.has_init[seq] != 0 : true);
+    auto has_init = [&](int seq) { return A.window && (A.has_init ? A.has_init[seq] != 0 : true); };
+    auto window = [&](int seq, int row, float (&v)[4]) {
+        const bool init = has_init(seq);
         const int64_t at = init ? (int64_t)A.page_idx[seq] * A.window_stride + row * (int64_t)A.C + c0 : 0;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = init && i < nc ? to_f32(static_cast<const T*>(A.window)[at + i]) : 0.0f;
     };
-    {
-        int have = 0;  // rows above r0 of the same sequence, at most 3
-        if (m[3] >= 0 && !(m[3] & 1)) have = (m[2] & 1) ? 1 : (m[1] & 1) ? 2 : 3;
+    auto put_window = [&](int seq, int row, const float (&v)[4]) {
+        if (!A.d_window0) return;
+        const bool init = has_init(seq);
+        float* p = A.d_window0 + ((int64_t)seq * 3 + row) * A.C + c0;
 #pragma unroll
-        for (int j = 0; j < 3; ++j) {  // X[j] is row r0 - 3 + j
+        for (int i = 0; i < 4; ++i)
+            if (i < nc) p[i] = init ? v[i] : 0.0f;
+    };
+    auto load = [&](ConvRows<T, YT>& g, int k) {  // rows r0 + k .. r0 + k + 3, k < own + 3
+        const uint32_t have = (uint32_t)(in >> (k + 3)) & 15u;
+        if (have == 15u && nc > 0) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) X[j][i] = rx[j].get(i);
-            if (m[3] >= 0 && j < 3 - have) window(m[3], j + have, X[j]);
-        }
-    }
-#pragma unroll
-    for (int k = 0; k < CR + 3; ++k) {  // row r0 + k
-        const int32_t mr = m[k + 3];
-        const bool in = mr >= 0, first = in && (mr & 1);
-        if (k > 0 && first) {
-#pragma unroll
-            for (int j = 0; j < 3; ++j) window(mr, j, X[j]);
-        }
-        float x0[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            x0[i] = rx[k + 3].get(i);
-            float g = ry[k].get(i);
-            if (A.activation) {
-                const float z = fmaf(wt[3][i], x0[i], fmaf(wt[2][i], X[2][i], fmaf(wt[1][i], X[1][i], wt[0][i] * X[0][i])));
-                const float sg = sigmoid_hw(z);
-                g *= sg * fmaf(z, 1.0f - sg, 1.0f);
+            for (int e = 0; e < 4; ++e) {
+                g.x[e] = load4<T, VEC>(px + (k + e) * A.x_stride, nc);
+                g.y[e] = load4<YT, VEC>(py + (k + e) * A.dy_stride, nc);
             }
-            dz[0][i] = dz[1][i]; dz[1][i] = dz[2][i]; dz[2][i] = dz[3][i];
-            dz[3][i] = in ? g : 0.0f;
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                g.x[e] = zero4<T>();
+                g.y[e] = zero4<YT>();
+                if ((have >> e & 1u) && nc > 0) {
+                    g.x[e] = load4<T, VEC>(px + (k + e) * A.x_stride, nc);
+                    g.y[e] = load4<YT, VEC>(py + (k + e) * A.dy_stride, nc);
+                }
+            }
         }
-        if (k < CR) {
+    };
+
+    // X of the three rows before the current one and the open sums of the same rows
+    float X[3][4], acc[3][4] = {};
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+        Raw4<T> v = zero4<T>();
+        if ((in >> j & 1) && nc > 0) v = load4<T, VEC>(px + (j - 3) * A.x_stride, nc);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) X[j][i] = v.get(i);
+    }
+    if ((in >> 3 & 1) && !(cut >> 3 & 1) && (cut >> 1 & 3)) {  // a sequence begins one or two rows above r0
+        const int have = (cut >> 2 & 1) ? 1 : 2, seq = A.map[r0] >> 2;
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            if (j < 3 - have) window(seq, j + have, X[j]);
+    }
+
+    ConvRows<T, YT> now, next;
+    load(now, 0);
+    for (int k0 = 0; k0 < own + 3; k0 += 4) {  // own + 3 is a multiple of 4
+        if (k0 + 4 < own + 3) load(next, k0 + 4);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int k = k0 + e;
+            // the rows k, k - 1, k - 2 and whether a sequence begins there
+            const uint32_t near = (uint32_t)(cut >> (k + 1)) & 7u;
+            if (near & 4u) {
+                if (k > 0 && (in >> (k + 2) & 1)) {  // row k - 1 ended its sequence
+                    const int seq = A.map[r0 + k - 1] >> 2;
+                    // bit d: a sequence begins at row k - 1 - d
+                    const uint32_t begins = ((near >> 1 & 1u) | (near << 1 & 2u));
+                    const int rows = (begins & 1u) ? 1 : (begins & 2u) ? 2 : 3;  // of the sequence, 3: or more
+#pragma unroll
+                    for (int j = 0; j < 3; ++j) {
+                        const int p = k - 3 + j;  // the row this sum belongs to, if it is one
+                        if (A.d_window) {
+                            const float* src = A.d_window + ((int64_t)seq * 3 + j) * A.C + c0;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (i < nc) acc[j][i] += src[i];
+                        }
+                        if (j >= 3 - rows) {
+                            if (p >= 0 && p < own && nc > 0) store4<VEC>(pdx + p * A.dx_stride, acc[j], nc);
+                        } else if (k - rows >= 0) {  // the sequence begins in this thread's rows
+                            put_window(seq, rows + j, acc[j]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
+                if (k >= own) goto done;  // the rest is the next thread's
+                if (in >> (k + 3) & 1) {
+                    const int seq = A.map[r0 + k] >> 2;
+#pragma unroll
+                    for (int j = 0; j < 3; ++j) window(seq, j, X[j]);
+                }
+            }
+            float out[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                dw[0][i] = fmaf(dz[3][i], X[0][i], dw[0][i]);
-                dw[1][i] = fmaf(dz[3][i], X[1][i], dw[1][i]);
-                dw[2][i] = fmaf(dz[3][i], X[2][i], dw[2][i]);
-                dw[3][i] = fmaf(dz[3][i], x0[i], dw[3][i]);
+                const float x0 = now.x[e].get(i);
+                float dz = now.y[e].get(i);
+                if (A.activation) {
+                    const float z = fmaf(wt[3][i], x0, fmaf(wt[2][i], X[2][i], fmaf(wt[1][i], X[1][i], wt[0][i] * X[0][i])));
+                    const float sg = sigmoid_hw(z);
+                    dz *= sg * fmaf(z, 1.0f - sg, 1.0f);
+                }
+                if (!(in >> (k + 3) & 1)) dz = 0.0f;
+                if (k < own) {
+                    dw[0][i] = fmaf(dz, X[0][i], dw[0][i]);
+                    dw[1][i] = fmaf(dz, X[1][i], dw[1][i]);
+                    dw[2][i] = fmaf(dz, X[2][i], dw[2][i]);
+                    dw[3][i] = fmaf(dz, x0, dw[3][i]);
+                }
+                out[i] = fmaf(wt[0][i], dz, acc[0][i]);
+                acc[0][i] = fmaf(wt[1][i], dz, acc[1][i]);
+                acc[1][i] = fmaf(wt[2][i], dz, acc[2][i]);
+                acc[2][i] = wt[3][i] * dz;
+                X[0][i] = X[1][i]; X[1][i] = X[2][i]; X[2][i] = x0;
+            }
+            if (near == 0) {
+                if (k >= 3 && nc > 0) store4<VEC>(pdx + (k - 3) * A.dx_stride, out, nc);
+            } else if (in >> (k + 3) & 1) {
+                const int t = (near & 4u) ? 0 : (near & 2u) ? 1 : 2;  // row of its sequence: completes window row t
+                if (k - t >= 0) put_window(A.map[r0 + k] >> 2, t, out);
             }
         }
-        if (k >= 3) {  // dX of row p = r0 + k - 3, whose dz is dz[0]
-            const int32_t m0 = m[k], m1 = m[k + 1], m2 = m[k + 2];
-            // how many rows of the sequence follow row p, at most 3
-            const int after = (m0 & 2) ? 0 : (m1 & 2) ? 1 : (m2 & 2) ? 2 : 3;
-            if (m0 >= 0) {
-                float dx[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    dx[i] = wt[3][i] * dz[0][i];
-                    if (after >= 1) dx[i] = fmaf(wt[2][i], dz[1][i], dx[i]);
-                    if (after >= 2) dx[i] = fmaf(wt[1][i], dz[2][i], dx[i]);
-                    if (after >= 3) dx[i] = fmaf(wt[0][i], dz[3][i], dx[i]);
-                }
-                if (after < 3 && A.d_window) {  // row p is row 2 - after of the rolled window
-                    const float* p = A.d_window + ((int64_t)(m0 >> 2) * 3 + 2 - after) * A.C + c0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i < nc) dx[i] += p[i];
-                }
-                if (nc > 0) store4<VEC>(pdx + (r0 + k - 3) * A.dx_stride, dx, nc);
-                if ((m0 & 1) && A.d_window0) {
-                    const int seq = m0 >> 2, T_ = after + 1;  // rows of the sequence, 4 for 4 and more
-                    const bool init = A.window && (A.has_init ? A.has_init[seq] != 0 : true);
-                    const float* src = A.d_window ? A.d_window + (int64_t)seq * 3 * A.C + c0 : nullptr;
-                    float* dst = A.d_window0 + (int64_t)seq * 3 * A.C + c0;
-#pragma unroll
-                    for (int row = 0; row < 3; ++row)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            float v = 0.0f;  // row `row` meets tap row - t of row t
-#pragma unroll
-                            for (int t = 0; t <= row; ++t)
-                                if (t < T_) v = fmaf(wt[row - t][i], dz[t][i], v);
-                            // still in the rolled window, T rows further up
-                            if (row >= T_ && src && i < nc) v += src[(row - T_) * (int64_t)A.C + i];
-                            if (i < nc) dst[row * (int64_t)A.C + i] = init ? v : 0.0f;
-                        }
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) { X[0][i] = X[1][i]; X[1][i] = X[2][i]; X[2][i] = x0[i]; }
+        now = next;
     }
-    // d_conv_w over the tile's rows: lanes, then waves
+done:
+    // d_conv_w over the workgroup's rows: lanes, then waves
 #pragma unroll
     for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -174,12 +204,19 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArg
         (s_w[0][j][ch] + s_w[1][j][ch]) + (s_w[2][j][ch] + s_w[3][j][ch]);
 }
 
+static int conv_rows(int64_t n_rows, int64_t C) {
+    const int64_t nc = padded_channels(C) / kTileCols;
+    return (n_rows + kConvGroups * 57 - 1) / (kConvGroups * 57) * nc >= 1024 ? 57 : 13;
+}
+
 template <typename T, typename YT, bool VEC> static hipError_t conv_t(const ConvBwdArgs& a, hipStream_t s) {
     const int nc = (int)(padded_channels(a.C) / kTileCols);
-    const int64_t nt = n_tiles(a.n_rows), grid = nt * nc;
+    // 57 rows a thread where that leaves work for every compute unit, else 13
+    const int own = conv_rows(a.n_rows, a.C);
+    const int64_t nt = (a.n_rows + kConvGroups * own - 1) / (kConvGroups * own), grid = nt * nc;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
     if (grid > 0)
-        hipLaunchKernelGGL((k_conv_backward<T, YT, VEC>), dim3((unsigned)grid), dim3(kConvThreads), 0, s, a, nc);
+        hipLaunchKernelGGL((k_conv_backward<T, YT, VEC>), dim3((unsigned)grid), dim3(kConvThreads), 0, s, a, nc, own);
     return launch_sum_tiles(a.part, nt, a.C, 4, a.d_conv_w, nullptr, s);
 }
 

@@ -67,6 +67,9 @@ struct ConvBwdArgs {
 inline int64_t n_tiles(int64_t n_rows) { return (n_rows + kTileRows - 1) / kTileRows; }
 inline int64_t padded_channels(int64_t C) { return (C + kTileCols - 1) / kTileCols * kTileCols; }
 
+// Partial sums of d_conv_w: a tile of k_conv_backward has at least 16 * 13 rows.
+inline int64_t conv_tiles_max(int64_t n_rows) { return (n_rows + 16 * 13 - 1) / (16 * 13); }
+
 hipError_t launch_map(const MapArgs& a, hipStream_t s);
 hipError_t launch_scan_rows(const ScanArgs& a, hipStream_t s);
 hipError_t launch_scan_forward(const ScanArgs& a, hipStream_t s);
