@@ -12,6 +12,8 @@
 // t there are three open sums.  The rows before a sequence's first are its
 // window: their sums are d_window0, and where a sequence ends the open sums
 // are the rows of its rolled window, where d_window joins.
+#include <type_traits>
+
 #include "gdnt_device.hpp"
 
 namespace gdnt {
@@ -57,9 +59,22 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArg
             dw[j][i] = 0.0f;
         }
 
-    const T* px = static_cast<const T*>(A.x) + r0 * A.x_stride + c0;
-    const YT* py = static_cast<const YT*>(A.dy) + r0 * A.dy_stride + c0;
-    T* pdx = static_cast<T*>(A.dx) + r0 * A.dx_stride + c0;
+    // Byte offsets from three rows above the workgroup's first: they fit 32 bits
+    // where VEC is set (the launcher's rule on strides), which leaves one add a row.
+    using Off = typename std::conditional<VEC, uint32_t, int64_t>::type;
+    const int64_t t0 = tile * kConvGroups * own - 3;
+    const int64_t cb = (int64_t)col * kTileCols;
+    const char* px = static_cast<const char*>(A.x) + (t0 * A.x_stride + cb) * (int64_t)sizeof(T);
+    const char* py = static_cast<const char*>(A.dy) + (t0 * A.dy_stride + cb) * (int64_t)sizeof(YT);
+    char* pdx = static_cast<char*>(A.dx) + (t0 * A.dx_stride + cb) * (int64_t)sizeof(T);
+    const Off sx = (Off)A.x_stride * (Off)sizeof(T), sy = (Off)A.dy_stride * (Off)sizeof(YT);
+    const Off sd = (Off)A.dx_stride * (Off)sizeof(T);
+    const Off row3 = (Off)(rg * own + 3);  // row r0 counted from t0
+    const Off cx = (Off)(cl * 4 * sizeof(T)), cy = (Off)(cl * 4 * sizeof(YT));
+    Off ox = row3 * sx + cx, oy = row3 * sy + cy, od = (row3 - 3) * sd + cx;  // rows to load, row to store
+    auto at_x = [&](Off o) { return reinterpret_cast<const T*>(px + o); };
+    auto at_y = [&](Off o) { return reinterpret_cast<const YT*>(py + o); };
+    auto at_dx = [&](Off o) { return reinterpret_cast<T*>(pdx + o); };
 
     auto has_init = [&](int seq) { return A.window && (A.has_init ? A.has_init[seq] != 0 : true); };
     auto window = [&](int seq, int row, float (&v)[4]) {
@@ -81,8 +96,8 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArg
         if (have == 15u && nc > 0) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                g.x[e] = load4<T, VEC>(px + (k + e) * A.x_stride, nc);
-                g.y[e] = load4<YT, VEC>(py + (k + e) * A.dy_stride, nc);
+                g.x[e] = load4<T, VEC>(at_x(ox + e * sx), nc);
+                g.y[e] = load4<YT, VEC>(at_y(oy + e * sy), nc);
             }
         } else {
 #pragma unroll
@@ -90,11 +105,13 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArg
                 g.x[e] = zero4<T>();
                 g.y[e] = zero4<YT>();
                 if ((have >> e & 1u) && nc > 0) {
-                    g.x[e] = load4<T, VEC>(px + (k + e) * A.x_stride, nc);
-                    g.y[e] = load4<YT, VEC>(py + (k + e) * A.dy_stride, nc);
+                    g.x[e] = load4<T, VEC>(at_x(ox + e * sx), nc);
+                    g.y[e] = load4<YT, VEC>(at_y(oy + e * sy), nc);
                 }
             }
         }
+        ox += 4 * sx;
+        oy += 4 * sy;
     };
 
     // X of the three rows before the current one and the open sums of the same rows
@@ -102,7 +119,7 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArg
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
         Raw4<T> v = zero4<T>();
-        if ((in >> j & 1) && nc > 0) v = load4<T, VEC>(px + (j - 3) * A.x_stride, nc);
+        if ((in >> j & 1) && nc > 0) v = load4<T, VEC>(at_x((row3 + j - 3) * sx + cx), nc);
 #pragma unroll
         for (int i = 0; i < 4; ++i) X[j][i] = v.get(i);
     }
@@ -113,17 +130,15 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArg
             if (j < 3 - have) window(seq, j + have, X[j]);
     }
 
-    ConvRows<T, YT> now, next;
-    load(now, 0);
-    for (int k0 = 0; k0 < own + 3; k0 += 4) {  // own + 3 is a multiple of 4
-        if (k0 + 4 < own + 3) load(next, k0 + 4);
+    bool open = true;  // rows of this thread, or behind them with their sums open, are left
+    auto rows4 = [&](const ConvRows<T, YT>& g, int k0) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int k = k0 + e;
             // the rows k, k - 1, k - 2 and whether a sequence begins there
             const uint32_t near = (uint32_t)(cut >> (k + 1)) & 7u;
             if (near & 4u) {
-                if (k > 0 && (in >> (k + 2) & 1)) {  // row k - 1 ended its sequence
+                if (k > 0 && open && (in >> (k + 2) & 1)) {  // row k - 1 ended its sequence
                     const int seq = A.map[r0 + k - 1] >> 2;
                     // bit d: a sequence begins at row k - 1 - d
                     const uint32_t begins = ((near >> 1 & 1u) | (near << 1 & 2u));
@@ -138,7 +153,7 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArg
                                 if (i < nc) acc[j][i] += src[i];
                         }
                         if (j >= 3 - rows) {
-                            if (p >= 0 && p < own && nc > 0) store4<VEC>(pdx + p * A.dx_stride, acc[j], nc);
+                            if (p >= 0 && p < own && nc > 0) store4<VEC>(at_dx((row3 + p) * sd + cx), acc[j], nc);
                         } else if (k - rows >= 0) {  // the sequence begins in this thread's rows
                             put_window(seq, rows + j, acc[j]);
                         }
@@ -148,24 +163,25 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArg
                 for (int j = 0; j < 3; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-                if (k >= own) goto done;  // the rest is the next thread's
-                if (in >> (k + 3) & 1) {
-                    const int seq = A.map[r0 + k] >> 2;
+                open = open && k < own;  // the rest is the next thread's
+                const bool begins = open && (in >> (k + 3) & 1);
+                const int seq = begins ? A.map[r0 + k] >> 2 : 0;
 #pragma unroll
-                    for (int j = 0; j < 3; ++j) window(seq, j, X[j]);
+                for (int j = 0; j < 3; ++j) {
+                    if (begins) window(seq, j, X[j]);
+                    else X[j][0] = X[j][1] = X[j][2] = X[j][3] = 0.0f;  // a row of no sequence adds nothing
                 }
             }
             float out[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float x0 = now.x[e].get(i);
-                float dz = now.y[e].get(i);
+                const float x0 = g.x[e].get(i);
+                float dz = g.y[e].get(i);
                 if (A.activation) {
                     const float z = fmaf(wt[3][i], x0, fmaf(wt[2][i], X[2][i], fmaf(wt[1][i], X[1][i], wt[0][i] * X[0][i])));
                     const float sg = sigmoid_hw(z);
                     dz *= sg * fmaf(z, 1.0f - sg, 1.0f);
                 }
-                if (!(in >> (k + 3) & 1)) dz = 0.0f;
                 if (k < own) {
                     dw[0][i] = fmaf(dz, X[0][i], dw[0][i]);
                     dw[1][i] = fmaf(dz, X[1][i], dw[1][i]);
@@ -179,15 +195,24 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArg
                 X[0][i] = X[1][i]; X[1][i] = X[2][i]; X[2][i] = x0;
             }
             if (near == 0) {
-                if (k >= 3 && nc > 0) store4<VEC>(pdx + (k - 3) * A.dx_stride, out, nc);
-            } else if (in >> (k + 3) & 1) {
+                if (k >= 3 && open && nc > 0) store4<VEC>(at_dx(od), out, nc);
+            } else if (open && (in >> (k + 3) & 1)) {
                 const int t = (near & 4u) ? 0 : (near & 2u) ? 1 : 2;  // row of its sequence: completes window row t
                 if (k - t >= 0) put_window(A.map[r0 + k] >> 2, t, out);
             }
+            od += sd;
         }
-        now = next;
+    };
+    // two buffers that change roles; own + 3 is a multiple of 4
+    ConvRows<T, YT> ga, gb;
+    load(ga, 0);
+    for (int k0 = 0; k0 < own + 3; k0 += 8) {
+        if (k0 + 4 < own + 3) load(gb, k0 + 4);
+        rows4(ga, k0);
+        if (k0 + 4 >= own + 3) break;
+        if (k0 + 8 < own + 3) load(ga, k0 + 8);
+        rows4(gb, k0 + 4);
     }
-done:
     // d_conv_w over the workgroup's rows: lanes, then waves
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -211,6 +236,8 @@ static int conv_rows(int64_t n_rows, int64_t C) {
 
 template <typename T, typename YT, bool VEC> static hipError_t conv_t(const ConvBwdArgs& a, hipStream_t s) {
     const int nc = (int)(padded_channels(a.C) / kTileCols);
+    // VEC addresses a workgroup's rows (16 * 57 + 6 at most) by 32-bit byte offsets
+    if (VEC && (a.x_stride | a.dy_stride | a.dx_stride) >> 20) return conv_t<T, YT, false>(a, s);
     // 57 rows a thread where that leaves work for every compute unit, else 13
     const int own = conv_rows(a.n_rows, a.C);
     const int64_t nt = (a.n_rows + kConvGroups * own - 1) / (kConvGroups * own), grid = nt * nc;
