@@ -65,7 +65,7 @@ struct ConvBwdArgs {
 };
 
 inline int64_t n_tiles(int64_t n_rows) { return (n_rows + kTileRows - 1) / kTileRows; }
-inline int64_t padded_channels(int64_t C) { return (C + kTileCols - 1) / kTileCols * kTileCols; }
+__host__ __device__ inline int64_t padded_channels(int64_t C) { return (C + kTileCols - 1) / kTileCols * kTileCols; }
 
 // Partial sums of d_conv_w: a tile of k_conv_backward has at least 16 * 13 rows.
 inline int64_t conv_tiles_max(int64_t n_rows) { return (n_rows + 16 * 13 - 1) / (16 * 13); }
@@ -79,6 +79,8 @@ hipError_t launch_conv_backward(const ConvBwdArgs& a, hipStream_t s);
 // out0 (j = 0), out1 (j = 1), or out0 [C][n_out] when out1 is NULL.
 hipError_t launch_sum_tiles(const float* part, int64_t n_tiles, int32_t C, int n_out, float* out0, float* out1,
                             hipStream_t s);
+// The row map of a scan call, and the words its kernels find at zero.
+MapArgs scan_map_args(const ScanArgs& a);
 // Chain words and partial sums of the scan's workspace (gdnt_api.cpp lays it out).
 size_t scan_chain_bytes(int64_t n_rows, int32_t C);
 

@@ -1,466 +1,273 @@
-// gdnt_scan.hip -- the vector-state gated linear recurrence and its backward
-// pass:  h_t = e^{g_t} h_{t-1} + beta_t x_t  per channel.
+// gdnt_scan.hip -- the vector-state gated linear recurrence
+//   h_t = e^{g_t} h_{t-1} + beta_t x_t  per channel, forward.
 //
-// A tile is 256 packed rows by 64 channels, one workgroup of 512 threads: 16
-// lanes side by side hold four channels each, 32 row groups hold eight
-// consecutive rows each.  A thread turns its rows into a Run (h -> a h + u),
-// the runs of a tile are joined by lane shuffles and through LDS, and with
-// the state before its rows each thread walks them again from registers.
-// Sequence boundaries may fall anywhere in a tile: a first row makes its run
-// independent of what is before it.
-#include "gdnt_device.hpp"
+// A tile is 128 packed rows by 128 channels, one workgroup of eight waves: a
+// wave holds 16 consecutive rows, a lane two channels of each, so everything
+// about a row (its sequence, its address) is uniform over the wave and costs
+// no vector instruction, and a row's piece is 256 consecutive bytes in bf16
+// (a copy in such pieces runs at 5.4 TB/s here, in 128-byte pieces at 4.7).
+// A wave turns its rows into a run (h -> a h + u) per channel, the runs of a
+// tile are joined through LDS, the state comes from the tile before
+// (gdnt_chain.hpp), and each wave walks its rows again from registers: x, a
+// and b are read once.  Sequence boundaries may fall anywhere.
+#include "gdnt_chain.hpp"
 
 namespace gdnt {
 
-constexpr int R = 8;                         // rows of a thread
-constexpr int kThreads = 512;
-constexpr int kWaves = kThreads / 64;
-static_assert(kThreads / 16 * R == kTileRows && 16 * 4 == kTileCols, "tile shape");
+constexpr int FR = 16;                       // rows of a wave
+constexpr int kWaves = 8;
+constexpr int kThreads = kWaves * 64;
+constexpr int kFwdRows = FR * kWaves;        // 128
+constexpr int kFwdCols = 128;
+static_assert(kTileRows % kFwdRows == 0 && FR == GDNT_CKPT_ROWS, "tile shape");
 
-// A run that contains a first row is marked by a negative `a`.
-__device__ __forceinline__ float walk(float a, float u, float h) { return a < 0.0f ? u : fmaf(a, h, u); }
-// first `p`, then `q`
-__device__ __forceinline__ void join(float pa, float pu, float& qa, float& qu) {
-    if (qa >= 0.0f) {
-        qu = fmaf(qa, pu, qu);
-        qa = copysignf(fmaxf(fabsf(pa) * qa, kTiny), pa);
+// Two channels of a row as they are stored.
+template <typename T> struct Raw2;
+template <> struct Raw2<bf16_t> {
+    uint32_t v;
+    __device__ __forceinline__ float get(int i) const { return __uint_as_float(i ? v & 0xffff0000u : v << 16); }
+    // the larger of |value|s as bits, kept per channel; NaN above Inf above all others
+    __device__ __forceinline__ uint32_t top(uint32_t t) const {
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, t),
+                                                                     __builtin_bit_cast(u16x2, v & 0x7fff7fffu)));
     }
-}
-
-template <typename T> struct Rows {
-    int32_t m[R];   // row map
-    int nc;         // channels of this thread that exist, 0..4
-    int64_t c0, r0;
+    static __device__ __forceinline__ uint32_t top_bits(uint32_t t) {
+        const uint32_t a = t << 16, b = t & 0xffff0000u;
+        return a > b ? a : b;
+    }
 };
+template <> struct Raw2<float> {
+    float2 v;
+    __device__ __forceinline__ float get(int i) const { return i ? v.y : v.x; }
+    __device__ __forceinline__ uint32_t top(uint32_t t) const {
+        const uint32_t a = __float_as_uint(v.x) & 0x7fffffffu, b = __float_as_uint(v.y) & 0x7fffffffu;
+        return max(t, max(a, b));
+    }
+    static __device__ __forceinline__ uint32_t top_bits(uint32_t t) { return t; }
+};
+template <typename T> __device__ __forceinline__ Raw2<T> zero2() {
+    Raw2<T> r;
+    __builtin_memset(&r, 0, sizeof(r));
+    return r;
+}
+template <typename T, bool VEC> __device__ __forceinline__ Raw2<T> load2(const T* p, int nc) {
+    Raw2<T> r;
+    if constexpr (VEC) {
+        r.v = *reinterpret_cast<const decltype(r.v)*>(p);
+    } else {
+        T e[2] = {T(0), T(0)};
+        if (nc > 0) e[0] = p[0];
+        if (nc > 1) e[1] = p[1];
+        __builtin_memcpy(&r, e, sizeof(r));
+    }
+    return r;
+}
+template <bool VEC> __device__ __forceinline__ void store2(bf16_t* p, float a, float b, int nc) {
+    const uint32_t v = gdn::f32x2_to_bf16x2(a, b);
+    if constexpr (VEC) {
+        *reinterpret_cast<uint32_t*>(p) = v;
+    } else {
+        if (nc > 0) p[0] = (bf16_t)v;
+        if (nc > 1) p[1] = (bf16_t)(v >> 16);
+    }
+}
+template <bool VEC> __device__ __forceinline__ void store2(float* p, float a, float b, int nc) {
+    if constexpr (VEC) {
+        *reinterpret_cast<float2*>(p) = make_float2(a, b);
+    } else {
+        if (nc > 0) p[0] = a;
+        if (nc > 1) p[1] = b;
+    }
+}
 
+// The wave's 16 rows of one tensor by this lane's two channels in 8 bits: a
+// block of the checkpoint is two neighbouring lanes' values, so one exchange
+// between them gives the scale, and another gives each lane eight whole rows
+// of the block (32 of its 64 bytes).
 template <typename T>
-__device__ __forceinline__ Rows<T> rows_of(const ScanArgs& A, int64_t tile, int col, int cl, int rg) {
-    Rows<T> w;
-    w.r0 = tile * kTileRows + rg * R;
-    w.c0 = (int64_t)col * kTileCols + cl * 4;
-    const int64_t left = (int64_t)A.C - w.c0;
-    w.nc = left >= 4 ? 4 : left > 0 ? (int)left : 0;
-    const int4* mp = reinterpret_cast<const int4*>(A.map + w.r0);
-    const int4 m0 = mp[0], m1 = mp[1];
-    w.m[0] = m0.x; w.m[1] = m0.y; w.m[2] = m0.z; w.m[3] = m0.w;
-    w.m[4] = m1.x; w.m[5] = m1.y; w.m[6] = m1.z; w.m[7] = m1.w;
-    return w;
-}
-
-// Tiles are handed out in time order by a ticket, so a tile only ever waits
-// for tiles that already run: the wait below ends.  The state between two
-// tiles travels in one 64-bit word per channel, value and ready mark
-// together, stored and polled with device-scope atomics; it needs no fence.
-__device__ __forceinline__ void publish(uint64_t* p, float v) {
-    __hip_atomic_store(p, (1ull << 32) | (uint64_t)__float_as_uint(v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ float await(uint64_t* p, int32_t* err) {
-    // bounded: some seconds, far beyond any tile's run
-    for (int k = 0; k < (1 << 21); ++k) {
-        const uint64_t v = __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (v >> 32) return __uint_as_float((uint32_t)v);
-        __builtin_amdgcn_s_sleep(1);
+__device__ __forceinline__ void put_ckpt(const Raw2<T> (&v)[FR], int8_t* q, float* scale, int lane, bool mine) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int r = 0; r < FR; ++r) top = v[r].top(top);
+    top = Raw2<T>::top_bits(top);
+    const uint32_t other = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)top, 0xB1, 0xF, 0xF, false);
+    top = top > other ? top : other;
+    const float m = __uint_as_float(top);
+    const bool finite = top < 0x7f800000u, live = m >= 7.888609052210118e-31f && finite;  // 2^-100
+    const float up = live ? 127.0f / m : 0.0f;
+    const float sc = !finite ? __uint_as_float(0x7fc00000u) : live ? m / 127.0f : 0.0f;
+    uint32_t w[FR / 2];
+#pragma unroll
+    for (int r = 0; r < FR / 2; ++r) {
+        // v * up + 1.5 * 2^23 rounds once to an integer, which then is the low byte
+        uint32_t e[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            e[k] = __float_as_uint(fmaf(v[r + (k >> 1) * (FR / 2)].get(k & 1), up, 12582912.0f));
+        // row r in the low half, row r + 8 in the high half
+        const uint32_t lo = __builtin_amdgcn_perm(e[1], e[0], 0x0c0c0400u);
+        const uint32_t hi = __builtin_amdgcn_perm(e[3], e[2], 0x04000c0cu);
+        const uint32_t p = lo | hi;
+        const uint32_t x = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)p, 0xB1, 0xF, 0xF, false);
+        // even lane: its low half below the other's; odd lane: the other's high half below its own
+        w[r] = (lane & 1) ? __builtin_amdgcn_perm(p, x, 0x07060302u) : __builtin_amdgcn_perm(x, p, 0x05040100u);
     }
-    raise(err, GDNT_DEVERR_TIMEOUT);
-    return 0.0f;
-}
-// The state a tile starts from (0 where nothing continues into it), handing
-// on the state it ends with: `mine` is written, `prev` read.
-__device__ __forceinline__ float hand_on(uint64_t* mine, uint64_t* prev, bool cont, bool next, float a, float u,
-                                         int32_t* err) {
-    const bool early = a < 0.0f || !cont;
-    if (next && early) publish(mine, u);
-    const float h = cont ? await(prev, err) : 0.0f;
-    if (next && !early) publish(mine, fmaf(a, h, u));
-    return h;
-}
-
-template <typename T, bool VEC>
-__global__ __launch_bounds__(kThreads) void k_scan_forward(const ScanArgs A, int n_cols, int64_t n_tiles) {
-    __shared__ float4 s_a[kWaves][16], s_u[kWaves][16], s_h[16];
-    __shared__ uint32_t s_ticket;
-    if (threadIdx.x == 0) s_ticket = atomicAdd(A.ticket, 1u);
-    __syncthreads();
-    const int64_t tile = s_ticket / (uint32_t)n_cols;
-    const int col = (int)(s_ticket % (uint32_t)n_cols);
-    const int cl = threadIdx.x & 15, rg = threadIdx.x >> 4, wave = threadIdx.x >> 6;
-    const int64_t Cp = (int64_t)n_cols * kTileCols;
-    const Rows<T> w = rows_of<T>(A, tile, col, cl, rg);
-
-    Raw4<T> rx[R], ra[R], rb[R];
-    const T* px = static_cast<const T*>(A.x) + w.r0 * A.x_stride + w.c0;
-    const T* pa = static_cast<const T*>(A.a) + w.r0 * A.ab_stride + w.c0;
-    const T* pb = static_cast<const T*>(A.b) + w.r0 * A.ab_stride + w.c0;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        rx[r] = zero4<T>(); ra[r] = zero4<T>(); rb[r] = zero4<T>();
-        if (w.m[r] >= 0 && w.nc > 0) {
-            rx[r] = load4<T, VEC>(px + r * A.x_stride, w.nc);
-            ra[r] = load4<T, VEC>(pa + r * A.ab_stride, w.nc);
-            rb[r] = load4<T, VEC>(pb + r * A.ab_stride, w.nc);
-        }
-    }
-    const ChanP P = load_params(A.a_log, A.dt_bias, w.c0, w.nc);
-
-    float al[R][4], u[R][4];
-    float ea[4] = {1.0f, 1.0f, 1.0f, 1.0f}, eu[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const bool in = w.m[r] >= 0, first = in && (w.m[r] & 1);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float t;
-            const float sp = softplus_t(ra[r].get(i) + P.dt[i], t);
-            al[r][i] = in ? exp2_hw(P.k[i] * sp) : 1.0f;
-            u[r][i] = in ? sigmoid_hw(rb[r].get(i)) * rx[r].get(i) : 0.0f;
-        }
-        if (first) {  // the state page joins the row, nothing before it does
-            const int seq = w.m[r] >> 2;
-            const bool init = A.has_init ? A.has_init[seq] != 0 : true;
-            const int64_t at = (int64_t)A.page_idx[seq] * A.st_in_stride + w.c0;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (init && i < w.nc) u[r][i] = fmaf(al[r][i], load_state(A.st_in, at + i, A.state_dtype), u[r][i]);
-                al[r][i] = -1.0f;
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            eu[i] = walk(al[r][i], u[r][i], eu[i]);
-            ea[i] = first ? -1.0f : ea[i] * al[r][i];
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) ea[i] = copysignf(fmaxf(fabsf(ea[i]), kTiny), ea[i]);
-
-    // inclusive runs over the wave's four row groups, then the run before each
-#pragma unroll
-    for (int d = 16; d <= 32; d <<= 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float qa = __shfl_up(ea[i], d), qu = __shfl_up(eu[i], d);
-            if ((int)(threadIdx.x & 63) >= d) join(qa, qu, ea[i], eu[i]);
-        }
-    }
-    if ((threadIdx.x & 63) >= 48) {
-        s_a[wave][cl] = make_float4(ea[0], ea[1], ea[2], ea[3]);
-        s_u[wave][cl] = make_float4(eu[0], eu[1], eu[2], eu[3]);
-    }
-    float xa[4], xu[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        xa[i] = __shfl_up(ea[i], 16);
-        xu[i] = __shfl_up(eu[i], 16);
-        if ((threadIdx.x & 63) < 16) { xa[i] = 1.0f; xu[i] = 0.0f; }
-    }
-    __syncthreads();
-
-    const int32_t m_first = A.map[tile * kTileRows];
-    const bool cont = m_first >= 0 && !(m_first & 1);
-    if (threadIdx.x < 64) {  // one channel a lane
-        const int32_t m_next = tile + 1 < n_tiles ? A.map[(tile + 1) * kTileRows] : -1;
-        const float* fa = reinterpret_cast<const float*>(s_a) + threadIdx.x;
-        const float* fu = reinterpret_cast<const float*>(s_u) + threadIdx.x;
-        float ta = fa[0], tu = fu[0];
-#pragma unroll
-        for (int v = 1; v < kWaves; ++v) {
-            float qa = fa[v * kTileCols], qu = fu[v * kTileCols];
-            join(ta, tu, qa, qu);
-            ta = qa; tu = qu;
-        }
-        const int64_t c = (int64_t)col * kTileCols + threadIdx.x;
-        uint64_t* mine = A.chain + tile * Cp + c;
-        const float h = hand_on(mine, mine - Cp, cont, m_next >= 0 && !(m_next & 1), ta, tu, A.err);
-        reinterpret_cast<float*>(s_h)[threadIdx.x] = h;
-        if (A.states && cont && c < A.C) A.states[tile * A.C + c] = h;
-    }
-    __syncthreads();
-    {
-        float h[4] = {s_h[cl].x, s_h[cl].y, s_h[cl].z, s_h[cl].w};
-        for (int v = 0; v < wave; ++v) {
-            const float4 va = s_a[v][cl], vu = s_u[v][cl];
-            h[0] = walk(va.x, vu.x, h[0]); h[1] = walk(va.y, vu.y, h[1]);
-            h[2] = walk(va.z, vu.z, h[2]); h[3] = walk(va.w, vu.w, h[3]);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = walk(xa[i], xu[i], h[i]);
-        T* ph = static_cast<T*>(A.h) + w.r0 * A.h_stride + w.c0;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = walk(al[r][i], u[r][i], h[i]);
-            if (w.m[r] >= 0 && w.nc > 0) {
-                store4<VEC>(ph + r * A.h_stride, h, w.nc);
-                if (w.m[r] & 2) {
-                    const int64_t at = (int64_t)A.page_idx[w.m[r] >> 2] * A.st_out_stride + w.c0;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (i < w.nc) store_state(A.st_out, at + i, A.state_dtype, h[i]);
-                }
-            }
-        }
+    if (mine) {
+        uint4* out = reinterpret_cast<uint4*>(q + (lane >> 1) * 64 + (lane & 1) * 32);
+        out[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        out[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        if (!(lane & 1)) scale[lane >> 1] = sc;
     }
 }
 
-// The backward pass.  With mu_t = alpha_t lambda_t the reverse recurrence is
-// lambda_t = dh_t + mu_{t+1}, mu_t = alpha_t lambda_t: the same kind of run,
-// from the last row to the first, and new at a last row.
-// h_{t-1} comes from the kept state before the tile and the same runs as in
-// the forward pass; only the reverse recurrence goes from tile to tile.
 template <typename T, bool VEC, bool CKPT>
-__global__ __launch_bounds__(kThreads) void k_scan_backward(const ScanArgs A, int n_cols, int64_t n_tiles) {
-    __shared__ float4 s_a[kWaves][16], s_u[kWaves][16], s_ra[kWaves][16], s_ru[kWaves][16], s_h[16];
+__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void k_scan_forward(const ScanArgs A, int n_cols,
+                                                                                    int64_t n_tiles) {
+    __shared__ float2 s_a[kWaves][64], s_u[kWaves][64], s_h[64];
     __shared__ uint32_t s_ticket;
     if (threadIdx.x == 0) s_ticket = atomicAdd(A.ticket, 1u);
     __syncthreads();
-    const int64_t tile = n_tiles - 1 - s_ticket / (uint32_t)n_cols;
-    const int col = (int)(s_ticket % (uint32_t)n_cols);
-    const int lane = threadIdx.x & 63, cl = threadIdx.x & 15, rg = threadIdx.x >> 4, wave = threadIdx.x >> 6;
-    const int64_t Cp = (int64_t)n_cols * kTileCols;
-    const Rows<T> w = rows_of<T>(A, tile, col, cl, rg);
-
-    float x[R][4], a[R][4], b[R][4];
-    Raw4<T> rd[R];
-    const T* pd = static_cast<const T*>(A.dh) + w.r0 * A.dh_stride + w.c0;
+    const uint32_t ticket = __builtin_amdgcn_readfirstlane(s_ticket);
+    const int64_t tile = ticket / (uint32_t)n_cols;
+    const int col = (int)(ticket % (uint32_t)n_cols);
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t r0 = tile * kFwdRows + wave * FR, c0 = (int64_t)col * kFwdCols + lane * 2;
+    const int64_t left = (int64_t)A.C - c0;
+    const int nc = left >= 2 ? 2 : left > 0 ? (int)left : 0;
+    const int32_t* map = A.map + r0;
+    int32_t m[FR];
+    uint32_t in = 0, special = 0;  // rows of a sequence; of these the first and last ones
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        rd[r] = zero4<T>();
-        if (w.m[r] >= 0 && w.nc > 0) rd[r] = load4<T, VEC>(pd + r * A.dh_stride, w.nc);
+    for (int r = 0; r < FR; ++r) {
+        m[r] = map[r];
+        in |= m[r] >= 0 ? 1u << r : 0u;
+        special |= m[r] >= 0 && (m[r] & 3) ? 1u << r : 0u;
     }
-    if constexpr (CKPT) {
-        const int64_t n4 = Cp / 4, blk = w.r0 / GDNT_CKPT_ROWS, c4 = w.c0 / 4;
+
+    Raw2<T> rx[FR], ra[FR], rb[FR];
+    const T* px = static_cast<const T*>(A.x) + r0 * A.x_stride + c0;
+    const T* pa = static_cast<const T*>(A.a) + r0 * A.ab_stride + c0;
+    const T* pb = static_cast<const T*>(A.b) + r0 * A.ab_stride + c0;
+    if (in == 0xffffu && nc > 0) {
 #pragma unroll
-        for (int t = 0; t < 3; ++t) {
-            const int64_t at = (blk * 3 + t) * n4 + c4;
-            uint32_t q[R];
-            if (w.r0 < A.n_rows) {
-                const uint4* p = reinterpret_cast<const uint4*>(A.q + at * 64 + (rg & 1) * 32);
-                const uint4 q0 = p[0], q1 = p[1];
-                q[0] = q0.x; q[1] = q0.y; q[2] = q0.z; q[3] = q0.w;
-                q[4] = q1.x; q[5] = q1.y; q[6] = q1.z; q[7] = q1.w;
-            } else {
-#pragma unroll
-                for (int r = 0; r < R; ++r) q[r] = 0;
-            }
-            const float sc = w.r0 < A.n_rows ? A.q_scale[at] : 0.0f;
-#pragma unroll
-            for (int r = 0; r < R; ++r)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    (t == 0 ? x : t == 1 ? a : b)[r][i] = (float)(int8_t)(q[r] >> (8 * i)) * sc;
+        for (int r = 0; r < FR; ++r) {
+            ra[r] = load2<T, VEC>(pa + r * A.ab_stride, nc);
+            rx[r] = load2<T, VEC>(px + r * A.x_stride, nc);
+            rb[r] = load2<T, VEC>(pb + r * A.ab_stride, nc);
         }
     } else {
-        const T* px = static_cast<const T*>(A.x) + w.r0 * A.x_stride + w.c0;
-        const T* pa = static_cast<const T*>(A.a) + w.r0 * A.ab_stride + w.c0;
-        const T* pb = static_cast<const T*>(A.b) + w.r0 * A.ab_stride + w.c0;
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            Raw4<T> rx = zero4<T>(), ra = zero4<T>(), rb = zero4<T>();
-            if (w.m[r] >= 0 && w.nc > 0) {
-                rx = load4<T, VEC>(px + r * A.x_stride, w.nc);
-                ra = load4<T, VEC>(pa + r * A.ab_stride, w.nc);
-                rb = load4<T, VEC>(pb + r * A.ab_stride, w.nc);
+        for (int r = 0; r < FR; ++r) {
+            rx[r] = zero2<T>(); ra[r] = zero2<T>(); rb[r] = zero2<T>();
+            if ((in >> r & 1u) && nc > 0) {
+                ra[r] = load2<T, VEC>(pa + r * A.ab_stride, nc);
+                rx[r] = load2<T, VEC>(px + r * A.x_stride, nc);
+                rb[r] = load2<T, VEC>(pb + r * A.ab_stride, nc);
             }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) { x[r][i] = rx.get(i); a[r][i] = ra.get(i); b[r][i] = rb.get(i); }
         }
     }
-    const ChanP P = load_params(A.a_log, A.dt_bias, w.c0, w.nc);
-
-    // forward run (ea, eu) and reverse run (fa, fu) of the rows; h0[r] is kept in u
-    float al[R][4], u[R][4];
-    float ea[4] = {1.0f, 1.0f, 1.0f, 1.0f}, eu[4] = {}, fa[4] = {1.0f, 1.0f, 1.0f, 1.0f}, fu[4] = {};
-    float h0[R][4];
+    float dt[2], kk[2];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const bool in = w.m[r] >= 0, first = in && (w.m[r] & 1);
-        int64_t at = 0;
-        bool init = false;
-        if (first) {
-            const int seq = w.m[r] >> 2;
-            init = A.has_init ? A.has_init[seq] != 0 : true;
-            at = (int64_t)A.page_idx[seq] * A.st_in_stride + w.c0;
+    for (int i = 0; i < 2; ++i) {
+        dt[i] = i < nc ? A.dt_bias[c0 + i] : 0.0f;
+        kk[i] = i < nc ? -expf(A.a_log[c0 + i]) * kLog2e : 0.0f;
+    }
+    if constexpr (CKPT) {
+        const int64_t n4 = padded_channels(A.C) / 4, c4 = (int64_t)col * (kFwdCols / 4);
+        if (r0 < A.n_rows) {
+            const bool mine = c4 + (lane >> 1) < n4;
+            const int64_t at = (r0 / FR) * 3 * n4 + c4;
+            put_ckpt<T>(rx, A.q + at * 64, A.q_scale + at, lane, mine);
+            put_ckpt<T>(ra, A.q + (at + n4) * 64, A.q_scale + at + n4, lane, mine);
+            put_ckpt<T>(rb, A.q + (at + 2 * n4) * 64, A.q_scale + at + 2 * n4, lane, mine);
         }
+    }
+
+    float al[FR][2], u[FR][2];
+    float ea[2] = {1.0f, 1.0f}, eu[2] = {0.0f, 0.0f};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+    for (int r = 0; r < FR; ++r) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
             float t;
-            const float sp = softplus_t(a[r][i] + P.dt[i], t);
-            al[r][i] = in ? exp2_hw(P.k[i] * sp) : 1.0f;
-            u[r][i] = in ? sigmoid_hw(b[r][i]) * x[r][i] : 0.0f;
-            h0[r][i] = 0.0f;
-            if (first) {
-                if (init && i < w.nc) h0[r][i] = load_state(A.st_in, at + i, A.state_dtype);
-                eu[i] = fmaf(al[r][i], h0[r][i], u[r][i]);
+            al[r][i] = exp2_hw(kk[i] * softplus_t(ra[r].get(i) + dt[i], t));
+            u[r][i] = sigmoid_hw(rb[r].get(i)) * rx[r].get(i);
+        }
+        if (!(in >> r & 1u)) {  // a row of no sequence changes nothing
+#pragma unroll
+            for (int i = 0; i < 2; ++i) { al[r][i] = 1.0f; u[r][i] = 0.0f; }
+        }
+        if ((special >> r & 1u) && (m[r] & 1)) {  // the state page joins a first row, nothing before it does
+            const int seq = m[r] >> 2;
+            const bool init = A.has_init ? A.has_init[seq] != 0 : true;
+            const int64_t at = (int64_t)A.page_idx[seq] * A.st_in_stride + c0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (init && i < nc) u[r][i] = fmaf(al[r][i], load_state(A.st_in, at + i, A.state_dtype), u[r][i]);
+                al[r][i] = -1.0f;
+                eu[i] = u[r][i];
                 ea[i] = -1.0f;
-            } else {
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
                 eu[i] = fmaf(al[r][i], eu[i], u[r][i]);
                 ea[i] *= al[r][i];
             }
         }
     }
 #pragma unroll
-    for (int r = R - 1; r >= 0; --r) {
-        const bool in = w.m[r] >= 0, last = in && (w.m[r] & 2);
+    for (int i = 0; i < 2; ++i) ea[i] = copysignf(fmaxf(fabsf(ea[i]), kTiny), ea[i]);
+    s_a[wave][lane] = make_float2(ea[0], ea[1]);
+    s_u[wave][lane] = make_float2(eu[0], eu[1]);
+    __syncthreads();
+    if (wave == 0) {
+        float ta[2] = {ea[0], ea[1]}, tu[2] = {eu[0], eu[1]};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float lam = rd[r].get(i);
-            if (last) {
-                if (A.d_state && i < w.nc) lam += A.d_state[(int64_t)(w.m[r] >> 2) * A.C + w.c0 + i];
-                fa[i] = -1.0f;
-            } else {
-                lam += fu[i];
-            }
-            fu[i] = in ? al[r][i] * lam : fu[i];
-            fa[i] = fa[i] * al[r][i];
+        for (int v = 1; v < kWaves; ++v) {
+            float2 qa = s_a[v][lane], qu = s_u[v][lane];
+            join(ta[0], tu[0], qa.x, qu.x);
+            join(ta[1], tu[1], qa.y, qu.y);
+            ta[0] = qa.x; ta[1] = qa.y; tu[0] = qu.x; tu[1] = qu.y;
         }
-    }
+        const int32_t m_next = tile + 1 < n_tiles ? A.map[(tile + 1) * kFwdRows] : -1;
+        const bool cont = m[0] >= 0 && !(m[0] & 1);
+        const int64_t Cw = (int64_t)n_cols * kFwdCols;
+        const Chain chain{A.chain, A.chain + n_tiles * Cw};
+        float h[2];
+        hand_on<2>(chain, tile * Cw + (int64_t)col * kFwdCols, -Cw, tile, cont, m_next >= 0 && !(m_next & 1), ta, tu,
+                   h, A.err);
+        s_h[lane] = make_float2(h[0], h[1]);
+        if (A.states && cont && r0 % kTileRows == 0) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        ea[i] = copysignf(fmaxf(fabsf(ea[i]), kTiny), ea[i]);
-        fa[i] = copysignf(fmaxf(fabsf(fa[i]), kTiny), fa[i]);
-    }
-#pragma unroll
-    for (int d = 16; d <= 32; d <<= 1) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float qa = __shfl_up(ea[i], d), qu = __shfl_up(eu[i], d);
-            const float sa = __shfl_down(fa[i], d), su = __shfl_down(fu[i], d);
-            if (lane >= d) join(qa, qu, ea[i], eu[i]);
-            if (lane + d < 64) join(sa, su, fa[i], fu[i]);
+            for (int i = 0; i < 2; ++i)
+                if (i < nc) A.states[r0 / kTileRows * A.C + c0 + i] = h[i];
         }
-    }
-    if (lane >= 48) {
-        s_a[wave][cl] = make_float4(ea[0], ea[1], ea[2], ea[3]);
-        s_u[wave][cl] = make_float4(eu[0], eu[1], eu[2], eu[3]);
-    }
-    if (lane < 16) {
-        s_ra[wave][cl] = make_float4(fa[0], fa[1], fa[2], fa[3]);
-        s_ru[wave][cl] = make_float4(fu[0], fu[1], fu[2], fu[3]);
-    }
-    float xa[4], xu[4], ya[4], yu[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        xa[i] = __shfl_up(ea[i], 16);
-        xu[i] = __shfl_up(eu[i], 16);
-        ya[i] = __shfl_down(fa[i], 16);
-        yu[i] = __shfl_down(fu[i], 16);
-        if (lane < 16) { xa[i] = 1.0f; xu[i] = 0.0f; }
-        if (lane >= 48) { ya[i] = 1.0f; yu[i] = 0.0f; }
     }
     __syncthreads();
-    const int32_t m_first = A.map[tile * kTileRows];
-    if (threadIdx.x < 64) {
-        const int32_t m_last = A.map[tile * kTileRows + kTileRows - 1];
-        const int32_t m_prev = tile > 0 ? A.map[tile * kTileRows - 1] : -1;
-        const float* pa = reinterpret_cast<const float*>(s_ra) + threadIdx.x;
-        const float* pu = reinterpret_cast<const float*>(s_ru) + threadIdx.x;
-        float ta = pa[(kWaves - 1) * kTileCols], tu = pu[(kWaves - 1) * kTileCols];
-#pragma unroll
-        for (int v = kWaves - 2; v >= 0; --v) {
-            float qa = pa[v * kTileCols], qu = pu[v * kTileCols];
-            join(ta, tu, qa, qu);
-            ta = qa; tu = qu;
-        }
-        uint64_t* mine = A.chain + tile * Cp + (int64_t)col * kTileCols + threadIdx.x;
-        reinterpret_cast<float*>(s_h)[threadIdx.x] = hand_on(mine, mine + Cp, m_last >= 0 && !(m_last & 2),
-                                                             m_prev >= 0 && !(m_prev & 2), ta, tu, A.err);
-    }
-    __syncthreads();
-    float h[4] = {}, mu[4] = {s_h[cl].x, s_h[cl].y, s_h[cl].z, s_h[cl].w};
-    if (m_first >= 0 && !(m_first & 1)) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i < w.nc) h[i] = A.states[tile * A.C + w.c0 + i];
-    }
+    float h[2] = {s_h[lane].x, s_h[lane].y};
     for (int v = 0; v < wave; ++v) {
-        const float4 va = s_a[v][cl], vu = s_u[v][cl];
-        h[0] = walk(va.x, vu.x, h[0]); h[1] = walk(va.y, vu.y, h[1]);
-        h[2] = walk(va.z, vu.z, h[2]); h[3] = walk(va.w, vu.w, h[3]);
+        const float2 va = s_a[v][lane], vu = s_u[v][lane];
+        h[0] = walk(va.x, vu.x, h[0]);
+        h[1] = walk(va.y, vu.y, h[1]);
     }
-    for (int v = kWaves - 1; v > wave; --v) {
-        const float4 va = s_ra[v][cl], vu = s_ru[v][cl];
-        mu[0] = walk(va.x, vu.x, mu[0]); mu[1] = walk(va.y, vu.y, mu[1]);
-        mu[2] = walk(va.z, vu.z, mu[2]); mu[3] = walk(va.w, vu.w, mu[3]);
-    }
+    T* ph = static_cast<T*>(A.h) + r0 * A.h_stride + c0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        h[i] = walk(xa[i], xu[i], h[i]);
-        mu[i] = walk(ya[i], yu[i], mu[i]);
-    }
-    // h before each row, in h0
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const bool first = w.m[r] >= 0 && (w.m[r] & 1);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            h0[r][i] = first ? h0[r][i] : h[i];
-            h[i] = fmaf(al[r][i], h0[r][i], u[r][i]);
+    for (int r = 0; r < FR; ++r) {
+        if ((special >> r & 1u) && (m[r] & 1)) {
+            h[0] = u[r][0]; h[1] = u[r][1];
+        } else {
+            h[0] = fmaf(al[r][0], h[0], u[r][0]);
+            h[1] = fmaf(al[r][1], h[1], u[r][1]);
         }
-    }
-    float s1[4] = {}, s2[4] = {};  // sums of dg softplus(z) and of dg sigmoid(z)
-    T* pdx = static_cast<T*>(A.dx) + w.r0 * A.dx_stride + w.c0;
-    T* pda = static_cast<T*>(A.da) + w.r0 * A.dab_stride + w.c0;
-    T* pdb = static_cast<T*>(A.db) + w.r0 * A.dab_stride + w.c0;
+        if ((in >> r & 1u) && nc > 0) store2<VEC>(ph + r * A.h_stride, h[0], h[1], nc);
+        if ((special >> r & 1u) && (m[r] & 2)) {
+            const int64_t at = (int64_t)A.page_idx[m[r] >> 2] * A.st_out_stride + c0;
 #pragma unroll
-    for (int r = R - 1; r >= 0; --r) {
-        const bool in = w.m[r] >= 0, last = in && (w.m[r] & 2);
-        float dx[4], da[4], db[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float lam = rd[r].get(i);
-            if (last) {
-                if (A.d_state && i < w.nc) lam += A.d_state[(int64_t)(w.m[r] >> 2) * A.C + w.c0 + i];
-            } else {
-                lam += mu[i];
-            }
-            float t;
-            const float z = a[r][i] + P.dt[i];
-            const float sp = softplus_t(z, t);
-            const float sg = (z >= 0.0f ? 1.0f : t) * rcp(1.0f + t);
-            const float be = sigmoid_hw(b[r][i]);
-            mu[i] = in ? al[r][i] * lam : mu[i];
-            const float dg = in ? mu[i] * h0[r][i] : 0.0f;
-            dx[i] = be * lam;
-            db[i] = dx[i] * x[r][i] * (1.0f - be);
-            const float ds = dg * sg;
-            da[i] = ds * (P.k[i] / kLog2e);
-            s1[i] = fmaf(dg, sp, s1[i]);
-            s2[i] += ds;
+            for (int i = 0; i < 2; ++i)
+                if (i < nc) store_state(A.st_out, at + i, A.state_dtype, h[i]);
         }
-        if (in && w.nc > 0) {
-            store4<VEC>(pdx + r * A.dx_stride, dx, w.nc);
-            store4<VEC>(pda + r * A.dab_stride, da, w.nc);
-            store4<VEC>(pdb + r * A.dab_stride, db, w.nc);
-            if ((w.m[r] & 1) && A.d_state0) {
-                const int seq = w.m[r] >> 2;
-                const bool init = A.has_init ? A.has_init[seq] != 0 : true;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (i < w.nc) A.d_state0[(int64_t)seq * A.C + w.c0 + i] = init ? mu[i] : 0.0f;
-            }
-        }
-    }
-    // sums over the tile's rows: lanes, then waves
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float k = P.k[i] / kLog2e;
-        s1[i] *= k; s2[i] *= k;
-        s1[i] += __shfl_xor(s1[i], 16); s2[i] += __shfl_xor(s2[i], 16);
-        s1[i] += __shfl_xor(s1[i], 32); s2[i] += __shfl_xor(s2[i], 32);
-    }
-    __syncthreads();
-    if (lane < 16) {
-        s_a[wave][cl] = make_float4(s1[0], s1[1], s1[2], s1[3]);
-        s_u[wave][cl] = make_float4(s2[0], s2[1], s2[2], s2[3]);
-    }
-    __syncthreads();
-    if (threadIdx.x < 128) {
-        const int ch = threadIdx.x & 63, which = threadIdx.x >> 6;
-        const float* p = reinterpret_cast<const float*>(which ? s_u : s_a) + ch;
-        float v = 0.0f;
-#pragma unroll
-        for (int k = 0; k < kWaves; ++k) v += p[k * kTileCols];
-        A.part[(tile * 2 + which) * Cp + (int64_t)col * kTileCols + ch] = v;
     }
 }
 
@@ -515,60 +322,15 @@ __global__ __launch_bounds__(256) void k_scan_rows(const ScanArgs A, int n_x) {
     else store4<VEC>(static_cast<float*>(A.st_out) + at_out, h, nc);
 }
 
-// ------------------------------------------------------------- 8-bit checkpoint
-
-// One thread per block of 16 rows by 4 channels of one tensor.
-template <typename T, bool VEC>
-__global__ __launch_bounds__(256) void k_ckpt(const ScanArgs A, int64_t n4, int64_t n_items) {
-    const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (item >= n_items) return;
-    const int64_t c4 = item % n4, bt = item / n4, blk = bt / 3;
-    const int t = (int)(bt % 3);
-    const int64_t c0 = c4 * 4, left = (int64_t)A.C - c0;
-    const int nc = left >= 4 ? 4 : left > 0 ? (int)left : 0;
-    const int64_t stride = t == 0 ? A.x_stride : A.ab_stride;
-    const T* p = static_cast<const T*>(t == 0 ? A.x : t == 1 ? A.a : A.b) + blk * GDNT_CKPT_ROWS * stride + c0;
-    float v[GDNT_CKPT_ROWS][4];
-    uint32_t top = 0;  // |v| as bits: ordered like the values, NaN above Inf
-#pragma unroll
-    for (int r = 0; r < GDNT_CKPT_ROWS; ++r) {
-        Raw4<T> raw = zero4<T>();
-        if (nc > 0 && A.map[blk * GDNT_CKPT_ROWS + r] >= 0) raw = load4<T, VEC>(p + r * stride, nc);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[r][i] = raw.get(i);
-            const uint32_t bits = __float_as_uint(v[r][i]) & 0x7fffffffu;
-            top = bits > top ? bits : top;
-        }
-    }
-    const float m = __uint_as_float(top);
-    const bool live = m >= 7.888609052210118e-31f && top < 0x7f800000u;  // 2^-100
-    const float up = live ? 127.0f / m : 0.0f;
-    const float sc = top >= 0x7f800000u ? __uint_as_float(0x7fc00000u) : live ? m / 127.0f : 0.0f;
-    uint32_t q[GDNT_CKPT_ROWS];
-#pragma unroll
-    for (int r = 0; r < GDNT_CKPT_ROWS; ++r) {
-        uint32_t e[4];
-#pragma unroll
-        // v * up + 1.5 * 2^23 rounds once to an integer, which then is the low byte
-        for (int i = 0; i < 4; ++i) e[i] = __float_as_uint(fmaf(v[r][i], up, 12582912.0f)) & 0xffu;
-        q[r] = e[0] | (e[1] << 8) | (e[2] << 16) | (e[3] << 24);
-    }
-    uint4* out = reinterpret_cast<uint4*>(A.q + item * 64);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) out[k] = make_uint4(q[4 * k], q[4 * k + 1], q[4 * k + 2], q[4 * k + 3]);
-    A.q_scale[item] = sc;
-}
-
 // ------------------------------------------------------------------- launches
 
 size_t scan_chain_bytes(int64_t n_rows, int32_t C) {
-    return (size_t)n_tiles(n_rows) * (size_t)padded_channels(C) * sizeof(uint64_t);
+    // the forward tiles are the smaller ones: two words a channel and tile
+    const int64_t cols = (C + kFwdCols - 1) / kFwdCols;
+    return (size_t)((n_rows + kFwdRows - 1) / kFwdRows) * (size_t)(cols * kFwdCols) * 2 * sizeof(uint64_t);
 }
 
-static int cols_of(const ScanArgs& a) { return (int)(padded_channels(a.C) / kTileCols); }
-
-static MapArgs map_args(const ScanArgs& a) {
+MapArgs scan_map_args(const ScanArgs& a) {
     MapArgs m{};
     m.cu = a.cu; m.page_idx = a.page_idx; m.n_seqs = a.n_seqs;
     m.n_rows = a.n_rows; m.n_map = n_tiles(a.n_rows) * kTileRows;
@@ -592,45 +354,22 @@ hipError_t launch_scan_rows(const ScanArgs& a, hipStream_t s) {
 }
 
 template <typename T, bool VEC> static hipError_t forward_t(const ScanArgs& a, hipStream_t s) {
-    const int nc = cols_of(a);
-    const int64_t nt = n_tiles(a.n_rows), grid = nt * nc;
+    const int nc = (int)((a.C + kFwdCols - 1) / kFwdCols);
+    const int64_t nt = (a.n_rows + kFwdRows - 1) / kFwdRows, grid = nt * nc;
     if (grid == 0) return hipSuccess;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_scan_forward<T, VEC>), dim3((unsigned)grid), dim3(kThreads), 0, s, a, nc, nt);
-    if (a.q) {
-        const int64_t n4 = padded_channels(a.C) / 4, n = (a.n_rows + GDNT_CKPT_ROWS - 1) / GDNT_CKPT_ROWS * 3 * n4;
-        hipLaunchKernelGGL((k_ckpt<T, VEC>), dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a, n4, n);
-    }
+    if (a.q)
+        hipLaunchKernelGGL((k_scan_forward<T, VEC, true>), dim3((unsigned)grid), dim3(kThreads), 0, s, a, nc, nt);
+    else
+        hipLaunchKernelGGL((k_scan_forward<T, VEC, false>), dim3((unsigned)grid), dim3(kThreads), 0, s, a, nc, nt);
     return hipGetLastError();
 }
 
 hipError_t launch_scan_forward(const ScanArgs& a, hipStream_t s) {
-    const hipError_t e = launch_map(map_args(a), s);
+    const hipError_t e = launch_map(scan_map_args(a), s);
     if (e != hipSuccess) return e;
     if (a.act_dtype == GDN_BF16) return a.vec ? forward_t<bf16_t, true>(a, s) : forward_t<bf16_t, false>(a, s);
     return a.vec ? forward_t<float, true>(a, s) : forward_t<float, false>(a, s);
-}
-
-template <typename T, bool VEC, bool CKPT> static hipError_t backward_t(const ScanArgs& a, hipStream_t s) {
-    const int nc = cols_of(a);
-    const int64_t nt = n_tiles(a.n_rows), grid = nt * nc;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    if (grid > 0)
-        hipLaunchKernelGGL((k_scan_backward<T, VEC, CKPT>), dim3((unsigned)grid), dim3(kThreads), 0, s, a, nc, nt);
-    return launch_sum_tiles(a.part, nt, a.C, 2, a.d_a_log, a.d_dt_bias, s);
-}
-
-template <typename T> static hipError_t backward_d(const ScanArgs& a, hipStream_t s) {
-    if (a.q) return a.vec ? backward_t<T, true, true>(a, s) : backward_t<T, false, true>(a, s);
-    return a.vec ? backward_t<T, true, false>(a, s) : backward_t<T, false, false>(a, s);
-}
-
-hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t s) {
-    MapArgs m = map_args(a);
-    m.pass_src = a.d_state; m.pass_dst = a.d_state0; m.pass_width = a.C;
-    const hipError_t e = launch_map(m, s);
-    if (e != hipSuccess) return e;
-    return a.act_dtype == GDN_BF16 ? backward_d<bf16_t>(a, s) : backward_d<float>(a, s);
 }
 
 }  // namespace gdnt
