@@ -96,16 +96,34 @@ __device__ __forceinline__ float exp2_hw(float v) { return __builtin_amdgcn_exp2
 // Chebyshev nodes of [0, 1] (3.4e-8 off, 1.7e-7 with fp32's roundings).
 // Relative accuracy holds for small softplus too, where log(1 + t) would
 // lose it: a decay near 1 is raised to long powers.
-__device__ __forceinline__ float softplus_t(float z, float& t) {
+// The coefficients sit in scalar registers: a vector instruction takes one
+// such operand for free, while a literal costs a move into the accumulator.
+template <uint32_t BITS> __device__ __forceinline__ float scalar_const() {
+    float c;
+    asm("s_mov_b32 %0, %1" : "=s"(c) : "i"(BITS));
+    return c;
+}
+struct SoftplusC {
+    float c[9];
+};
+__device__ __forceinline__ SoftplusC softplus_consts() {
+    SoftplusC k;
+    k.c[8] = scalar_const<0x3ba7f8ddu>();  // 0.00512610236f
+    k.c[7] = scalar_const<0xbcee2cbcu>();  // -0.0290740654f
+    k.c[6] = scalar_const<0x3d9ec0c1u>();  // 0.0775160864f
+    k.c[5] = scalar_const<0xbe0b497au>();  // -0.136022478f
+    k.c[4] = scalar_const<0x3e4358e6u>();  // 0.190768808f
+    k.c[3] = scalar_const<0xbe7e5082u>();  // -0.248353988f
+    k.c[2] = scalar_const<0x3eaa96bau>();  // 0.333181202f
+    k.c[1] = scalar_const<0xbeffff46u>();  // -0.499994457f
+    k.c[0] = scalar_const<0x3f7fffffu>();  // 0.99999994f
+    return k;
+}
+__device__ __forceinline__ float softplus_t(const SoftplusC& k, float z, float& t) {
     t = exp2_hw(-fabsf(z) * kLog2e);
-    float p = fmaf(t, 0.00512610236f, -0.0290740654f);
-    p = fmaf(t, p, 0.0775160864f);
-    p = fmaf(t, p, -0.136022478f);
-    p = fmaf(t, p, 0.190768808f);
-    p = fmaf(t, p, -0.248353988f);
-    p = fmaf(t, p, 0.333181202f);
-    p = fmaf(t, p, -0.499994457f);
-    p = fmaf(t, p, 0.99999994f);
+    float p = k.c[8];
+#pragma unroll
+    for (int i = 7; i >= 0; --i) p = fmaf(t, p, k.c[i]);
     return fmaf(t, p, fmaxf(z, 0.0f));
 }
 // sigmoid(b); the hardware exponential and reciprocal, about an ulp each.

@@ -51,35 +51,51 @@ template <typename T> __device__ __forceinline__ Raw2<T> zero2() {
     __builtin_memset(&r, 0, sizeof(r));
     return r;
 }
-template <typename T, bool VEC> __device__ __forceinline__ Raw2<T> load2(const T* p, int nc) {
-    Raw2<T> r;
-    if constexpr (VEC) {
-        r.v = *reinterpret_cast<const decltype(r.v)*>(p);
-    } else {
-        T e[2] = {T(0), T(0)};
-        if (nc > 0) e[0] = p[0];
-        if (nc > 1) e[1] = p[1];
-        __builtin_memcpy(&r, e, sizeof(r));
+// The rows of one tensor that a wave works on, from its first row on.  VEC: a
+// buffer descriptor, so that a row's place is a scalar offset and a lane's
+// place in the row one vector register for all rows and tensors of a type.
+template <typename T, bool VEC> struct WaveRows {
+    __amdgpu_buffer_rsrc_t rs;
+    T* p;
+    int64_t stride;
+    __device__ __forceinline__ WaveRows(const void* base, int64_t first, int64_t stride_, int64_t col)
+        : p(static_cast<T*>(const_cast<void*>(base)) + first * stride_ + col), stride(stride_) {
+        if constexpr (VEC) rs = __builtin_amdgcn_make_buffer_rsrc(p, 0, 0xffffffffu, 0x00020000);
     }
-    return r;
-}
-template <bool VEC> __device__ __forceinline__ void store2(bf16_t* p, float a, float b, int nc) {
-    const uint32_t v = gdn::f32x2_to_bf16x2(a, b);
-    if constexpr (VEC) {
-        *reinterpret_cast<uint32_t*>(p) = v;
-    } else {
-        if (nc > 0) p[0] = (bf16_t)v;
-        if (nc > 1) p[1] = (bf16_t)(v >> 16);
+    __device__ __forceinline__ Raw2<T> load(int r, int lane, int nc) const {
+        Raw2<T> v;
+        if constexpr (VEC) {
+            const uint32_t row = (uint32_t)(r * (uint32_t)stride * sizeof(T)), at = lane * 2 * sizeof(T);
+            if constexpr (sizeof(T) == 2) {
+                v.v = __builtin_amdgcn_raw_buffer_load_b32(rs, at, row, 0);
+            } else {
+                v.v = __builtin_bit_cast(float2, __builtin_amdgcn_raw_buffer_load_b64(rs, at, row, 0));
+            }
+        } else {
+            const T* q = p + r * stride + lane * 2;
+            T e[2] = {T(0), T(0)};
+            if (nc > 0) e[0] = q[0];
+            if (nc > 1) e[1] = q[1];
+            __builtin_memcpy(&v, e, sizeof(v));
+        }
+        return v;
     }
-}
-template <bool VEC> __device__ __forceinline__ void store2(float* p, float a, float b, int nc) {
-    if constexpr (VEC) {
-        *reinterpret_cast<float2*>(p) = make_float2(a, b);
-    } else {
-        if (nc > 0) p[0] = a;
-        if (nc > 1) p[1] = b;
+    __device__ __forceinline__ void store(int r, int lane, int nc, float a, float b) const {
+        if constexpr (VEC) {
+            const uint32_t row = (uint32_t)(r * (uint32_t)stride * sizeof(T)), at = lane * 2 * sizeof(T);
+            if constexpr (sizeof(T) == 2) {
+                __builtin_amdgcn_raw_buffer_store_b32(gdn::f32x2_to_bf16x2(a, b), rs, at, row, 0);
+            } else {
+                typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+                __builtin_amdgcn_raw_buffer_store_b64((u32x2){__float_as_uint(a), __float_as_uint(b)}, rs, at, row, 0);
+            }
+        } else {
+            T* q = p + r * stride + lane * 2;
+            if (nc > 0) q[0] = from_f32<T>(a);
+            if (nc > 1) q[1] = from_f32<T>(b);
+        }
     }
-}
+};
 
 // The wave's 16 rows of one tensor by this lane's two channels in 8 bits: a
 // block of the checkpoint is two neighbouring lanes' values, so one exchange
@@ -135,35 +151,31 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void k_scan_forwa
     const int64_t r0 = tile * kFwdRows + wave * FR, c0 = (int64_t)col * kFwdCols + lane * 2;
     const int64_t left = (int64_t)A.C - c0;
     const int nc = left >= 2 ? 2 : left > 0 ? (int)left : 0;
-    const int32_t* map = A.map + r0;
-    int32_t m[FR];
-    uint32_t in = 0, special = 0;  // rows of a sequence; of these the first and last ones
-#pragma unroll
-    for (int r = 0; r < FR; ++r) {
-        m[r] = map[r];
-        in |= m[r] >= 0 ? 1u << r : 0u;
-        special |= m[r] >= 0 && (m[r] & 3) ? 1u << r : 0u;
-    }
+    // rows of a sequence, and its first and last ones among them, as bits
+    const int32_t m16 = lane < FR ? A.map[r0 + lane] : -1;
+    const uint32_t in = (uint32_t)__ballot(m16 >= 0), firsts = (uint32_t)__ballot(m16 >= 0 && (m16 & 1)),
+                   lasts = (uint32_t)__ballot(m16 >= 0 && (m16 & 2));
+    auto seq_of = [&](int r) { return __builtin_amdgcn_readlane(m16, r) >> 2; };
 
+    const int64_t cb = (int64_t)col * kFwdCols;
+    const WaveRows<T, VEC> X(A.x, r0, A.x_stride, cb), Ag(A.a, r0, A.ab_stride, cb), Bg(A.b, r0, A.ab_stride, cb),
+        H(A.h, r0, A.h_stride, cb);
     Raw2<T> rx[FR], ra[FR], rb[FR];
-    const T* px = static_cast<const T*>(A.x) + r0 * A.x_stride + c0;
-    const T* pa = static_cast<const T*>(A.a) + r0 * A.ab_stride + c0;
-    const T* pb = static_cast<const T*>(A.b) + r0 * A.ab_stride + c0;
     if (in == 0xffffu && nc > 0) {
 #pragma unroll
         for (int r = 0; r < FR; ++r) {
-            ra[r] = load2<T, VEC>(pa + r * A.ab_stride, nc);
-            rx[r] = load2<T, VEC>(px + r * A.x_stride, nc);
-            rb[r] = load2<T, VEC>(pb + r * A.ab_stride, nc);
+            ra[r] = Ag.load(r, lane, nc);
+            rx[r] = X.load(r, lane, nc);
+            rb[r] = Bg.load(r, lane, nc);
         }
     } else {
 #pragma unroll
         for (int r = 0; r < FR; ++r) {
             rx[r] = zero2<T>(); ra[r] = zero2<T>(); rb[r] = zero2<T>();
             if ((in >> r & 1u) && nc > 0) {
-                ra[r] = load2<T, VEC>(pa + r * A.ab_stride, nc);
-                rx[r] = load2<T, VEC>(px + r * A.x_stride, nc);
-                rb[r] = load2<T, VEC>(pb + r * A.ab_stride, nc);
+                ra[r] = Ag.load(r, lane, nc);
+                rx[r] = X.load(r, lane, nc);
+                rb[r] = Bg.load(r, lane, nc);
             }
         }
     }
@@ -186,34 +198,28 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void k_scan_forwa
 
     float al[FR][2], u[FR][2];
     float ea[2] = {1.0f, 1.0f}, eu[2] = {0.0f, 0.0f};
+    // Rows of no sequence run along on zeros: what they make of the state goes
+    // nowhere, a first row follows them.
+    const SoftplusC spc = softplus_consts();
 #pragma unroll
     for (int r = 0; r < FR; ++r) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             float t;
-            al[r][i] = exp2_hw(kk[i] * softplus_t(ra[r].get(i) + dt[i], t));
+            al[r][i] = exp2_hw(kk[i] * softplus_t(spc, ra[r].get(i) + dt[i], t));
             u[r][i] = sigmoid_hw(rb[r].get(i)) * rx[r].get(i);
+            eu[i] = fmaf(al[r][i], eu[i], u[r][i]);
+            ea[i] *= al[r][i];
         }
-        if (!(in >> r & 1u)) {  // a row of no sequence changes nothing
-#pragma unroll
-            for (int i = 0; i < 2; ++i) { al[r][i] = 1.0f; u[r][i] = 0.0f; }
-        }
-        if ((special >> r & 1u) && (m[r] & 1)) {  // the state page joins a first row, nothing before it does
-            const int seq = m[r] >> 2;
+        if (firsts >> r & 1u) {  // the state page joins a first row, nothing before it does
+            const int seq = seq_of(r);
             const bool init = A.has_init ? A.has_init[seq] != 0 : true;
             const int64_t at = (int64_t)A.page_idx[seq] * A.st_in_stride + c0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (init && i < nc) u[r][i] = fmaf(al[r][i], load_state(A.st_in, at + i, A.state_dtype), u[r][i]);
-                al[r][i] = -1.0f;
                 eu[i] = u[r][i];
                 ea[i] = -1.0f;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                eu[i] = fmaf(al[r][i], eu[i], u[r][i]);
-                ea[i] *= al[r][i];
             }
         }
     }
@@ -232,7 +238,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void k_scan_forwa
             ta[0] = qa.x; ta[1] = qa.y; tu[0] = qu.x; tu[1] = qu.y;
         }
         const int32_t m_next = tile + 1 < n_tiles ? A.map[(tile + 1) * kFwdRows] : -1;
-        const bool cont = m[0] >= 0 && !(m[0] & 1);
+        const bool cont = (in & ~firsts) & 1u;
         const int64_t Cw = (int64_t)n_cols * kFwdCols;
         const Chain chain{A.chain, A.chain + n_tiles * Cw};
         float h[2];
@@ -252,18 +258,14 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void k_scan_forwa
         h[0] = walk(va.x, vu.x, h[0]);
         h[1] = walk(va.y, vu.y, h[1]);
     }
-    T* ph = static_cast<T*>(A.h) + r0 * A.h_stride + c0;
 #pragma unroll
     for (int r = 0; r < FR; ++r) {
-        if ((special >> r & 1u) && (m[r] & 1)) {
-            h[0] = u[r][0]; h[1] = u[r][1];
-        } else {
-            h[0] = fmaf(al[r][0], h[0], u[r][0]);
-            h[1] = fmaf(al[r][1], h[1], u[r][1]);
-        }
-        if ((in >> r & 1u) && nc > 0) store2<VEC>(ph + r * A.h_stride, h[0], h[1], nc);
-        if ((special >> r & 1u) && (m[r] & 2)) {
-            const int64_t at = (int64_t)A.page_idx[m[r] >> 2] * A.st_out_stride + c0;
+        h[0] = fmaf(al[r][0], h[0], u[r][0]);
+        h[1] = fmaf(al[r][1], h[1], u[r][1]);
+        if (firsts >> r & 1u) { h[0] = u[r][0]; h[1] = u[r][1]; }
+        if ((in >> r & 1u) && nc > 0) H.store(r, lane, nc, h[0], h[1]);
+        if (lasts >> r & 1u) {
+            const int64_t at = (int64_t)A.page_idx[seq_of(r)] * A.st_out_stride + c0;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
                 if (i < nc) store_state(A.st_out, at + i, A.state_dtype, h[i]);
@@ -305,6 +307,7 @@ __global__ __launch_bounds__(256) void k_scan_rows(const ScanArgs A, int n_x) {
             for (int i = 0; i < 4; ++i) h[i] = v.get(i);
         }
     }
+    const SoftplusC spc = softplus_consts();
     const ChanP P = load_params(A.a_log, A.dt_bias, c0, nc);
     for (int64_t r = r0; r < r1; ++r) {
         const Raw4<T> x = load4<T, VEC>(static_cast<const T*>(A.x) + r * A.x_stride + c0, nc);
@@ -313,7 +316,7 @@ __global__ __launch_bounds__(256) void k_scan_rows(const ScanArgs A, int n_x) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float t;
-            const float sp = softplus_t(a.get(i) + P.dt[i], t);
+            const float sp = softplus_t(spc, a.get(i) + P.dt[i], t);
             h[i] = fmaf(exp2_hw(P.k[i] * sp), h[i], sigmoid_hw(b.get(i)) * x.get(i));
         }
         store4<VEC>(static_cast<T*>(A.h) + r * A.h_stride + c0, h, nc);
@@ -354,6 +357,8 @@ hipError_t launch_scan_rows(const ScanArgs& a, hipStream_t s) {
 }
 
 template <typename T, bool VEC> static hipError_t forward_t(const ScanArgs& a, hipStream_t s) {
+    // VEC addresses a wave's 16 rows by 32-bit byte offsets
+    if (VEC && (a.x_stride | a.ab_stride | a.h_stride) >> 25) return forward_t<T, false>(a, s);
     const int nc = (int)((a.C + kFwdCols - 1) / kFwdCols);
     const int64_t nt = (a.n_rows + kFwdRows - 1) / kFwdRows, grid = nt * nc;
     if (grid == 0) return hipSuccess;

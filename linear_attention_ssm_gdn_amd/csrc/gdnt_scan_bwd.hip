@@ -99,6 +99,7 @@ __global__ __launch_bounds__(kThreads) void k_scan_backward(const ScanArgs A, in
             for (int i = 0; i < 4; ++i) { x[r][i] = rx.get(i); a[r][i] = ra.get(i); b[r][i] = rb.get(i); }
         }
     }
+    const SoftplusC spc = softplus_consts();
     const ChanP P = load_params(A.a_log, A.dt_bias, w.c0, w.nc);
 
     // forward run (ea, eu) and reverse run (fa, fu) of the rows; h0[r] is kept in u
@@ -118,7 +119,7 @@ __global__ __launch_bounds__(kThreads) void k_scan_backward(const ScanArgs A, in
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float t;
-            const float sp = softplus_t(a[r][i] + P.dt[i], t);
+            const float sp = softplus_t(spc, a[r][i] + P.dt[i], t);
             al[r][i] = in ? exp2_hw(P.k[i] * sp) : 1.0f;
             u[r][i] = in ? sigmoid_hw(b[r][i]) * x[r][i] : 0.0f;
             h0[r][i] = 0.0f;
@@ -252,7 +253,7 @@ __global__ __launch_bounds__(kThreads) void k_scan_backward(const ScanArgs A, in
             }
             float t;
             const float z = a[r][i] + P.dt[i];
-            const float sp = softplus_t(z, t);
+            const float sp = softplus_t(spc, z, t);
             const float sg = (z >= 0.0f ? 1.0f : t) * rcp(1.0f + t);
             const float be = sigmoid_hw(b[r][i]);
             mu[i] = in ? al[r][i] * lam : mu[i];
