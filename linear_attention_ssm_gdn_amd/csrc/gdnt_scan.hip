@@ -11,96 +11,17 @@
 // (gdnt_chain.hpp), and each wave walks its rows again from registers: x, a
 // and b are read once.  Sequence boundaries may fall anywhere.
 #include "gdnt_chain.hpp"
+#include "gdnt_rows.hpp"
 
 namespace gdnt {
 
-constexpr int FR = 16;                       // rows of a wave
 constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * 64;
 constexpr int kFwdRows = FR * kWaves;        // 128
 constexpr int kFwdCols = 128;
-static_assert(kTileRows % kFwdRows == 0 && FR == GDNT_CKPT_ROWS, "tile shape");
+static_assert(kTileRows % kFwdRows == 0, "tile shape");
 
-// Two channels of a row as they are stored.
-template <typename T> struct Raw2;
-template <> struct Raw2<bf16_t> {
-    uint32_t v;
-    __device__ __forceinline__ float get(int i) const { return __uint_as_float(i ? v & 0xffff0000u : v << 16); }
-    // the larger of |value|s as bits, kept per channel; NaN above Inf above all others
-    __device__ __forceinline__ uint32_t top(uint32_t t) const {
-        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-        return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, t),
-                                                                     __builtin_bit_cast(u16x2, v & 0x7fff7fffu)));
-    }
-    static __device__ __forceinline__ uint32_t top_bits(uint32_t t) {
-        const uint32_t a = t << 16, b = t & 0xffff0000u;
-        return a > b ? a : b;
-    }
-};
-template <> struct Raw2<float> {
-    float2 v;
-    __device__ __forceinline__ float get(int i) const { return i ? v.y : v.x; }
-    __device__ __forceinline__ uint32_t top(uint32_t t) const {
-        const uint32_t a = __float_as_uint(v.x) & 0x7fffffffu, b = __float_as_uint(v.y) & 0x7fffffffu;
-        return max(t, max(a, b));
-    }
-    static __device__ __forceinline__ uint32_t top_bits(uint32_t t) { return t; }
-};
-template <typename T> __device__ __forceinline__ Raw2<T> zero2() {
-    Raw2<T> r;
-    __builtin_memset(&r, 0, sizeof(r));
-    return r;
-}
-// The rows of one tensor that a wave works on, from its first row on.  VEC: a
-// buffer descriptor, so that a row's place is a scalar offset and a lane's
-// place in the row one vector register for all rows and tensors of a type.
-template <typename T, bool VEC> struct WaveRows {
-    __amdgpu_buffer_rsrc_t rs;
-    T* p;
-    int64_t stride;
-    __device__ __forceinline__ WaveRows(const void* base, int64_t first, int64_t stride_, int64_t col)
-        : p(static_cast<T*>(const_cast<void*>(base)) + first * stride_ + col), stride(stride_) {
-        if constexpr (VEC) rs = __builtin_amdgcn_make_buffer_rsrc(p, 0, 0xffffffffu, 0x00020000);
-    }
-    __device__ __forceinline__ Raw2<T> load(int r, int lane, int nc) const {
-        Raw2<T> v;
-        if constexpr (VEC) {
-            const uint32_t row = (uint32_t)(r * (uint32_t)stride * sizeof(T)), at = lane * 2 * sizeof(T);
-            if constexpr (sizeof(T) == 2) {
-                v.v = __builtin_amdgcn_raw_buffer_load_b32(rs, at, row, 0);
-            } else {
-                v.v = __builtin_bit_cast(float2, __builtin_amdgcn_raw_buffer_load_b64(rs, at, row, 0));
-            }
-        } else {
-            const T* q = p + r * stride + lane * 2;
-            T e[2] = {T(0), T(0)};
-            if (nc > 0) e[0] = q[0];
-            if (nc > 1) e[1] = q[1];
-            __builtin_memcpy(&v, e, sizeof(v));
-        }
-        return v;
-    }
-    __device__ __forceinline__ void store(int r, int lane, int nc, float a, float b) const {
-        if constexpr (VEC) {
-            const uint32_t row = (uint32_t)(r * (uint32_t)stride * sizeof(T)), at = lane * 2 * sizeof(T);
-            if constexpr (sizeof(T) == 2) {
-                __builtin_amdgcn_raw_buffer_store_b32(gdn::f32x2_to_bf16x2(a, b), rs, at, row, 0);
-            } else {
-                typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-                __builtin_amdgcn_raw_buffer_store_b64((u32x2){__float_as_uint(a), __float_as_uint(b)}, rs, at, row, 0);
-            }
-        } else {
-            T* q = p + r * stride + lane * 2;
-            if (nc > 0) q[0] = from_f32<T>(a);
-            if (nc > 1) q[1] = from_f32<T>(b);
-        }
-    }
-};
-
-// The wave's 16 rows of one tensor by this lane's two channels in 8 bits: a
-// block of the checkpoint is two neighbouring lanes' values, so one exchange
-// between them gives the scale, and another gives each lane eight whole rows
-// of the block (32 of its 64 bytes).
+// The wave's 16 rows of one tensor by this lane's two channels in 8 bits.
 template <typename T>
 __device__ __forceinline__ void put_ckpt(const Raw2<T> (&v)[FR], int8_t* q, float* scale, int lane, bool mine) {
     uint32_t top = 0;
@@ -124,10 +45,7 @@ __device__ __forceinline__ void put_ckpt(const Raw2<T> (&v)[FR], int8_t* q, floa
         // row r in the low half, row r + 8 in the high half
         const uint32_t lo = __builtin_amdgcn_perm(e[1], e[0], 0x0c0c0400u);
         const uint32_t hi = __builtin_amdgcn_perm(e[3], e[2], 0x04000c0cu);
-        const uint32_t p = lo | hi;
-        const uint32_t x = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)p, 0xB1, 0xF, 0xF, false);
-        // even lane: its low half below the other's; odd lane: the other's high half below its own
-        w[r] = (lane & 1) ? __builtin_amdgcn_perm(p, x, 0x07060302u) : __builtin_amdgcn_perm(x, p, 0x05040100u);
+        w[r] = swap_halves(lo | hi, lane);
     }
     if (mine) {
         uint4* out = reinterpret_cast<uint4*>(q + (lane >> 1) * 64 + (lane & 1) * 32);
@@ -158,26 +76,32 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void k_scan_forwa
     auto seq_of = [&](int r) { return __builtin_amdgcn_readlane(m16, r) >> 2; };
 
     const int64_t cb = (int64_t)col * kFwdCols;
-    const WaveRows<T, VEC> X(A.x, r0, A.x_stride, cb), Ag(A.a, r0, A.ab_stride, cb), Bg(A.b, r0, A.ab_stride, cb),
-        H(A.h, r0, A.h_stride, cb);
+    const WaveRows<T, VEC> X(A.x, A.x_stride, A.n_rows, r0, A.C, cb, lane * 2),
+        Ag(A.a, A.ab_stride, A.n_rows, r0, A.C, cb, lane * 2), Bg(A.b, A.ab_stride, A.n_rows, r0, A.C, cb, lane * 2),
+        H(A.h, A.h_stride, A.n_rows, r0, A.C, cb, lane * 2);
     Raw2<T> rx[FR], ra[FR], rb[FR];
     if (in == 0xffffu && nc > 0) {
 #pragma unroll
         for (int r = 0; r < FR; ++r) {
-            ra[r] = Ag.load(r, lane, nc);
-            rx[r] = X.load(r, lane, nc);
-            rb[r] = Bg.load(r, lane, nc);
+            ra[r] = Ag.load(r, nc);
+            rx[r] = X.load(r, nc);
+            rb[r] = Bg.load(r, nc);
         }
     } else {
 #pragma unroll
         for (int r = 0; r < FR; ++r) {
             rx[r] = zero2<T>(); ra[r] = zero2<T>(); rb[r] = zero2<T>();
             if ((in >> r & 1u) && nc > 0) {
-                ra[r] = Ag.load(r, lane, nc);
-                rx[r] = X.load(r, lane, nc);
-                rb[r] = Bg.load(r, lane, nc);
+                ra[r] = Ag.load(r, nc);
+                rx[r] = X.load(r, nc);
+                rb[r] = Bg.load(r, nc);
             }
         }
+    }
+    if (VEC && (A.C & 1) && col == n_cols - 1) {
+        fix_last(rx, nc);
+        fix_last(ra, nc);
+        fix_last(rb, nc);
     }
     float dt[2], kk[2];
 #pragma unroll
@@ -263,7 +187,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void k_scan_forwa
         h[0] = fmaf(al[r][0], h[0], u[r][0]);
         h[1] = fmaf(al[r][1], h[1], u[r][1]);
         if (firsts >> r & 1u) { h[0] = u[r][0]; h[1] = u[r][1]; }
-        if ((in >> r & 1u) && nc > 0) H.store(r, lane, nc, h[0], h[1]);
+        if ((in >> r & 1u) && nc > 0) H.store(r, nc, h[0], h[1]);
         if (lasts >> r & 1u) {
             const int64_t at = (int64_t)A.page_idx[seq_of(r)] * A.st_out_stride + c0;
 #pragma unroll
@@ -358,7 +282,7 @@ hipError_t launch_scan_rows(const ScanArgs& a, hipStream_t s) {
 
 template <typename T, bool VEC> static hipError_t forward_t(const ScanArgs& a, hipStream_t s) {
     // VEC addresses a wave's 16 rows by 32-bit byte offsets
-    if (VEC && (a.x_stride | a.ab_stride | a.h_stride) >> 25) return forward_t<T, false>(a, s);
+    if (VEC && (a.x_stride | a.ab_stride | a.h_stride) >> 24) return forward_t<T, false>(a, s);
     const int nc = (int)((a.C + kFwdCols - 1) / kFwdCols);
     const int64_t nt = (a.n_rows + kFwdRows - 1) / kFwdRows, grid = nt * nc;
     if (grid == 0) return hipSuccess;
@@ -373,8 +297,8 @@ template <typename T, bool VEC> static hipError_t forward_t(const ScanArgs& a, h
 hipError_t launch_scan_forward(const ScanArgs& a, hipStream_t s) {
     const hipError_t e = launch_map(scan_map_args(a), s);
     if (e != hipSuccess) return e;
-    if (a.act_dtype == GDN_BF16) return a.vec ? forward_t<bf16_t, true>(a, s) : forward_t<bf16_t, false>(a, s);
-    return a.vec ? forward_t<float, true>(a, s) : forward_t<float, false>(a, s);
+    if (a.act_dtype == GDN_BF16) return a.vec2 ? forward_t<bf16_t, true>(a, s) : forward_t<bf16_t, false>(a, s);
+    return a.vec2 ? forward_t<float, true>(a, s) : forward_t<float, false>(a, s);
 }
 
 }  // namespace gdnt
