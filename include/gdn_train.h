@@ -28,8 +28,10 @@
  * - Sequences of length 0 are no-ops; a backward pass hands the gradient of
  *   their final state or window through to the initial one.
  * - Any row stride >= channels and any element-aligned pointer is accepted.
- *   Rows that start 8-byte (bf16) or 16-byte (fp32) aligned, in channels a
- *   multiple of 4, are read and written as vectors, others one by one.
+ *   Rows on whole vectors are faster: on 4 bytes for the recurrence (any
+ *   fp32 rows; bf16 rows of even stride), on four elements and in channels a
+ *   multiple of 4 for the conv and the one-launch form.  Others are read and
+ *   written element by element.
  * - Inputs and outputs of one call must not overlap, but a state pool may be
  *   both state_in and state_out.
  * - workspace: 256-byte aligned device memory of at least the queried size,
@@ -130,7 +132,7 @@ int32_t gdnt_scan_forward(const gdnt_scan_dims* dims, const gdnt_scan_params* pa
  * dx: [n_rows][dx_stride]; da, db: [n_rows][dab_stride] (act dtype);
  * d_a_log, d_dt_bias: [channels] fp32, over the sequences of this call,
  * overwritten (zeros for an empty batch); d_state0: [n_seqs][channels] fp32
- * or NULL, zeros where has_init is 0, unwritten for skipped sequences. */
+ * or NULL, zeros where has_init is 0 and for padding and skipped sequences. */
 int32_t gdnt_scan_backward(const gdnt_scan_dims* dims, const gdnt_scan_params* params,
                            const void* x, int64_t x_stride, const void* a, const void* b, int64_t ab_stride,
                            const void* ckpt, const gdn_batch* batch, gdn_state_pool state_in, const float* states,
@@ -153,7 +155,7 @@ int32_t gdnt_scan_backward(const gdnt_scan_dims* dims, const gdnt_scan_params* p
  * dx: [n_rows][dx_stride] act dtype; d_conv_w: [C_conv][conv_w] fp32, over
  * the sequences of this call, overwritten (zeros for an empty batch);
  * d_window0: [n_seqs][conv_w-1][C_conv] fp32 or NULL, zeros where has_init is
- * 0, unwritten for skipped sequences. */
+ * 0 and for padding and skipped sequences. */
 int32_t gdnt_conv_backward(const gdn_dims* dims, const void* conv_w, const void* x, int64_t x_stride,
                            const void* dy, int32_t dy_dtype, int64_t dy_stride,
                            const gdn_batch* batch, gdn_conv_pool conv, int32_t activation, const float* d_window,

@@ -29,7 +29,7 @@ __device__ __forceinline__ void join(float pa, float pu, float& qa, float& qu) {
 
 struct Chain {
     uint64_t* state;  // {1, end state}
-    uint64_t* run;    // {a with its sign bit set, u}, a > 0
+    int64_t run;      // as many words further: {a with its sign bit set, u}, a > 0
 };
 constexpr int kLookBack = 8;
 constexpr int kSpins = 1 << 21;  // some seconds, far beyond any tile's run
@@ -52,7 +52,7 @@ __device__ __forceinline__ void look_back(const Chain& C, int64_t at, int64_t st
     int found = -1;
     for (int spin = 0; spin < kSpins; ++spin) {
         uint64_t v = 0;
-        if (lane < 2 * kLookBack && j <= n_pred) v = chain_load((lane & 8 ? C.run : C.state) + at + j * step);
+        if (lane < 2 * kLookBack && j <= n_pred) v = chain_load(C.state + (lane & 8 ? C.run : 0) + at + j * step);
         const uint64_t ready = __ballot((v >> 32) != 0);
         const uint32_t states = (uint32_t)ready & 0xffu, runs = (uint32_t)(ready >> 8) & 0xffu;
         if (states) {
@@ -75,7 +75,7 @@ __device__ __forceinline__ void look_back(const Chain& C, int64_t at, int64_t st
             for (int q = 0; q < kLookBack - 1; ++q)
                 if (q < found) {
 #pragma unroll
-                    for (int i = 0; i < NCH; ++i) g[q][i] = chain_load(C.run + mine + (q + 1) * step + i);
+                    for (int i = 0; i < NCH; ++i) g[q][i] = chain_load(C.state + C.run + mine + (q + 1) * step + i);
                 }
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
@@ -113,7 +113,7 @@ __device__ __forceinline__ void hand_on(const Chain& C, int64_t at, int64_t step
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
             if (known) chain_store(C.state + mine + i, 1u, u[i]);
-            else chain_store(C.run + mine + i, __float_as_uint(a[i]) | 0x80000000u, u[i]);
+            else chain_store(C.state + C.run + mine + i, __float_as_uint(a[i]) | 0x80000000u, u[i]);
         }
     }
 #pragma unroll

@@ -25,8 +25,9 @@ struct MapArgs {
     int32_t page_limit, max_len;   // 0 <= page < page_limit; max_len 0: any length
     int32_t* map;
     uint32_t* zero; int64_t n_zero;  // words to clear for the kernel that follows
-    // a backward pass hands the final gradient of empty sequences through:
-    // rows of `width` values, NULL src: zeros, NULL dst: nothing to do
+    // a backward pass hands the final gradient of empty sequences through and
+    // clears that of skipped ones: rows of `width` values, NULL src: zeros,
+    // NULL dst: nothing to do
     const float* pass_src; float* pass_dst; int64_t pass_width;
     int32_t* err;
 };

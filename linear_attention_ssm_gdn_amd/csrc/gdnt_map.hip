@@ -78,14 +78,15 @@ __global__ __launch_bounds__(kMapThreads) void k_row_map(const MapArgs A) {
             else if (A.max_len > 0 && A.cu[s + 1] - A.cu[s] > A.max_len) raise(A.err, GDN_DEVERR_BATCH);
         }
     }
-    if (A.pass_dst) {
+    if (A.pass_dst) {  // rows of sequences that no kernel behind this one writes
         for (int s = blockIdx.x; s < A.n_seqs; s += gridDim.x) {
-            const int page = A.page_idx[s];
-            if (page < 0 || page >= A.page_limit || A.cu[s] != A.cu[s + 1]) continue;
-            if (bad && !valid_slow(A, s)) continue;
+            const int page = A.page_idx[s], c0 = A.cu[s], c1 = A.cu[s + 1];
+            const bool live = page >= 0 && page < A.page_limit && !(bad && !valid_slow(A, s)) &&
+                              (A.max_len == 0 || c1 - c0 <= A.max_len);
+            if (live && c0 != c1) continue;
             const int64_t at = (int64_t)s * A.pass_width;
             for (int64_t i = tid; i < A.pass_width; i += kMapThreads)
-                A.pass_dst[at + i] = A.pass_src ? A.pass_src[at + i] : 0.0f;
+                A.pass_dst[at + i] = live && A.pass_src ? A.pass_src[at + i] : 0.0f;
         }
     }
 }

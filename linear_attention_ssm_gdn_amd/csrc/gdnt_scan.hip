@@ -164,7 +164,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void k_scan_forwa
         const int32_t m_next = tile + 1 < n_tiles ? A.map[(tile + 1) * kFwdRows] : -1;
         const bool cont = (in & ~firsts) & 1u;
         const int64_t Cw = (int64_t)n_cols * kFwdCols;
-        const Chain chain{A.chain, A.chain + n_tiles * Cw};
+        const Chain chain{A.chain, n_tiles * Cw};
         float h[2];
         hand_on<2>(chain, tile * Cw + (int64_t)col * kFwdCols, -Cw, tile, cont, m_next >= 0 && !(m_next & 1), ta, tu,
                    h, A.err);

@@ -232,7 +232,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
             join(ta, tu, ja, ju);
             ta = ja; tu = ju;
         }
-        const Chain chain{A.chain, A.chain + n_tiles * Cp};
+        const Chain chain{A.chain, n_tiles * Cp};
         const float a1[1] = {ta}, u1[1] = {tu};
         float h1[1];
         hand_on<1>(chain, tile * Cp + cb, Cp, n_tiles - 1 - tile, m_last >= 0 && !(m_last & 2),

@@ -98,26 +98,34 @@ def gdnt_conv_workspace_bytes(dims: Dims, n_seqs: int, n_rows: int) -> int:
 
 
 def _on(dev: torch.device, **tensors) -> None:
+    where = dev.index
     for name, t in tensors.items():
-        if t is not None and t.device != dev:
+        if t is not None and (t.get_device() != where if where is not None else t.device != dev):
             raise ValueError(f"{name} is on {t.device}, not on {dev}")
 
 
 def _rows2(name: str, t: torch.Tensor, rows: int, cols: int, dt: torch.dtype) -> int:
     """The row stride of a [rows][cols] tensor."""
-    if t.dtype != dt:
+    if t.dtype is not dt:
         raise ValueError(f"{name} must be {dt}, not {t.dtype}")
-    if t.shape != (rows, cols) or (cols > 1 and t.stride(1) != 1):
+    st = t.stride()
+    if t.shape != (rows, cols) or (cols > 1 and st[1] != 1):
         raise ValueError(f"{name} must be [{rows}][{cols}] with unit inner stride")
-    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
+    return st[0] if rows > 1 else max(st[0], cols)
 
 
 def _flat(name: str, t: Optional[torch.Tensor], shape: tuple, dt: torch.dtype) -> Optional[int]:
     if t is None:
         return None
-    if t.dtype != dt or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype is not dt or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dt} tensor of shape {list(shape)}")
     return t.data_ptr()
+
+
+def _err(err: Optional[torch.Tensor]) -> Optional[int]:
+    if err is not None and (err.dtype is not torch.int32 or err.numel() < 1):
+        raise ValueError("err must be an int32 tensor")
+    return _p(err)
 
 
 def _check_batch(batch: Batch, dev: torch.device) -> None:
@@ -130,7 +138,7 @@ def _check_batch(batch: Batch, dev: torch.device) -> None:
 
 def _check_state_pool(name: str, pool: StatePool, dims: ScanDims) -> None:
     t = pool.buf
-    if t.dtype != dims.state_torch or t.dim() != 2 or t.shape[1] != dims.channels or \
+    if t.dtype is not dims.state_torch or t.dim() != 2 or t.shape[1] != dims.channels or \
             (dims.channels > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be [pages][{dims.channels}] of {dims.state_torch} with unit inner stride")
 
@@ -140,13 +148,24 @@ def _check_params(params: ScanParams, dims: ScanDims) -> None:
     _flat("dt_bias", params.dt_bias, (dims.channels,), torch.float32)
 
 
-def _workspace(ws: Optional[torch.Tensor], need: int, dev: torch.device) -> torch.Tensor:
+def _workspace(ws: Optional[torch.Tensor], size, dims, n_seqs: int, n_rows: int, dev: torch.device) -> torch.Tensor:
     if ws is None:
-        return torch.empty(need, dtype=torch.uint8, device=dev)
-    if ws.dtype != torch.uint8 or not ws.is_contiguous():
-        raise ValueError("workspace must be a contiguous uint8 tensor")
+        return torch.empty(size(dims, n_seqs, n_rows), dtype=torch.uint8, device=dev)
+    if ws.dtype is not torch.uint8 or not ws.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")  # its size is the library's to check
     _on(dev, workspace=ws)
     return ws
+
+
+def _call(fn: str, dev: torch.device, *args) -> None:
+    """The C entry point on the current stream of `dev`, with `dev` current."""
+    f = getattr(L.load(), fn)
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    _check(fn, st)
 
 
 def _p(t: Optional[torch.Tensor]):
@@ -165,8 +184,9 @@ def gdnt_scan_forward(dims: ScanDims, params: ScanParams, x: torch.Tensor, a: to
                       h: Optional[torch.Tensor] = None, saved: Optional[ScanSaved] = None,
                       workspace: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None) -> torch.Tensor:
     """h [n_rows][channels] (rows of no sequence and of padding left as they
-    are); the final states go to state_out (default: state_in, in place).  `saved` receives what gdnt_scan_backward needs, x, a
-    and b in 8 bits among it where it has a ckpt."""
+    are); the final states go to state_out (default: state_in, in place).
+    `saved` receives what gdnt_scan_backward needs, x, a and b in 8 bits among
+    it where it has a ckpt."""
     dev, n, C = x.device, batch.n_rows, dims.channels
     state_out = state_in if state_out is None else state_out
     if h is None:
@@ -183,15 +203,12 @@ def gdnt_scan_forward(dims: ScanDims, params: ScanParams, x: torch.Tensor, a: to
         raise ValueError("a and b must share their row stride")
     if saved is not None:
         _check_saved(saved, dims, n, dev)
-    ws = _workspace(workspace, gdnt_scan_workspace_bytes(dims, batch.n_seqs, n), dev)
+    ws = _workspace(workspace, gdnt_scan_workspace_bytes, dims, batch.n_seqs, n, dev)
     d, p, bt = dims.c(), params.c(), batch.c()
-    with torch.cuda.device(dev):
-        st = L.load().gdnt_scan_forward(
-            ctypes.byref(d), ctypes.byref(p), x.data_ptr(), xs, a.data_ptr(), b.data_ptr(), as_, ctypes.byref(bt),
-            state_in.c(), state_out.c(), h.data_ptr(), hs, _p(saved.states) if saved is not None else None,
-            _p(saved.ckpt) if saved is not None else None, ws.data_ptr(), ws.numel(), _p(err),
-            torch.cuda.current_stream(dev).cuda_stream)
-    _check("gdnt_scan_forward", st)
+    _call("gdnt_scan_forward", dev,
+          ctypes.byref(d), ctypes.byref(p), x.data_ptr(), xs, a.data_ptr(), b.data_ptr(), as_, ctypes.byref(bt),
+          state_in.c(), state_out.c(), h.data_ptr(), hs, _p(saved.states) if saved is not None else None,
+          _p(saved.ckpt) if saved is not None else None, ws.data_ptr(), ws.numel(), _err(err))
     return h
 
 
@@ -214,7 +231,7 @@ def gdnt_scan_backward(dims: ScanDims, params: ScanParams, batch: Batch, state_i
     if out is None:
         out = ScanGrads(*(torch.empty((n, C), dtype=dims.act_torch, device=dev) for _ in range(3)),
                         *(torch.empty(C, dtype=torch.float32, device=dev) for _ in range(2)),
-                        torch.zeros((s, C), dtype=torch.float32, device=dev))
+                        torch.empty((s, C), dtype=torch.float32, device=dev))
     _on(dev, x=x, a=a, b=b, d_state=d_state, state_in=state_in.buf, a_log=params.a_log, dt_bias=params.dt_bias,
         err=err, **out._asdict())
     _check_params(params, dims)
@@ -232,16 +249,13 @@ def gdnt_scan_backward(dims: ScanDims, params: ScanParams, batch: Batch, state_i
     _flat("d_a_log", out.d_a_log, (C,), torch.float32)
     _flat("d_dt_bias", out.d_dt_bias, (C,), torch.float32)
     _flat("d_state0", out.d_state0, (s, C), torch.float32)
-    ws = _workspace(workspace, gdnt_scan_workspace_bytes(dims, s, n), dev)
+    ws = _workspace(workspace, gdnt_scan_workspace_bytes, dims, s, n, dev)
     d, p, bt = dims.c(), params.c(), batch.c()
-    with torch.cuda.device(dev):
-        st = L.load().gdnt_scan_backward(
-            ctypes.byref(d), ctypes.byref(p), _p(x), xs, _p(a), _p(b), as_, None if all(given) else _p(saved.ckpt),
-            ctypes.byref(bt), state_in.c(), saved.states.data_ptr(), dh.data_ptr(), hs, _p(d_state),
-            out.dx.data_ptr(), dxs, out.da.data_ptr(), out.db.data_ptr(), das, out.d_a_log.data_ptr(),
-            out.d_dt_bias.data_ptr(), out.d_state0.data_ptr(), ws.data_ptr(), ws.numel(), _p(err),
-            torch.cuda.current_stream(dev).cuda_stream)
-    _check("gdnt_scan_backward", st)
+    _call("gdnt_scan_backward", dev,
+          ctypes.byref(d), ctypes.byref(p), _p(x), xs, _p(a), _p(b), as_, None if all(given) else _p(saved.ckpt),
+          ctypes.byref(bt), state_in.c(), saved.states.data_ptr(), dh.data_ptr(), hs, _p(d_state),
+          out.dx.data_ptr(), dxs, out.da.data_ptr(), out.db.data_ptr(), das, out.d_a_log.data_ptr(),
+          out.d_dt_bias.data_ptr(), out.d_state0.data_ptr(), ws.data_ptr(), ws.numel(), _err(err))
     return out
 
 
@@ -258,8 +272,9 @@ def gdnt_conv_backward(dims: Dims, conv_w: torch.Tensor, x: torch.Tensor, dy: to
     if dy.dtype not in _NAMES:
         raise ValueError(f"dy must be fp32 or bf16, not {dy.dtype}")
     if out is None:
-        out = ConvGrads(torch.empty((n, C), dtype=dims.act_torch, device=dev), torch.empty((C, dims.conv_w), dtype=torch.float32, device=dev),
-                        torch.zeros((s, k, C), dtype=torch.float32, device=dev))
+        out = ConvGrads(torch.empty((n, C), dtype=dims.act_torch, device=dev),
+                        torch.empty((C, dims.conv_w), dtype=torch.float32, device=dev),
+                        torch.empty((s, k, C), dtype=torch.float32, device=dev))
     _on(dev, conv_w=conv_w, dy=dy, conv=conv.buf if conv is not None else None, d_window=d_window, err=err,
         **out._asdict())
     _check_batch(batch, dev)
@@ -276,13 +291,10 @@ def gdnt_conv_backward(dims: Dims, conv_w: torch.Tensor, x: torch.Tensor, dy: to
     _flat("d_window", d_window, (s, k, C), torch.float32)
     _flat("d_conv_w", out.d_conv_w, (C, dims.conv_w), torch.float32)
     _flat("d_window0", out.d_window0, (s, k, C), torch.float32)
-    ws = _workspace(workspace, gdnt_conv_workspace_bytes(dims, s, n), dev)
+    ws = _workspace(workspace, gdnt_conv_workspace_bytes, dims, s, n, dev)
     d, bt = dims.c(), batch.c()
-    with torch.cuda.device(dev):
-        st = L.load().gdnt_conv_backward(
-            ctypes.byref(d), conv_w.data_ptr(), x.data_ptr(), xs, dy.data_ptr(), _DT[_NAMES[dy.dtype]], ys,
-            ctypes.byref(bt), cp, 1 if activation else 0, _p(d_window), out.dx.data_ptr(), dxs,
-            out.d_conv_w.data_ptr(), out.d_window0.data_ptr(), ws.data_ptr(), ws.numel(), _p(err),
-            torch.cuda.current_stream(dev).cuda_stream)
-    _check("gdnt_conv_backward", st)
+    _call("gdnt_conv_backward", dev,
+          ctypes.byref(d), conv_w.data_ptr(), x.data_ptr(), xs, dy.data_ptr(), _DT[_NAMES[dy.dtype]], ys,
+          ctypes.byref(bt), cp, 1 if activation else 0, _p(d_window), out.dx.data_ptr(), dxs,
+          out.d_conv_w.data_ptr(), out.d_window0.data_ptr(), ws.data_ptr(), ws.numel(), _err(err))
     return out

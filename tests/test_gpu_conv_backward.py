@@ -77,9 +77,7 @@ class Conv:
         close("dx", host(out.dx), ref["dx"], mag["dx"], tol, self.act)
         # a sum of at most 16 + 4 + 2 fp32 additions deep, then fp64: inside tol
         close("d_conv_w", host(out.d_conv_w), ref["d_conv_w"], mag["d_conv_w"], tol, "f32")
-        d0 = ref["d_window0"].copy()
-        d0[[s for s, sp in enumerate(self.spans) if sp is None]] = np.nan
-        close("d_window0", host(out.d_window0), d0, mag["d_window0"], tol, "f32")
+        close("d_window0", host(out.d_window0), ref["d_window0"], mag["d_window0"], tol, "f32")  # zeros where skipped
 
 
 LENS = {"one": [1], "two": [2], "three": [3], "four": [4], "edge": [15, 16, 17], "tile": [256], "tile+2": [258, 1],
