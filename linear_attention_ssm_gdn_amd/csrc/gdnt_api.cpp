@@ -132,7 +132,7 @@ GDN_EXPORT int32_t gdnt_conv_workspace_bytes(const gdn_dims* dims, int32_t n_seq
     const int64_t C = 2 * (int64_t)dims->h_k * dims->d_k + (int64_t)dims->h_v * dims->d_v;
     if ((st = check_size(n_rows, C)) != GDN_OK) return st;
     *out_bytes = round_up((size_t)n_tiles(n_rows) * gdnt::kTileRows * sizeof(int32_t) +
-                          (size_t)gdnt::conv_tiles_max(n_rows) * 4 * (size_t)padded_channels(C) * sizeof(float));
+                          (size_t)gdnt::conv_tiles(n_rows, C) * 4 * (size_t)padded_channels(C) * sizeof(float));
     return GDN_OK;
 }
 

@@ -3,24 +3,69 @@
 //   z_t = sum_j w_j X_{t-3+j},  dz_t = dy_t silu'(z_t),
 //   dX_t = sum_j w_j dz_{t+3-j},  dw_j = sum_t dz_t X_{t-3+j}.
 //
-// Sixteen lanes side by side hold four channels each, sixteen row groups of a
-// workgroup hold `own` consecutive rows each.  A thread walks its rows and the
-// three behind them, whose dz reach back into its rows, four rows at a time
-// with the next four already loading; the rows around its own come from the
-// caches, where the neighbouring row groups read them too.  Walking down, row
-// t completes dX of row t-3 and adds to the three after it, so seen from row
-// t there are three open sums.  The rows before a sequence's first are its
-// window: their sums are d_window0, and where a sequence ends the open sums
-// are the rows of its rolled window, where d_window joins.
-#include <type_traits>
-
+// A wave walks a strip of `own` rows by 256 channels, a lane four of them, and
+// the three rows behind the strip, whose dz reach back into it: four rows at a
+// time with the next four already loading.  Everything about a row is uniform
+// over the wave, and a row's piece is 512 consecutive bytes in bf16 (a copy
+// runs at 5.5 TB/s in such pieces here, at 4.7 in pieces of 128).  The rows
+// around a strip come from the caches, where the neighbouring waves read them
+// too.  Walking down, row t completes dX of row t-3 and adds to the three
+// after it, so seen from row t there are three open sums.  The rows before a
+// sequence's first are its window: their sums are d_window0, and where a
+// sequence ends the open sums are the rows of its rolled window, where
+// d_window joins.
 #include "gdnt_device.hpp"
 
 namespace gdnt {
 
-constexpr int kConvThreads = 256;
-constexpr int kConvWaves = kConvThreads / 64;
-constexpr int kConvGroups = kConvThreads / 16;
+constexpr int kConvThreads = kConvWaves * 64;
+
+// The rows of one tensor around a wave's strip; row k counts from the strip's
+// first, from -3 on.  VEC: a buffer descriptor, a scalar offset for the row.
+template <typename T, bool VEC> struct Strip {
+    __amdgpu_buffer_rsrc_t rs;
+    uint32_t row, at;  // bytes
+    T* p;
+    int64_t stride;
+    __device__ __forceinline__ Strip(const void* base, int64_t stride_, int64_t n_rows, int64_t r0, int32_t C,
+                                     int64_t col, int lane)
+        : row((uint32_t)stride_ * (uint32_t)sizeof(T)), at(lane * 4 * (uint32_t)sizeof(T)),
+          p(static_cast<T*>(const_cast<void*>(base)) + (r0 - 3) * stride_ + col), stride(stride_) {
+        if constexpr (VEC) {
+            int64_t bytes = ((n_rows - 1 - (r0 - 3)) * stride_ + C - col) * (int64_t)sizeof(T);
+            bytes = bytes < 0 ? 0 : bytes > 0xfffffffcll ? 0xfffffffcll : bytes;
+            rs = __builtin_amdgcn_make_buffer_rsrc(p, 0, (uint32_t)bytes, 0x00020000);
+        } else {
+            p += lane * 4;
+        }
+    }
+    __device__ __forceinline__ Raw4<T> load(int k, int nc) const {
+        Raw4<T> v;
+        if constexpr (VEC) {
+            if constexpr (sizeof(T) == 2) v.v = __builtin_bit_cast(uint2, __builtin_amdgcn_raw_buffer_load_b64(rs, at, (uint32_t)(k + 3) * row, 0));
+            else v.v = __builtin_bit_cast(float4, __builtin_amdgcn_raw_buffer_load_b128(rs, at, (uint32_t)(k + 3) * row, 0));
+        } else {
+            v = load4<T, false>(p + (k + 3) * stride, nc);
+        }
+        return v;
+    }
+    __device__ __forceinline__ void store(int k, int nc, const float (&f)[4]) const {
+        if (nc == 0) return;
+        if constexpr (VEC) {
+            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+            typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+            if constexpr (sizeof(T) == 2) {
+                const u32x2 v = {gdn::f32x2_to_bf16x2(f[0], f[1]), gdn::f32x2_to_bf16x2(f[2], f[3])};
+                __builtin_amdgcn_raw_buffer_store_b64(v, rs, at, (uint32_t)(k + 3) * row, 0);
+            } else {
+                const u32x4 v = {__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3])};
+                __builtin_amdgcn_raw_buffer_store_b128(v, rs, at, (uint32_t)(k + 3) * row, 0);
+            }
+        } else {
+            store4<false>(p + (k + 3) * stride, f, nc);
+        }
+    }
+};
 
 template <typename T, typename YT> struct ConvRows {  // four rows as loaded
     Raw4<T> x[4];
@@ -29,26 +74,21 @@ template <typename T, typename YT> struct ConvRows {  // four rows as loaded
 
 template <typename T, typename YT, bool VEC>
 __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArgs A, int n_cols, int own) {
-    __shared__ float s_w[kConvWaves][4][kTileCols];
+    __shared__ float4 s_w[kConvWaves][4][64];
     const int64_t tile = blockIdx.x / n_cols;
     const int col = (int)(blockIdx.x % n_cols);
-    const int lane = threadIdx.x & 63, cl = threadIdx.x & 15, rg = threadIdx.x >> 4, wave = threadIdx.x >> 6;
-    const int64_t Cp = (int64_t)n_cols * kTileCols;
-    const int64_t r0 = (tile * kConvGroups + rg) * own, c0 = (int64_t)col * kTileCols + cl * 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t r0 = (tile * kConvWaves + wave) * own, cb = (int64_t)col * kConvCols, c0 = cb + lane * 4;
     const int64_t left = (int64_t)A.C - c0;
     const int nc = left >= 4 ? 4 : left > 0 ? (int)left : 0;
     const int64_t n_map = (A.n_rows + kTileRows - 1) / kTileRows * kTileRows;
 
     // bit k + 3 stands for row r0 + k, k = -3 .. own + 2 < 61: is it a
     // sequence's, and is it not the successor of the row above it
-    uint64_t in = 0, cut = 0;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const int64_t r = r0 - 3 + q * 16 + cl;
-        const int32_t m = r >= 0 && r < n_map ? A.map[r] : -1;
-        in |= ((__ballot(m >= 0) >> (lane & 48)) & 0xffffull) << (q * 16);
-        cut |= ((__ballot(m < 0 || (m & 1)) >> (lane & 48)) & 0xffffull) << (q * 16);
-    }
+    const int64_t rm = r0 - 3 + lane;
+    const int32_t m = rm >= 0 && rm < n_map ? A.map[rm] : -1;
+    const uint64_t in = __ballot(m >= 0), cut = __ballot(m < 0 || (m & 1));
+    auto seq_of = [&](int k) { return __builtin_amdgcn_readlane(m, k + 3) >> 2; };
 
     float wt[4][4], dw[4][4];  // [tap][channel]
 #pragma unroll
@@ -59,22 +99,8 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArg
             dw[j][i] = 0.0f;
         }
 
-    // Byte offsets from three rows above the workgroup's first: they fit 32 bits
-    // where VEC is set (the launcher's rule on strides), which leaves one add a row.
-    using Off = typename std::conditional<VEC, uint32_t, int64_t>::type;
-    const int64_t t0 = tile * kConvGroups * own - 3;
-    const int64_t cb = (int64_t)col * kTileCols;
-    const char* px = static_cast<const char*>(A.x) + (t0 * A.x_stride + cb) * (int64_t)sizeof(T);
-    const char* py = static_cast<const char*>(A.dy) + (t0 * A.dy_stride + cb) * (int64_t)sizeof(YT);
-    char* pdx = static_cast<char*>(A.dx) + (t0 * A.dx_stride + cb) * (int64_t)sizeof(T);
-    const Off sx = (Off)A.x_stride * (Off)sizeof(T), sy = (Off)A.dy_stride * (Off)sizeof(YT);
-    const Off sd = (Off)A.dx_stride * (Off)sizeof(T);
-    const Off row3 = (Off)(rg * own + 3);  // row r0 counted from t0
-    const Off cx = (Off)(cl * 4 * sizeof(T)), cy = (Off)(cl * 4 * sizeof(YT));
-    Off ox = row3 * sx + cx, oy = row3 * sy + cy, od = (row3 - 3) * sd + cx;  // rows to load, row to store
-    auto at_x = [&](Off o) { return reinterpret_cast<const T*>(px + o); };
-    auto at_y = [&](Off o) { return reinterpret_cast<const YT*>(py + o); };
-    auto at_dx = [&](Off o) { return reinterpret_cast<T*>(pdx + o); };
+    const Strip<T, VEC> Xs(A.x, A.x_stride, A.n_rows, r0, A.C, cb, lane), Ds(A.dx, A.dx_stride, A.n_rows, r0, A.C, cb, lane);
+    const Strip<YT, VEC> Ys(A.dy, A.dy_stride, A.n_rows, r0, A.C, cb, lane);
 
     auto has_init = [&](int seq) { return A.window && (A.has_init ? A.has_init[seq] != 0 : true); };
     auto window = [&](int seq, int row, float (&v)[4]) {
@@ -96,8 +122,8 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArg
         if (have == 15u && nc > 0) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                g.x[e] = load4<T, VEC>(at_x(ox + e * sx), nc);
-                g.y[e] = load4<YT, VEC>(at_y(oy + e * sy), nc);
+                g.x[e] = Xs.load(k + e, nc);
+                g.y[e] = Ys.load(k + e, nc);
             }
         } else {
 #pragma unroll
@@ -105,13 +131,11 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArg
                 g.x[e] = zero4<T>();
                 g.y[e] = zero4<YT>();
                 if ((have >> e & 1u) && nc > 0) {
-                    g.x[e] = load4<T, VEC>(at_x(ox + e * sx), nc);
-                    g.y[e] = load4<YT, VEC>(at_y(oy + e * sy), nc);
+                    g.x[e] = Xs.load(k + e, nc);
+                    g.y[e] = Ys.load(k + e, nc);
                 }
             }
         }
-        ox += 4 * sx;
-        oy += 4 * sy;
     };
 
     // X of the three rows before the current one and the open sums of the same rows
@@ -119,18 +143,18 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArg
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
         Raw4<T> v = zero4<T>();
-        if ((in >> j & 1) && nc > 0) v = load4<T, VEC>(at_x((row3 + j - 3) * sx + cx), nc);
+        if ((in >> j & 1) && nc > 0) v = Xs.load(j - 3, nc);
 #pragma unroll
         for (int i = 0; i < 4; ++i) X[j][i] = v.get(i);
     }
     if ((in >> 3 & 1) && !(cut >> 3 & 1) && (cut >> 1 & 3)) {  // a sequence begins one or two rows above r0
-        const int have = (cut >> 2 & 1) ? 1 : 2, seq = A.map[r0] >> 2;
+        const int have = (cut >> 2 & 1) ? 1 : 2, seq = seq_of(0);
 #pragma unroll
         for (int j = 0; j < 3; ++j)
             if (j < 3 - have) window(seq, j + have, X[j]);
     }
 
-    bool open = true;  // rows of this thread, or behind them with their sums open, are left
+    bool open = true;  // rows of this strip, or behind them with their sums open, are left
     auto rows4 = [&](const ConvRows<T, YT>& g, int k0) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -139,7 +163,7 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArg
             const uint32_t near = (uint32_t)(cut >> (k + 1)) & 7u;
             if (near & 4u) {
                 if (k > 0 && open && (in >> (k + 2) & 1)) {  // row k - 1 ended its sequence
-                    const int seq = A.map[r0 + k - 1] >> 2;
+                    const int seq = seq_of(k - 1);
                     // bit d: a sequence begins at row k - 1 - d
                     const uint32_t begins = ((near >> 1 & 1u) | (near << 1 & 2u));
                     const int rows = (begins & 1u) ? 1 : (begins & 2u) ? 2 : 3;  // of the sequence, 3: or more
@@ -153,8 +177,8 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArg
                                 if (i < nc) acc[j][i] += src[i];
                         }
                         if (j >= 3 - rows) {
-                            if (p >= 0 && p < own && nc > 0) store4<VEC>(at_dx((row3 + p) * sd + cx), acc[j], nc);
-                        } else if (k - rows >= 0) {  // the sequence begins in this thread's rows
+                            if (p >= 0 && p < own) Ds.store(p, nc, acc[j]);
+                        } else if (k - rows >= 0) {  // the sequence begins in this strip
                             put_window(seq, rows + j, acc[j]);
                         }
                     }
@@ -163,9 +187,9 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArg
                 for (int j = 0; j < 3; ++j)
 #pragma unroll
                     for (int i = 0; i < 4; ++i) acc[j][i] = 0.0f;
-                open = open && k < own;  // the rest is the next thread's
+                open = open && k < own;  // the rest is the next strip's
                 const bool begins = open && (in >> (k + 3) & 1);
-                const int seq = begins ? A.map[r0 + k] >> 2 : 0;
+                const int seq = begins ? seq_of(k) : 0;
 #pragma unroll
                 for (int j = 0; j < 3; ++j) {
                     if (begins) window(seq, j, X[j]);
@@ -195,12 +219,11 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArg
                 X[0][i] = X[1][i]; X[1][i] = X[2][i]; X[2][i] = x0;
             }
             if (near == 0) {
-                if (k >= 3 && open && nc > 0) store4<VEC>(at_dx(od), out, nc);
+                if (k >= 3 && open) Ds.store(k - 3, nc, out);
             } else if (open && (in >> (k + 3) & 1)) {
                 const int t = (near & 4u) ? 0 : (near & 2u) ? 1 : 2;  // row of its sequence: completes window row t
-                if (k - t >= 0) put_window(A.map[r0 + k] >> 2, t, out);
+                if (k - t >= 0) put_window(seq_of(k), t, out);
             }
-            od += sd;
         }
     };
     // two buffers that change roles; own + 3 is a multiple of 4
@@ -213,34 +236,25 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArg
         if (k0 + 8 < own + 3) load(ga, k0 + 8);
         rows4(gb, k0 + 4);
     }
-    // d_conv_w over the workgroup's rows: lanes, then waves
+    // d_conv_w over the workgroup's strips
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float v = dw[j][i];
-            v += __shfl_xor(v, 16);
-            v += __shfl_xor(v, 32);
-            if (lane < 16) s_w[wave][j][cl * 4 + i] = v;
-        }
+    for (int j = 0; j < 4; ++j) s_w[wave][j][lane] = make_float4(dw[j][0], dw[j][1], dw[j][2], dw[j][3]);
     __syncthreads();
-    const int j = threadIdx.x >> 6, ch = lane;  // 4 taps by 64 channels
-    A.part[(tile * 4 + j) * Cp + (int64_t)col * kTileCols + ch] =
-        (s_w[0][j][ch] + s_w[1][j][ch]) + (s_w[2][j][ch] + s_w[3][j][ch]);
-}
-
-static int conv_rows(int64_t n_rows, int64_t C) {
-    const int64_t nc = padded_channels(C) / kTileCols;
-    return (n_rows + kConvGroups * 57 - 1) / (kConvGroups * 57) * nc >= 1024 ? 57 : 13;
+    const int64_t Cp = padded_channels(A.C);
+    if (c0 < Cp) {  // tap `wave`
+        const float4 p = s_w[0][wave][lane], q = s_w[1][wave][lane], r = s_w[2][wave][lane], s = s_w[3][wave][lane];
+        *reinterpret_cast<float4*>(A.part + (tile * 4 + wave) * Cp + c0) =
+            make_float4((p.x + q.x) + (r.x + s.x), (p.y + q.y) + (r.y + s.y), (p.z + q.z) + (r.z + s.z),
+                        (p.w + q.w) + (r.w + s.w));
+    }
 }
 
 template <typename T, typename YT, bool VEC> static hipError_t conv_t(const ConvBwdArgs& a, hipStream_t s) {
-    const int nc = (int)(padded_channels(a.C) / kTileCols);
-    // VEC addresses a workgroup's rows (16 * 57 + 6 at most) by 32-bit byte offsets
-    if (VEC && (a.x_stride | a.dy_stride | a.dx_stride) >> 20) return conv_t<T, YT, false>(a, s);
-    // 57 rows a thread where that leaves work for every compute unit, else 13
+    const int nc = (int)((a.C + kConvCols - 1) / kConvCols);
+    // VEC addresses a strip's rows (at most 63) by 32-bit byte offsets
+    if (VEC && (a.x_stride | a.dy_stride | a.dx_stride) >> 24) return conv_t<T, YT, false>(a, s);
     const int own = conv_rows(a.n_rows, a.C);
-    const int64_t nt = (a.n_rows + kConvGroups * own - 1) / (kConvGroups * own), grid = nt * nc;
+    const int64_t nt = conv_tiles(a.n_rows, a.C), grid = nt * nc;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
     if (grid > 0)
         hipLaunchKernelGGL((k_conv_backward<T, YT, VEC>), dim3((unsigned)grid), dim3(kConvThreads), 0, s, a, nc, own);

@@ -69,8 +69,23 @@ struct ConvBwdArgs {
 inline int64_t n_tiles(int64_t n_rows) { return (n_rows + kTileRows - 1) / kTileRows; }
 __host__ __device__ inline int64_t padded_channels(int64_t C) { return (C + kTileCols - 1) / kTileCols * kTileCols; }
 
-// Partial sums of d_conv_w: a tile of k_conv_backward has at least 16 * 13 rows.
-inline int64_t conv_tiles_max(int64_t n_rows) { return (n_rows + 16 * 13 - 1) / (16 * 13); }
+// k_conv_backward: four strips to a workgroup, 256 channels wide.
+constexpr int kConvWaves = 4;
+constexpr int kConvCols = 256;
+// Rows of a strip: the most that leaves every SIMD four waves to choose from.
+// A strip reads six rows beside its own and computes three twice, so long
+// strips cost least (5% at 57, 60% at 5), but few of them are walked one
+// after the other while most of the card waits.
+inline int conv_rows(int64_t n_rows, int64_t C) {
+    const int64_t nc = (C + kConvCols - 1) / kConvCols;
+    for (int own : {57, 25, 13})
+        if ((n_rows + own - 1) / own * nc >= 4096) return own;
+    return 5;
+}
+inline int64_t conv_tiles(int64_t n_rows, int64_t C) {
+    const int64_t rows = kConvWaves * conv_rows(n_rows, C);
+    return (n_rows + rows - 1) / rows;
+}
 
 hipError_t launch_map(const MapArgs& a, hipStream_t s);
 hipError_t launch_scan_rows(const ScanArgs& a, hipStream_t s);
