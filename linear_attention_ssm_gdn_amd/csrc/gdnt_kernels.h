@@ -72,15 +72,16 @@ __host__ __device__ inline int64_t padded_channels(int64_t C) { return (C + kTil
 // k_conv_backward: four strips to a workgroup, 256 channels wide.
 constexpr int kConvWaves = 4;
 constexpr int kConvCols = 256;
-// Rows of a strip: the most that leaves every SIMD four waves to choose from.
-// A strip reads six rows beside its own and computes three twice, so long
-// strips cost least (5% at 57, 60% at 5), but few of them are walked one
-// after the other while most of the card waits.
+// Rows of a strip.  A strip reads six rows beside its own and computes three
+// twice, so long strips cost least where there are enough of them, and the
+// rows of one are walked one after the other: 57, 25, 13 rows take 374, 398,
+// 474 us over 32768 x 8192 channels (18400 strips of 57), 55, 47, 54 us over
+// 2159 x 8192 (1216, 2784, 5344 strips) and 54, 39, 31 us over 2066 x 672.
 inline int conv_rows(int64_t n_rows, int64_t C) {
     const int64_t nc = (C + kConvCols - 1) / kConvCols;
-    for (int own : {57, 25, 13})
-        if ((n_rows + own - 1) / own * nc >= 4096) return own;
-    return 5;
+    for (int own : {57, 25})
+        if ((n_rows + own - 1) / own * nc >= 2048) return own;
+    return 13;
 }
 inline int64_t conv_tiles(int64_t n_rows, int64_t C) {
     const int64_t rows = kConvWaves * conv_rows(n_rows, C);

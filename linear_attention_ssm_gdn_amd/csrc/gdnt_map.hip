@@ -101,19 +101,23 @@ hipError_t launch_map(const MapArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// 64 channels by 4 groups of tiles to a workgroup; fp64, every order fixed.
-__global__ __launch_bounds__(256) void k_sum_tiles(const float* part, int64_t n_tiles, int32_t C, int64_t Cp,
-                                                   int n_out, float* out0, float* out1) {
-    __shared__ double sum[4][64];
+// 64 channels by 16 groups of tiles to a workgroup; fp64, every order fixed.
+constexpr int kSumGroups = 16;
+__global__ __launch_bounds__(kSumGroups * 64) void k_sum_tiles(const float* part, int64_t n_tiles, int32_t C, int64_t Cp,
+                                                               int n_out, float* out0, float* out1) {
+    __shared__ double sum[kSumGroups][64];
     const int lane = threadIdx.x & 63, group = threadIdx.x >> 6;
     const int64_t c = (int64_t)blockIdx.x * 64 + lane;  // < Cp
     const int j = blockIdx.y;
     double acc = 0.0;
-    for (int64_t t = group; t < n_tiles; t += 4) acc += (double)part[(t * n_out + j) * Cp + c];
+#pragma unroll 4
+    for (int64_t t = group; t < n_tiles; t += kSumGroups) acc += (double)part[(t * n_out + j) * Cp + c];
     sum[group][lane] = acc;
     __syncthreads();
     if (group == 0 && c < C) {
-        const float v = (float)((sum[0][lane] + sum[1][lane]) + (sum[2][lane] + sum[3][lane]));
+#pragma unroll
+        for (int g = 1; g < kSumGroups; ++g) acc += sum[g][lane];
+        const float v = (float)acc;
         if (out1) (j == 0 ? out0 : out1)[c] = v;
         else out0[c * n_out + j] = v;
     }
@@ -122,7 +126,7 @@ __global__ __launch_bounds__(256) void k_sum_tiles(const float* part, int64_t n_
 hipError_t launch_sum_tiles(const float* part, int64_t n_tiles, int32_t C, int n_out, float* out0, float* out1,
                             hipStream_t s) {
     const int64_t Cp = padded_channels(C);
-    hipLaunchKernelGGL(k_sum_tiles, dim3((unsigned)(Cp / 64), (unsigned)n_out), dim3(256), 0, s, part, n_tiles, C, Cp,
+    hipLaunchKernelGGL(k_sum_tiles, dim3((unsigned)(Cp / 64), (unsigned)n_out), dim3(kSumGroups * 64), 0, s, part, n_tiles, C, Cp,
                        n_out, out0, out1);
     return hipGetLastError();
 }
