@@ -210,6 +210,9 @@ GDN_EXPORT int32_t gdnt_scan_backward(const gdnt_scan_dims* dims, const gdnt_sca
     A.vec2 = C > 1 && rows_dword(dh, dh_stride, dt) && rows_dword(dx, dx_stride, dt) &&
              rows_dword(da, dab_stride, dt) && rows_dword(db, dab_stride, dt) &&
              (ckpt || (rows_dword(x, x_stride, dt) && rows_dword(a, ab_stride, dt) && rows_dword(b, ab_stride, dt)));
+    auto on16 = [&](const void* p, int64_t stride) { return stride * elem_size(dt) % 16 == 0 && aligned(p, 16); };
+    A.vec8 = C % 8 == 0 && on16(dh, dh_stride) &&
+             (ckpt || (on16(x, x_stride) && on16(a, ab_stride) && on16(b, ab_stride)));
     return from_hip(gdnt::launch_scan_backward(A, (hipStream_t)stream));
 }
 

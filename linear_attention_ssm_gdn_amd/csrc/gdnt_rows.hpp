@@ -55,6 +55,8 @@ template <typename T, bool VEC> struct WaveRows {
                                         int64_t col, int64_t lane_at)
         : row((uint32_t)stride_ * (uint32_t)sizeof(T)), at((uint32_t)lane_at * (uint32_t)sizeof(T)),
           p(static_cast<T*>(const_cast<void*>(base)) + first * stride_ + col), stride(stride_) {
+        // where rows are walked tile after tile, keeps the rows' offsets from being held in registers
+        asm volatile("" : "+s"(row));
         if constexpr (VEC) {
             // up to the tensor's last element's dword
             int64_t bytes = (((n_rows - 1 - first) * stride_ + C - col) * (int64_t)sizeof(T) + 3) & ~3ll;

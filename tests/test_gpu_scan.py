@@ -30,6 +30,25 @@ def test_forward_and_backward(lens, C, act, state):
     check_grads(c, c.backward(saved), ora)
 
 
+@pytest.mark.parametrize("ckpt", [False, True])
+@pytest.mark.parametrize("C", [8, 72, 200, 328])
+def test_backward_of_many_tiles(C, ckpt):
+    """bf16 rows on 16 bytes and channels a multiple of 8: tiles whose rows are loaded ahead, between ones that are
+    not (a sequence's end inside), in columns that end before their 64 channels."""
+    c = Case([700, 1, 0, 513, 255, 90, 2000, 3], C, "bf16", "f32", tail=40, seed=C)
+    saved = c.saved(ckpt=ckpt)
+    h, _, so = c.forward(saved)
+    check_forward(c, h, so, ora)
+    if not ckpt:
+        check_grads(c, c.backward(saved), ora)
+        return
+    v, _, _ = decode(c, saved)
+    with np.errstate(invalid="ignore"):
+        before = ora.scan(c.f64("x"), c.f64("a"), c.f64("b"), c.a_log, c.dt_bias, c.spans, c.seq_h0())[2]
+        rb = ora.rebuilt(v[0], v[1], v[2], c.a_log, c.dt_bias, c.spans, before)
+    check_grads(c, c.backward(saved, from_ckpt=True), ora, x=v[0], a=v[1], b=v[2], before=rb)
+
+
 @pytest.mark.parametrize("act,state", [("bf16", "bf16"), ("f32", "f32")])
 def test_other_types_padding_gaps_tails_and_strides(act, state):
     """Padding sequences (their rows NaN: unread), rows before the first and behind the last sequence, padded rows
