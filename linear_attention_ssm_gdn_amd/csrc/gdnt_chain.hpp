@@ -2,7 +2,7 @@
 //
 // Tiles are handed out by a ticket in the order of the recurrence, so a tile
 // only ever waits for tiles that already run: every wait ends.  A tile first
-// publishes its run (h -> a h + u), then looks back over up to eight tiles
+// publishes its run (h -> a h + u), then looks back over up to four tiles
 // for the nearest one whose end state is known, applies the runs in between
 // in order, and publishes its own end state.  The order makes the bits the
 // same whichever tile the state was found at.  A value and its ready mark
@@ -31,7 +31,7 @@ struct Chain {
     uint64_t* state;  // {1, end state}
     int64_t run;      // as many words further: {a with its sign bit set, u}, a > 0
 };
-constexpr int kLookBack = 8;
+constexpr int kLookBack = 4;
 constexpr int kSpins = 1 << 21;  // some seconds, far beyond any tile's run
 
 __device__ __forceinline__ uint64_t chain_load(const uint64_t* p) {
@@ -43,58 +43,48 @@ __device__ __forceinline__ void chain_store(uint64_t* p, uint32_t hi, float lo) 
 }
 
 // One wave, NCH channels a lane from word `at` on; `step` words to the tile
-// before, of which n_pred exist.  The state before the tile, into h.
+// before, of which n_pred exist.  The state before the tile, into h.  Every
+// poll asks for all words at once: a trip to memory costs as much as a walk.
 template <int NCH>
 __device__ __forceinline__ void look_back(const Chain& C, int64_t at, int64_t step, int64_t n_pred, float (&h)[NCH],
                                           int32_t* err) {
-    const int lane = threadIdx.x & 63, j = (lane & 7) + 1;
-    // first the column's first channel alone, for all eight tiles
-    int found = -1;
+    const uint64_t* p = C.state + at + (threadIdx.x & 63) * NCH;
     for (int spin = 0; spin < kSpins; ++spin) {
-        uint64_t v = 0;
-        if (lane < 2 * kLookBack && j <= n_pred) v = chain_load(C.state + (lane & 8 ? C.run : 0) + at + j * step);
-        const uint64_t ready = __ballot((v >> 32) != 0);
-        const uint32_t states = (uint32_t)ready & 0xffu, runs = (uint32_t)(ready >> 8) & 0xffu;
-        if (states) {
-            const int k = __builtin_ctz(states);
-            if (!(~runs & ((1u << k) - 1u))) {
-                found = k;
-                break;
-            }
-        }
-        __builtin_amdgcn_s_sleep(2);
-    }
-    if (found >= 0) {
-        for (int spin = 0; spin < kSpins; ++spin) {
-            uint64_t s[NCH], g[kLookBack - 1][NCH];
-            const int64_t mine = at + lane * NCH;
-            bool ok = true;
+        uint64_t s[kLookBack][NCH], g[kLookBack][NCH];
 #pragma unroll
-            for (int i = 0; i < NCH; ++i) s[i] = chain_load(C.state + mine + (found + 1) * step + i);
-#pragma unroll
-            for (int q = 0; q < kLookBack - 1; ++q)
-                if (q < found) {
-#pragma unroll
-                    for (int i = 0; i < NCH; ++i) g[q][i] = chain_load(C.state + C.run + mine + (q + 1) * step + i);
-                }
+        for (int q = 0; q < kLookBack; ++q)
 #pragma unroll
             for (int i = 0; i < NCH; ++i) {
-                ok = ok && (s[i] >> 32) != 0;
-                h[i] = __uint_as_float((uint32_t)s[i]);
+                s[q][i] = q < n_pred ? chain_load(p + (q + 1) * step + i) : 0;
+                g[q][i] = q < n_pred && q < kLookBack - 1 ? chain_load(p + C.run + (q + 1) * step + i) : 0;
             }
+        // the nearest known state with every run behind it known, in all channels
+        int found = -1;
+        bool runs = true;
 #pragma unroll
-            for (int q = kLookBack - 2; q >= 0; --q)
-                if (q < found) {
+        for (int q = 0; q < kLookBack; ++q) {
+            bool ready = true, run = true;
 #pragma unroll
-                    for (int i = 0; i < NCH; ++i) {
-                        ok = ok && (g[q][i] >> 32) != 0;
+            for (int i = 0; i < NCH; ++i) {
+                ready = ready && (s[q][i] >> 32) != 0;
+                run = run && (g[q][i] >> 32) != 0;
+            }
+            if (found < 0 && runs && __all(ready)) found = q;
+            runs = runs && __all(run);
+        }
+        if (found >= 0) {
+#pragma unroll
+            for (int q = kLookBack - 1; q >= 0; --q)
+#pragma unroll
+                for (int i = 0; i < NCH; ++i) {
+                    if (q == found) h[i] = __uint_as_float((uint32_t)s[q][i]);
+                    else if (q < found)
                         h[i] = fmaf(__uint_as_float((uint32_t)(g[q][i] >> 32) & 0x7fffffffu), h[i],
                                     __uint_as_float((uint32_t)g[q][i]));
-                    }
                 }
-            if (__all(ok)) return;
-            __builtin_amdgcn_s_sleep(1);
+            return;
         }
+        __builtin_amdgcn_s_sleep(2);
     }
     raise(err, GDNT_DEVERR_TIMEOUT);
 #pragma unroll
@@ -106,14 +96,14 @@ __device__ __forceinline__ void look_back(const Chain& C, int64_t at, int64_t st
 template <int NCH>
 __device__ __forceinline__ void hand_on(const Chain& C, int64_t at, int64_t step, int64_t n_pred, bool cont, bool next,
                                         const float (&a)[NCH], const float (&u)[NCH], float (&h)[NCH], int32_t* err) {
-    const int64_t mine = at + (threadIdx.x & 63) * NCH;
+    uint64_t* mine = C.state + at + (threadIdx.x & 63) * NCH;
     // a tile with a first row in it, or that continues nothing, knows its end
     const bool known = a[0] < 0.0f || !cont;  // the same in every channel
     if (next) {
 #pragma unroll
         for (int i = 0; i < NCH; ++i) {
-            if (known) chain_store(C.state + mine + i, 1u, u[i]);
-            else chain_store(C.state + C.run + mine + i, __float_as_uint(a[i]) | 0x80000000u, u[i]);
+            if (known) chain_store(mine + i, 1u, u[i]);
+            else chain_store(mine + C.run + i, __float_as_uint(a[i]) | 0x80000000u, u[i]);
         }
     }
 #pragma unroll
@@ -121,7 +111,7 @@ __device__ __forceinline__ void hand_on(const Chain& C, int64_t at, int64_t step
     if (cont) look_back<NCH>(C, at, step, n_pred, h, err);
     if (next && !known) {
 #pragma unroll
-        for (int i = 0; i < NCH; ++i) chain_store(C.state + mine + i, 1u, fmaf(a[i], h[i], u[i]));
+        for (int i = 0; i < NCH; ++i) chain_store(mine + i, 1u, fmaf(a[i], h[i], u[i]));
     }
 }
 
