@@ -91,25 +91,33 @@ __device__ __forceinline__ void look_back(const Chain& C, int64_t at, int64_t st
     for (int i = 0; i < NCH; ++i) h[i] = 0.0f;
 }
 
-// One wave: from the tile's run (a, u) the state before it, into h (0 where
-// nothing continues into it); the tile after it, where one continues, is told.
+// A tile with a first row in it, or that continues nothing, knows its end from
+// its run alone (the same in every channel).
+template <int NCH> __device__ __forceinline__ bool end_known(const float (&a)[NCH], bool cont) {
+    return a[0] < 0.0f || !cont;
+}
+// One wave tells the tile after it, if one continues, its run or known end.
+template <int NCH>
+__device__ __forceinline__ void tell_run(const Chain& C, int64_t at, bool cont, bool next, const float (&a)[NCH],
+                                         const float (&u)[NCH]) {
+    uint64_t* mine = C.state + at + (threadIdx.x & 63) * NCH;
+    if (!next) return;
+#pragma unroll
+    for (int i = 0; i < NCH; ++i) {
+        if (end_known(a, cont)) chain_store(mine + i, 1u, u[i]);
+        else chain_store(mine + C.run + i, __float_as_uint(a[i]) | 0x80000000u, u[i]);
+    }
+}
+// The same wave, later: the state before the tile into h (0 where nothing
+// continues into it), and the tile's end to the tile after it.
 template <int NCH>
 __device__ __forceinline__ void hand_on(const Chain& C, int64_t at, int64_t step, int64_t n_pred, bool cont, bool next,
                                         const float (&a)[NCH], const float (&u)[NCH], float (&h)[NCH], int32_t* err) {
     uint64_t* mine = C.state + at + (threadIdx.x & 63) * NCH;
-    // a tile with a first row in it, or that continues nothing, knows its end
-    const bool known = a[0] < 0.0f || !cont;  // the same in every channel
-    if (next) {
-#pragma unroll
-        for (int i = 0; i < NCH; ++i) {
-            if (known) chain_store(mine + i, 1u, u[i]);
-            else chain_store(mine + C.run + i, __float_as_uint(a[i]) | 0x80000000u, u[i]);
-        }
-    }
 #pragma unroll
     for (int i = 0; i < NCH; ++i) h[i] = 0.0f;
     if (cont) look_back<NCH>(C, at, step, n_pred, h, err);
-    if (next && !known) {
+    if (next && !end_known(a, cont)) {
 #pragma unroll
         for (int i = 0; i < NCH; ++i) chain_store(mine + i, 1u, fmaf(a[i], h[i], u[i]));
     }

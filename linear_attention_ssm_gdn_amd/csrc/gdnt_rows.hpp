@@ -51,10 +51,12 @@ template <typename T, bool VEC> struct WaveRows {
     uint32_t row, at;  // bytes
     T* p;
     int64_t stride;
+    bool odd;  // uniform: a lane here has one channel
     __device__ __forceinline__ WaveRows(const void* base, int64_t stride_, int64_t n_rows, int64_t first, int32_t C,
                                         int64_t col, int64_t lane_at)
         : row((uint32_t)stride_ * (uint32_t)sizeof(T)), at((uint32_t)lane_at * (uint32_t)sizeof(T)),
-          p(static_cast<T*>(const_cast<void*>(base)) + first * stride_ + col), stride(stride_) {
+          p(static_cast<T*>(const_cast<void*>(base)) + first * stride_ + col), stride(stride_),
+          odd((C & 1) && C - col < 128) {
         // where rows are walked tile after tile, keeps the rows' offsets from being held in registers
         asm volatile("" : "+s"(row));
         if constexpr (VEC) {
@@ -70,7 +72,7 @@ template <typename T, bool VEC> struct WaveRows {
         Raw2<T> v;
         if constexpr (VEC) {
             if constexpr (sizeof(T) == 2) v.v = __builtin_amdgcn_raw_buffer_load_b32(rs, at, r * row, 0);
-            else v.v = __builtin_bit_cast(float2, __builtin_amdgcn_raw_buffer_load_b64(rs, nc == 1 ? at - 4 : at, r * row, 0));
+            else v.v = __builtin_bit_cast(float2, __builtin_amdgcn_raw_buffer_load_b64(rs, odd && nc == 1 ? at - 4 : at, r * row, 0));
         } else {
             T e[2] = {T(0), T(0)};
             if (nc > 0) e[0] = p[r * stride];
@@ -84,12 +86,12 @@ template <typename T, bool VEC> struct WaveRows {
             if constexpr (sizeof(T) == 2) {
                 const uint32_t v = gdn::f32x2_to_bf16x2(a, b);
                 if (nc == 2) __builtin_amdgcn_raw_buffer_store_b32(v, rs, at, r * row, 0);
-                else if (nc == 1) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)v, rs, at, r * row, 0);
+                if (odd && nc == 1) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)v, rs, at, r * row, 0);
             } else {
                 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
                 const u32x2 v = {__float_as_uint(a), __float_as_uint(b)};
                 if (nc == 2) __builtin_amdgcn_raw_buffer_store_b64(v, rs, at, r * row, 0);
-                else if (nc == 1) __builtin_amdgcn_raw_buffer_store_b32(v.x, rs, at, r * row, 0);
+                if (odd && nc == 1) __builtin_amdgcn_raw_buffer_store_b32(v.x, rs, at, r * row, 0);
             }
         } else {
             if (nc > 0) p[r * stride] = from_f32<T>(a);

@@ -165,9 +165,11 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void k_scan_forwa
         const bool cont = (in & ~firsts) & 1u;
         const int64_t Cw = (int64_t)n_cols * kFwdCols;
         const Chain chain{A.chain, n_tiles * Cw};
+        const int64_t at = tile * Cw + (int64_t)col * kFwdCols;
+        const bool next = m_next >= 0 && !(m_next & 1);
         float h[2];
-        hand_on<2>(chain, tile * Cw + (int64_t)col * kFwdCols, -Cw, tile, cont, m_next >= 0 && !(m_next & 1), ta, tu,
-                   h, A.err);
+        tell_run<2>(chain, at, cont, next, ta, tu);
+        hand_on<2>(chain, at, -Cw, tile, cont, next, ta, tu, h, A.err);
         s_h[lane] = make_float2(h[0], h[1]);
         if (A.states && cont && r0 % kTileRows == 0) {
 #pragma unroll
@@ -187,7 +189,7 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void k_scan_forwa
         h[0] = fmaf(al[r][0], h[0], u[r][0]);
         h[1] = fmaf(al[r][1], h[1], u[r][1]);
         if (firsts >> r & 1u) { h[0] = u[r][0]; h[1] = u[r][1]; }
-        if ((in >> r & 1u) && nc > 0) H.store(r, nc, h[0], h[1]);
+        if (in >> r & 1u) H.store(r, nc, h[0], h[1]);
         if (lasts >> r & 1u) {
             const int64_t at = (int64_t)A.page_idx[seq_of(r)] * A.st_out_stride + c0;
 #pragma unroll

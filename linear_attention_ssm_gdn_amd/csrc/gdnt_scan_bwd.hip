@@ -113,10 +113,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
     const uint32_t stage_lds = __builtin_amdgcn_readfirstlane(
         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)stage);
 
-    // What is drawn ahead of a tile: its row map, its parameters, its rows.
+    // What is drawn ahead of a tile: its row map and its parameters (ask), its rows (fetch).
     int32_t m32 = -1;
     float dt[2] = {}, al_log[2] = {};
-    auto draw = [&](uint32_t ticket) {
+    auto ask = [&](uint32_t ticket) {
         const int lane = fresh_lane(lane0), half = lane >> 5, hl = lane & 31;
         const int64_t tile = n_tiles - 1 - ticket / (uint32_t)n_cols;
         const int64_t cb = (int64_t)(ticket % (uint32_t)n_cols) * kTileCols, c0 = cb + hl * 2;
@@ -128,7 +128,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
             dt[i] = have ? A.dt_bias[c0 + i] : 0.0f;
             al_log[i] = have ? A.a_log[c0 + i] : 0.0f;
         }
+    };
+    auto fetch = [&](uint32_t ticket) {
         if constexpr (PIPE) {
+            const int lane = fresh_lane(lane0), half = lane >> 5, hl = lane & 31;
+            const int64_t tile = n_tiles - 1 - ticket / (uint32_t)n_cols;
+            const int64_t cb = (int64_t)(ticket % (uint32_t)n_cols) * kTileCols;
+            const int64_t r0 = tile * kTileRows + wave * 2 * FR;
             if ((uint32_t)__ballot(m32 >= 0) != 0xffffffffu) return;  // such a wave loads for itself
             stage_free();
             // lanes beyond the last channel read the column's first ones
@@ -167,7 +173,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
     __syncthreads();
     uint32_t ticket = __builtin_amdgcn_readfirstlane(s_ticket);
     __syncthreads();
-    if (ticket < total) draw(ticket);
+    if (ticket < total) {
+        ask(ticket);
+        fetch(ticket);
+    }
     while (ticket < total) {
         const int lane = fresh_lane(lane0), half = lane >> 5, hl = lane & 31;
         const int64_t tile = n_tiles - 1 - ticket / (uint32_t)n_cols;
@@ -347,51 +356,54 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
         float h[2] = {};
         const int32_t* map = rare_args()->map + tile * kTileRows;
         const int32_t m_first = map[0];
-        if (m_first >= 0 && !(m_first & 1)) {
+        const bool cont = m_first >= 0 && !(m_first & 1);
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (i < nc) h[i] = rare_args()->states[tile * A.C + c0 + i];
-        }
-        again(h[0]); again(h[1]);  // loaded before the next tile's rows are asked for
-        if (wave != 0) {
-            if (ticket < total) draw(ticket);
-        } else {  // one channel a lane
-            const int32_t m_last = map[kTileRows - 1];
-            const int32_t m_prev = tile > 0 ? map[-1] : -1;
+        for (int i = 0; i < 2; ++i) h[i] = cont && i < nc ? rare_args()->states[tile * A.C + c0 + i] : 0.0f;
+        if (ticket < total) ask(ticket);
+        if (wave == 0) {  // one channel a lane
+            const auto* R = rare_args();
+            const Chain chain{R->chain, n_tiles * Cp};
+            const int32_t m_last = map[kTileRows - 1], m_prev = tile > 0 ? map[-1] : -1;
+            const bool behind = m_last >= 0 && !(m_last & 2), ahead = m_prev >= 0 && !(m_prev & 2);
+            float ta[1], tu[1];
             const float* pa = reinterpret_cast<const float*>(s_ra) + lane;
             const float* pu = reinterpret_cast<const float*>(s_ru) + lane;
-            float ta = pa[(kWaves - 1) * kTileCols], tu = pu[(kWaves - 1) * kTileCols];
+            ta[0] = pa[(kWaves - 1) * kTileCols];
+            tu[0] = pu[(kWaves - 1) * kTileCols];
 #pragma unroll
             for (int v = kWaves - 2; v >= 0; --v) {
                 float ja = pa[v * kTileCols], ju = pu[v * kTileCols];
-                join(ta, tu, ja, ju);
-                ta = ja; tu = ju;
+                join(ta[0], tu[0], ja, ju);
+                ta[0] = ja; tu[0] = ju;
             }
-            const auto* R = rare_args();
-            const Chain chain{R->chain, n_tiles * Cp};
-            const float a1[1] = {ta}, u1[1] = {tu};
-            float h1[1];
-            hand_on<1>(chain, tile * Cp + cb, Cp, n_tiles - 1 - tile, m_last >= 0 && !(m_last & 2),
-                       m_prev >= 0 && !(m_prev & 2), a1, u1, h1, R->err);
-            reinterpret_cast<float*>(s_h)[lane] = h1[0];
+            tell_run<1>(chain, tile * Cp + cb, behind, ahead, ta, tu);
+            float m1[1];
+            hand_on<1>(chain, tile * Cp + cb, Cp, n_tiles - 1 - tile, behind, ahead, ta, tu, m1, R->err);
+            reinterpret_cast<float*>(s_h)[lane] = m1[0];
+        } else {
+            again(h[0]); again(h[1]);  // arrived before the next tile's rows are asked for
+            if (ticket < total) fetch(ticket);
         }
         __syncthreads();
-        if (wave == 0 && ticket < total) draw(ticket);  // not before the state is handed on
+        if (wave == 0 && ticket < total) fetch(ticket);  // not before the state is handed on
         float mu[2] = {s_h[hl].x, s_h[hl].y};
-        for (int v = 0; v < wave; ++v) {
-            const float2 va = s_a[v][hl], vu = s_u[v][hl];
-            h[0] = walk(va.x, vu.x, h[0]);
-            h[1] = walk(va.y, vu.y, h[1]);
-        }
         for (int v = kWaves - 1; v > wave; --v) {
             const float2 va = s_ra[v][hl], vu = s_ru[v][hl];
             mu[0] = walk(va.x, vu.x, mu[0]);
             mu[1] = walk(va.y, vu.y, mu[1]);
         }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            if (half) h[i] = walk(xa[i], xu[i], h[i]);
-            else mu[i] = walk(ya[i], yu[i], mu[i]);
+        if (!half) {
+            mu[0] = walk(ya[0], yu[0], mu[0]);
+            mu[1] = walk(ya[1], yu[1], mu[1]);
+        }
+        for (int v = 0; v < wave; ++v) {
+            const float2 va = s_a[v][hl], vu = s_u[v][hl];
+            h[0] = walk(va.x, vu.x, h[0]);
+            h[1] = walk(va.y, vu.y, h[1]);
+        }
+        if (half) {
+            h[0] = walk(xa[0], xu[0], h[0]);
+            h[1] = walk(xa[1], xu[1], h[1]);
         }
         // second walk: the state before each row
 #pragma unroll
