@@ -24,6 +24,34 @@ __device__ bool valid_slow(const MapArgs& A, int s) {
     return false;
 }
 
+// The sequence that row r (< n_rows) is computed for, and its bounds; -1: none.
+__device__ int owner(const MapArgs& A, int64_t r, bool bad, int& c0, int& c1) {
+    int seq = -1;
+    if (!bad) {
+        int lo = 0, hi = A.n_seqs;  // the last s with cu[s] <= r, or -1
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if ((int64_t)A.cu[mid] <= r) lo = mid + 1;
+            else hi = mid;
+        }
+        seq = lo - 1;
+        if (seq >= 0 && (int64_t)A.cu[seq + 1] <= r) seq = -1;
+    } else {
+        int end = 0;
+        for (int s = 0; s < A.n_seqs; ++s) {
+            const int b0 = A.cu[s], b1 = A.cu[s + 1];
+            if (b0 < end || !bounds_ok(A, b0, b1)) continue;
+            if ((int64_t)b0 <= r && r < (int64_t)b1) { seq = s; break; }
+            end = b1;
+        }
+    }
+    if (seq < 0) return -1;
+    c0 = A.cu[seq];
+    c1 = A.cu[seq + 1];
+    const int page = A.page_idx[seq];
+    return page >= 0 && page < A.page_limit && (A.max_len == 0 || c1 - c0 <= A.max_len) ? seq : -1;
+}
+
 // One thread per row finds its sequence by bisection of cu_seqlens; every
 // workgroup first looks all of cu_seqlens over (n_seqs / 256 loads a thread)
 // and takes the slow scan where a bound is bad.  The first workgroup raises
@@ -39,34 +67,9 @@ __global__ __launch_bounds__(kMapThreads) void k_row_map(const MapArgs A) {
     bad = __syncthreads_or(bad) != 0;
 
     for (int64_t r = gid; r < A.n_map; r += stride) {
-        int seq = -1;
-        if (r < A.n_rows) {
-            if (!bad) {
-                int lo = 0, hi = A.n_seqs;  // the last s with cu[s] <= r, or -1
-                while (lo < hi) {
-                    const int mid = (lo + hi) >> 1;
-                    if ((int64_t)A.cu[mid] <= r) lo = mid + 1;
-                    else hi = mid;
-                }
-                seq = lo - 1;
-                if (seq >= 0 && (int64_t)A.cu[seq + 1] <= r) seq = -1;
-            } else {
-                int end = 0;
-                for (int s = 0; s < A.n_seqs; ++s) {
-                    const int c0 = A.cu[s], c1 = A.cu[s + 1];
-                    if (c0 < end || !bounds_ok(A, c0, c1)) continue;
-                    if ((int64_t)c0 <= r && r < (int64_t)c1) { seq = s; break; }
-                    end = c1;
-                }
-            }
-        }
-        int32_t m = -1;
-        if (seq >= 0) {
-            const int c0 = A.cu[seq], c1 = A.cu[seq + 1], page = A.page_idx[seq];
-            if (page >= 0 && page < A.page_limit && (A.max_len == 0 || c1 - c0 <= A.max_len))
-                m = seq * 4 + (r == (int64_t)c1 - 1 ? 2 : 0) + (r == (int64_t)c0 ? 1 : 0);
-        }
-        A.map[r] = m;
+        int c0, c1;
+        const int seq = r < A.n_rows ? owner(A, r, bad, c0, c1) : -1;
+        A.map[r] = seq < 0 ? -1 : seq * 4 + (r == (int64_t)c1 - 1 ? 2 : 0) + (r == (int64_t)c0 ? 1 : 0);
     }
 
     if (blockIdx.x == 0) {

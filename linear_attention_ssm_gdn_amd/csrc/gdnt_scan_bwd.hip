@@ -85,8 +85,9 @@ template <typename P> __device__ __forceinline__ P* scalar_ptr(P* p) {
 // A wave's place in LDS for its next rows: 4 KB for each bf16 tensor, line r
 // of 256 bytes being row r of the first half and row r of the second; of a
 // checkpoint 2 KB for each tensor, two lots of 16 bytes a lane, and the scales.
-constexpr int kStageRows = 4096, kStageCkpt = 2048 + 256;
-constexpr int stage_bytes(bool ckpt) { return ckpt ? kStageRows + 3 * kStageCkpt : 4 * kStageRows; }
+// In front of them, of the tile's 64 channels: dt_bias, A_log and the kept state.
+constexpr int kStageHead = 3 * 256, kStageRows = 4096, kStageCkpt = 2048 + 256;
+constexpr int stage_bytes(bool ckpt) { return kStageHead + (ckpt ? kStageRows + 3 * kStageCkpt : 4 * kStageRows); }
 
 // The kernel's arguments read again where they are used once in a while: kept
 // in registers all the time they would push others out.
@@ -113,39 +114,42 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
     const uint32_t stage_lds = __builtin_amdgcn_readfirstlane(
         (uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)stage);
 
-    // What is drawn ahead of a tile: its row map and its parameters (ask), its rows (fetch).
-    int32_t m32 = -1;
-    float dt[2] = {}, al_log[2] = {};
-    auto ask = [&](uint32_t ticket) {
-        const int lane = fresh_lane(lane0), half = lane >> 5, hl = lane & 31;
-        const int64_t tile = n_tiles - 1 - ticket / (uint32_t)n_cols;
-        const int64_t cb = (int64_t)(ticket % (uint32_t)n_cols) * kTileCols, c0 = cb + hl * 2;
-        const int64_t r0 = tile * kTileRows + wave * 2 * FR;
-        m32 = lane < 2 * FR ? A.map[r0 + lane] : -1;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const bool have = c0 + i < A.C;
-            dt[i] = have ? A.dt_bias[c0 + i] : 0.0f;
-            al_log[i] = have ? A.a_log[c0 + i] : 0.0f;
-        }
+    auto tile_of = [&](uint32_t ticket) -> int64_t {
+        return ticket < total ? n_tiles - 1 - ticket / (uint32_t)n_cols : 0;
     };
-    auto fetch = [&](uint32_t ticket) {
+    // The row map of the wave's 32 rows, a lane each; in lanes 32 to 34 that of
+    // the tile's last row, of the row before the tile, of its first row.
+    auto map_of = [&](int64_t tile) {
+        const int lane = fresh_lane(lane0);
+        const int32_t* map = A.map + tile * kTileRows;
+        int at = wave * 2 * FR + lane;
+        if (lane == 32) at = kTileRows - 1;
+        if (lane == 33) at = -1;
+        if (lane == 34) at = 0;
+        return lane < 35 && (at >= 0 || tile > 0) ? map[at] : -1;
+    };
+    auto whole_of = [&](int32_t m) { return (uint32_t)__ballot(m >= 0) == 0xffffffffu; };
+    // A tile's head and rows on their way into the stage; m: its row map.
+    auto fetch = [&](uint32_t ticket, int64_t tile, int32_t m) {
         if constexpr (PIPE) {
             const int lane = fresh_lane(lane0), half = lane >> 5, hl = lane & 31;
-            const int64_t tile = n_tiles - 1 - ticket / (uint32_t)n_cols;
             const int64_t cb = (int64_t)(ticket % (uint32_t)n_cols) * kTileCols;
             const int64_t r0 = tile * kTileRows + wave * 2 * FR;
-            if ((uint32_t)__ballot(m32 >= 0) != 0xffffffffu) return;  // such a wave loads for itself
             stage_free();
-            // lanes beyond the last channel read the column's first ones
+            const uint32_t c1 = (cb + lane < A.C ? lane : 0) * 4;  // lanes beyond the last channel: the column's first
+            stage4(scalar_ptr(A.dt_bias + cb), c1, stage_lds);
+            stage4(scalar_ptr(A.a_log + cb), c1, stage_lds + 256);
+            stage4(scalar_ptr(A.states + tile * A.C + cb), c1, stage_lds + 512);  // not used where nothing was kept
+            if (!whole_of(m)) return;  // such a wave loads its rows itself
             const uint32_t c8 = cb + (lane & 7) * 8 < A.C ? (lane & 7) * 8 : 0;
+            const uint32_t stage_rows = stage_lds + kStageHead;
             auto rows = [&](const void* base, int64_t stride, int slot) {
                 const T* p = scalar_ptr(static_cast<const T*>(base) + r0 * stride + cb);
                 const uint32_t row = fresh_scalar((uint32_t)stride * (uint32_t)sizeof(T));
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     stage16(p, ((lane >> 3 & 1) * FR + 4 * q + (lane >> 4)) * row + c8 * (uint32_t)sizeof(T),
-                            stage_lds + slot + q * 1024);
+                            stage_rows + slot + q * 1024);
             };
             if constexpr (CKPT) {
                 const int64_t n4 = Cp / 4;
@@ -155,13 +159,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
                     const char* p = scalar_ptr(reinterpret_cast<const char*>(A.q) + at * 64);
                     const float* s = scalar_ptr(A.q_scale + at);
                     const uint32_t block = (uint32_t)half * 3u * (uint32_t)n4 + (hl >> 1);
-                    const uint32_t slot = stage_lds + kStageRows + t * kStageCkpt;
+                    const uint32_t slot = stage_rows + kStageRows + t * kStageCkpt;
                     stage16(p, block * 64 + (hl & 1) * 32, slot);
                     stage16(p, block * 64 + (hl & 1) * 32 + 16, slot + 1024);
                     stage4(s, block * 4, slot + 2048);
                 }
             } else {
-                rows(A.a, A.ab_stride, 0 * kStageRows + kStageRows);
+                rows(A.a, A.ab_stride, 1 * kStageRows);
                 rows(A.b, A.ab_stride, 2 * kStageRows);
                 rows(A.x, A.x_stride, 3 * kStageRows);
             }
@@ -169,31 +173,48 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
         }
     };
 
+    // Tickets are drawn two ahead: by the time a tile's rows are asked for,
+    // its place and row map have long arrived.
     if (threadIdx.x == 0) s_ticket = atomicAdd(A.ticket, 1u);
     __syncthreads();
-    uint32_t ticket = __builtin_amdgcn_readfirstlane(s_ticket);
+    const uint32_t ticket0 = __builtin_amdgcn_readfirstlane(s_ticket);
     __syncthreads();
-    if (ticket < total) {
-        ask(ticket);
-        fetch(ticket);
+    uint32_t ticket = ticket0, ticket1 = total;
+    if constexpr (PIPE) {
+        if (threadIdx.x == 0) s_ticket = atomicAdd(A.ticket, 1u);
+        __syncthreads();
+        ticket1 = __builtin_amdgcn_readfirstlane(s_ticket);
+        __syncthreads();
     }
+    if (ticket >= total) return;
+    int64_t tile = tile_of(ticket), tile1 = tile_of(ticket1);
+    int32_t m_next = map_of(tile);
+    fetch(ticket, tile, m_next);
     while (ticket < total) {
         const int lane = fresh_lane(lane0), half = lane >> 5, hl = lane & 31;
-        const int64_t tile = n_tiles - 1 - ticket / (uint32_t)n_cols;
         const int col = (int)(ticket % (uint32_t)n_cols);
         const int64_t r0 = tile * kTileRows + wave * 2 * FR, cb = (int64_t)col * kTileCols, c0 = cb + hl * 2;
         const int64_t left = (int64_t)A.C - c0;
         const int nc = left >= 2 ? 2 : left > 0 ? (int)left : 0;
-        uint32_t drawn = total;  // without the stage a workgroup has one tile
-        if (PIPE && threadIdx.x == 0) drawn = atomicAdd(A.ticket, 1u);
+        const int32_t m32 = m_next;
+        if constexpr (PIPE) stage_wait();
+        // on their way through the first walk: the next row map and a ticket
+        uint32_t drawn = total;
+        const int32_t m_last = __builtin_amdgcn_readlane(m32, 32), m_prev = __builtin_amdgcn_readlane(m32, 33),
+                      m_first = __builtin_amdgcn_readlane(m32, 34);
+        const bool behind = m_last >= 0 && !(m_last & 2), ahead = m_prev >= 0 && !(m_prev & 2);
+        const bool cont = m_first >= 0 && !(m_first & 1);
+        if constexpr (PIPE) {
+            m_next = map_of(tile1);
+            if (threadIdx.x == 0) drawn = atomicAdd(A.ticket, 1u);
+        }
 
         // the wave's 32 rows as bits, and this half's 16
         const uint32_t in = (uint32_t)__ballot(m32 >= 0), firsts = (uint32_t)__ballot(m32 >= 0 && (m32 & 1)),
                        lasts = (uint32_t)__ballot(m32 >= 0 && (m32 & 2));
         const uint32_t my_in = in >> (half * FR), my_firsts = firsts >> (half * FR), my_lasts = lasts >> (half * FR);
         const uint32_t any_first = firsts | firsts >> FR, any_last = lasts | lasts >> FR;
-        const int32_t m_tile = m32;
-        auto seq_of = [&](int r) { return __shfl(m_tile, half * FR + r) >> 2; };  // all lanes together
+        auto seq_of = [&](int r) { return __shfl(m32, half * FR + r) >> 2; };  // all lanes together
 
         auto rows = [&](const void* base, int64_t stride) {
             return WaveRows<T, VEC>(base, stride, A.n_rows, r0, A.C, cb, half * FR * stride + hl * 2);
@@ -203,15 +224,15 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
         Raw2<T> rd[FR], rx[FR], ra[FR], rb[FR];
         Ckpt2 qx, qa, qb;
         if (PIPE && whole) {
-            stage_wait();
+            const char* stage_rows = stage + kStageHead;
             auto get = [&](int slot, Raw2<T> (&v)[FR]) {
 #pragma unroll
                 for (int r = 0; r < FR; ++r)
-                    v[r].v = *reinterpret_cast<const decltype(v[r].v)*>(stage + slot + r * 256 + lane * 4);
+                    v[r].v = *reinterpret_cast<const decltype(v[r].v)*>(stage_rows + slot + r * 256 + lane * 4);
             };
             if constexpr (CKPT) {
                 auto getq = [&](int t, Ckpt2& q) {
-                    const char* p = stage + kStageRows + t * kStageCkpt;
+                    const char* p = stage_rows + kStageRows + t * kStageCkpt;
                     const uint4 lo = *reinterpret_cast<const uint4*>(p + lane * 16);
                     const uint4 hi = *reinterpret_cast<const uint4*>(p + 1024 + lane * 16);
                     q.sc = *reinterpret_cast<const float*>(p + 2048 + lane * 4);
@@ -268,8 +289,24 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
                 fix_last(rb, nc);
             }
         }
-        const float kk[2] = {nc > 0 ? -expf(al_log[0]) * kLog2e : 0.0f, nc > 1 ? -expf(al_log[1]) * kLog2e : 0.0f};
-        const float dtb[2] = {dt[0], dt[1]};
+        float dtb[2], kk[2], h[2];  // h: the kept state
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            float dt, al;
+            if constexpr (PIPE) {
+                const float* head = reinterpret_cast<const float*>(stage) + hl * 2 + i;
+                dt = head[0];
+                al = head[64];
+                h[i] = head[128];
+            } else {
+                dt = i < nc ? A.dt_bias[c0 + i] : 0.0f;
+                al = i < nc ? A.a_log[c0 + i] : 0.0f;
+                h[i] = 0.0f;
+            }
+            dtb[i] = i < nc ? dt : 0.0f;
+            kk[i] = i < nc ? -expf(al) * kLog2e : 0.0f;
+            h[i] = cont && i < nc ? h[i] : 0.0f;
+        }
         auto get_x = [&](int r, int i) { return CKPT ? qx.get(r, i) : rx[r].get(i); };
 
         // the state a sequence starts from (seq -1: none)
@@ -352,20 +389,15 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
         }
         if (PIPE && threadIdx.x == 0) s_ticket = drawn;
         __syncthreads();
-        ticket = PIPE ? __builtin_amdgcn_readfirstlane(s_ticket) : total;
-        float h[2] = {};
-        const int32_t* map = rare_args()->map + tile * kTileRows;
-        const int32_t m_first = map[0];
-        const bool cont = m_first >= 0 && !(m_first & 1);
+        if constexpr (!PIPE) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) h[i] = cont && i < nc ? rare_args()->states[tile * A.C + c0 + i] : 0.0f;
-        if (ticket < total) ask(ticket);
+            for (int i = 0; i < 2; ++i) h[i] = cont && i < nc ? rare_args()->states[tile * A.C + c0 + i] : 0.0f;
+        }
+        const uint32_t ticket2 = PIPE ? __builtin_amdgcn_readfirstlane(s_ticket) : total;
         if (wave == 0) {  // one channel a lane
             const auto* R = rare_args();
             const Chain chain{R->chain, n_tiles * Cp};
-            const int32_t m_last = map[kTileRows - 1], m_prev = tile > 0 ? map[-1] : -1;
-            const bool behind = m_last >= 0 && !(m_last & 2), ahead = m_prev >= 0 && !(m_prev & 2);
-            float ta[1], tu[1];
+            float ta[1], tu[1], m1[1];
             const float* pa = reinterpret_cast<const float*>(s_ra) + lane;
             const float* pu = reinterpret_cast<const float*>(s_ru) + lane;
             ta[0] = pa[(kWaves - 1) * kTileCols];
@@ -377,15 +409,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
                 ta[0] = ja; tu[0] = ju;
             }
             tell_run<1>(chain, tile * Cp + cb, behind, ahead, ta, tu);
-            float m1[1];
             hand_on<1>(chain, tile * Cp + cb, Cp, n_tiles - 1 - tile, behind, ahead, ta, tu, m1, R->err);
             reinterpret_cast<float*>(s_h)[lane] = m1[0];
-        } else {
-            again(h[0]); again(h[1]);  // arrived before the next tile's rows are asked for
-            if (ticket < total) fetch(ticket);
+        } else if (ticket1 < total) {
+            fetch(ticket1, tile1, m_next);
         }
         __syncthreads();
-        if (wave == 0 && ticket < total) fetch(ticket);  // not before the state is handed on
+        if (wave == 0 && ticket1 < total) fetch(ticket1, tile1, m_next);  // not before the state is handed on
         float mu[2] = {s_h[hl].x, s_h[hl].y};
         for (int v = kWaves - 1; v > wave; --v) {
             const float2 va = s_ra[v][hl], vu = s_ru[v][hl];
@@ -501,6 +531,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
             for (int q = 0; q < kWaves; ++q) v += p[q * kTileCols];
             rare_args()->part[(tile * 2 + wave) * Cp + cb + lane] = v;
         }
+        ticket = ticket1;
+        tile = tile1;
+        ticket1 = ticket2;
+        tile1 = tile_of(ticket2);
     }
 }
 
