@@ -85,6 +85,23 @@ __device__ __forceinline__ void raise(int32_t* err, uint32_t bit) {
     if (err) atomicOr(reinterpret_cast<unsigned int*>(err), bit);
 }
 
+// Bounds of a sequence are in range and not decreasing.
+__device__ __forceinline__ bool bounds_ok(int64_t n_rows, int c0, int c1) {
+    return c0 >= 0 && c1 >= c0 && (int64_t)c1 <= n_rows;
+}
+// Is sequence s valid, given that some sequence has bad bounds?  It may not
+// begin before the end of a valid one above it, so every row has one owner.
+__device__ inline bool valid_slow(const int32_t* cu, int64_t n_rows, int s) {
+    int end = 0;
+    for (int j = 0; j <= s; ++j) {
+        const int c0 = cu[j], c1 = cu[j + 1];
+        const bool ok = c0 >= end && bounds_ok(n_rows, c0, c1);
+        if (j == s) return ok;
+        if (ok) end = c1;
+    }
+    return false;
+}
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kTiny = 1.17549435e-38f;  // smallest normal number
 

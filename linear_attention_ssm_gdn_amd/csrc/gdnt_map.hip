@@ -6,24 +6,6 @@ namespace gdnt {
 
 constexpr int kMapThreads = 256;
 
-// Bounds of sequence s are in range and not decreasing.
-__device__ __forceinline__ bool bounds_ok(const MapArgs& A, int c0, int c1) {
-    return c0 >= 0 && c1 >= c0 && (int64_t)c1 <= A.n_rows;
-}
-
-// Is sequence `s` free of bad bounds, given that some sequence is not?  The
-// running end of the valid sequences before it decides, so rows have one owner.
-__device__ bool valid_slow(const MapArgs& A, int s) {
-    int end = 0;
-    for (int j = 0; j <= s; ++j) {
-        const int c0 = A.cu[j], c1 = A.cu[j + 1];
-        const bool ok = c0 >= end && bounds_ok(A, c0, c1);
-        if (j == s) return ok;
-        if (ok) end = c1;
-    }
-    return false;
-}
-
 // The sequence that row r (< n_rows) is computed for, and its bounds; -1: none.
 __device__ int owner(const MapArgs& A, int64_t r, bool bad, int& c0, int& c1) {
     int seq = -1;
@@ -40,7 +22,7 @@ __device__ int owner(const MapArgs& A, int64_t r, bool bad, int& c0, int& c1) {
         int end = 0;
         for (int s = 0; s < A.n_seqs; ++s) {
             const int b0 = A.cu[s], b1 = A.cu[s + 1];
-            if (b0 < end || !bounds_ok(A, b0, b1)) continue;
+            if (b0 < end || !bounds_ok(A.n_rows, b0, b1)) continue;
             if ((int64_t)b0 <= r && r < (int64_t)b1) { seq = s; break; }
             end = b1;
         }
@@ -63,7 +45,7 @@ __global__ __launch_bounds__(kMapThreads) void k_row_map(const MapArgs A) {
     for (int64_t i = gid; i < A.n_zero; i += stride) A.zero[i] = 0;
 
     bool bad = false;
-    for (int s = tid; s < A.n_seqs; s += kMapThreads) bad |= !bounds_ok(A, A.cu[s], A.cu[s + 1]);
+    for (int s = tid; s < A.n_seqs; s += kMapThreads) bad |= !bounds_ok(A.n_rows, A.cu[s], A.cu[s + 1]);
     bad = __syncthreads_or(bad) != 0;
 
     for (int64_t r = gid; r < A.n_map; r += stride) {
@@ -77,14 +59,14 @@ __global__ __launch_bounds__(kMapThreads) void k_row_map(const MapArgs A) {
             const int page = A.page_idx[s];
             if (page < 0) continue;
             if (page >= A.page_limit) raise(A.err, GDN_DEVERR_PAGE);
-            else if (bad && !valid_slow(A, s)) raise(A.err, GDN_DEVERR_BATCH);
+            else if (bad && !valid_slow(A.cu, A.n_rows, s)) raise(A.err, GDN_DEVERR_BATCH);
             else if (A.max_len > 0 && A.cu[s + 1] - A.cu[s] > A.max_len) raise(A.err, GDN_DEVERR_BATCH);
         }
     }
     if (A.pass_dst) {  // rows of sequences that no kernel behind this one writes
         for (int s = blockIdx.x; s < A.n_seqs; s += gridDim.x) {
             const int page = A.page_idx[s], c0 = A.cu[s], c1 = A.cu[s + 1];
-            const bool live = page >= 0 && page < A.page_limit && !(bad && !valid_slow(A, s)) &&
+            const bool live = page >= 0 && page < A.page_limit && !(bad && !valid_slow(A.cu, A.n_rows, s)) &&
                               (A.max_len == 0 || c1 - c0 <= A.max_len);
             if (live && c0 != c1) continue;
             const int64_t at = (int64_t)s * A.pass_width;

@@ -206,14 +206,17 @@ __global__ __launch_bounds__(256) void k_scan_rows(const ScanArgs A, int n_x) {
     const int seq = (int)(blockIdx.x / n_x);
     const int64_t c0 = ((int64_t)(blockIdx.x % n_x) * 256 + threadIdx.x) * 4;
     const bool tell = blockIdx.x % n_x == 0 && threadIdx.x == 0;
-    const int page = A.page_idx[seq];
+    const int page = A.page_idx[seq], r0 = A.cu[seq], r1 = A.cu[seq + 1];
+    // all bounds up to this sequence's, as the row map does
+    bool bad = false;
+    for (int s = threadIdx.x; s <= seq; s += 256) bad |= !bounds_ok(A.n_rows, A.cu[s], A.cu[s + 1]);
+    bad = __syncthreads_or(bad) != 0;
     if (page < 0) return;
     if (page >= A.page_limit) {
         if (tell) raise(A.err, GDN_DEVERR_PAGE);
         return;
     }
-    const int r0 = A.cu[seq], r1 = A.cu[seq + 1];
-    if (r0 < 0 || r1 < r0 || (int64_t)r1 > A.n_rows || r1 - r0 > A.max_len) {
+    if ((bad && !valid_slow(A.cu, A.n_rows, seq)) || r1 - r0 > A.max_len) {
         if (tell) raise(A.err, GDN_DEVERR_BATCH);
         return;
     }

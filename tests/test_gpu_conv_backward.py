@@ -99,6 +99,27 @@ def test_conv_backward_padding_gaps_and_strides(pad, offset, heads):
         c.check(c.run(**kw), **kw)
 
 
+def test_long_strips_equal_short_ones():
+    """A batch large enough for strips of 57 and of 25 rows gives every row of dx and d_window0 the bits that the same
+    sequence alone gives in shorter strips: a row's sums do not depend on where it lies."""
+    g = gdn()
+    lens = [1, 700, 0, 58, 57, 2, 3000, 115, 26, 900]
+    for heads, ask in (((16, 32, 128, 128), 57), ((8, 16, 128, 128), 25)):
+        c = Conv(lens, heads, act="bf16", ydt="bf16", seed=21)
+        waves = lambda own: -(-c.rows // own) * -(-c.C // 256)
+        assert (57 if waves(57) >= 2048 else 25 if waves(25) >= 2048 else 13) == ask
+        out = c.run()
+        for s, (r0, r1) in enumerate(c.spans):
+            if r0 == r1:
+                continue
+            one = g.Batch(torch.tensor([0, r1 - r0], dtype=torch.int32, device=DEV), c.batch.page_idx[s:s + 1], None, 0,
+                          r1 - r0)
+            got = g.gdnt_conv_backward(c.dims, c.w, c.x[r0:r1], c.dy[r0:r1], one, g.ConvPool(c.win, None),
+                                       d_window=torch.from_numpy(c.d_window[s:s + 1]).to(DEV))
+            assert torch.equal(got.dx, out.dx[r0:r1]), s
+            assert torch.equal(got.d_window0[0], out.d_window0[s]), s
+
+
 def test_conv_backward_bad_batches():
     g = gdn()
     c = Conv([20, 20, 20], act="f32", seed=4)

@@ -126,8 +126,53 @@ def test_bad_batches_are_skipped_and_flagged(max_seqlen):
     assert e == g.GDN_DEVERR_BATCH and np.array_equal(h[:8], base[:8]) and np.isnan(so[pages[2]]).all()
     h, so, e = run([-3, 4, 8, 12, 16], pages)
     assert e == g.GDN_DEVERR_BATCH and np.isnan(h[:4]).all() and np.array_equal(h[4:], base[4:])
+    h, so, e = run([0, 4, 2, 6, 8], pages)  # the second decreases, the third begins inside the first
+    assert e == g.GDN_DEVERR_BATCH and np.array_equal(h[:4], base[:4])
+    assert np.isnan(h[4:6]).all() and np.isnan(so[pages[1:3]]).all() and not np.isnan(h[6:8]).any()
     h, so, e = run(cu.tolist(), pages, limit=3)
     assert e == g.GDN_DEVERR_BATCH and np.isnan(h).all() and np.isnan(so).all()
+
+
+def test_many_sequences():
+    """More sequences than a workgroup has threads, of every length from 0 to 6, in both forms."""
+    g = gdn()
+    rng = np.random.default_rng(0)
+    lens = rng.integers(0, 7, 1500).tolist()
+    c = Case(lens, 20, "f32", "f32", skip=(7, 900), seed=8)
+    saved = c.saved()
+    h, _, so = c.forward(saved)
+    check_forward(c, h, so, ora)
+    check_grads(c, c.backward(saved), ora)
+    b = g.Batch(c.batch.cu_seqlens, c.batch.page_idx, None, 6, c.rows)
+    h, _, so = c.forward(batch=b)
+    check_forward(c, h, so, ora)
+
+
+def test_rows_beyond_four_gigabytes():
+    """Row offsets that pass 32 bits: x, dh and dx with 3 MB between rows, against the same rows packed."""
+    c = Case([300, 1400], 64, "bf16", "f32", seed=19)
+    saved = c.saved(ckpt=True)
+    h, _, so = c.forward(saved)
+    want = c.backward(saved)
+    stride = 3 << 19
+    wide = {k: torch.zeros((c.rows, stride), dtype=torch.bfloat16, device=DEV) for k in ("x", "dh", "dx")}
+    assert c.rows * stride * 2 > 1 << 32
+    for k in ("x", "dh"):
+        wide[k][:, :64].copy_(c.t[k])
+        c.t[k] = wide[k][:, :64]
+    saved2 = c.saved()
+    h2, _, so2 = c.forward(saved2)
+    assert torch.equal(h2, h) and torch.equal(saved2.states[1:2], saved.states[1:2])
+    g = gdn()
+    out = c.grads_out()._replace(dx=wide["dx"][:, :64])
+    plain = Case([300, 1400], 64, "bf16", "f32", seed=19)
+    ref = plain.backward(saved2)
+    g.gdnt_scan_backward(c.dims, c.params, c.batch, g.StatePool(c.h0.to(DEV)), saved2, c.t["dh"], x=c.t["x"],
+                         a=c.t["a"], b=c.t["b"], d_state=torch.from_numpy(c.d_state).to(DEV), out=out)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(out, ref))
+    assert float(wide["dx"][:, 64:].abs().max()) == 0
+    del want
 
 
 def test_bad_batches_in_the_backward_pass():
