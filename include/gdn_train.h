@@ -27,7 +27,8 @@
  *   (GDN_DEVERR_BATCH).
  * - Sequences of length 0 are no-ops; a backward pass hands the gradient of
  *   their final state or window through to the initial one.
- * - Any row stride >= channels and any element-aligned pointer is accepted.
+ * - Any row stride from channels to 2^24 and any element-aligned pointer is
+ *   accepted.
  *   Rows on whole vectors are faster: on 4 bytes for the recurrence (any
  *   fp32 rows; bf16 rows of even stride), on four elements and in channels a
  *   multiple of 4 for the conv and the one-launch form.  Others are read and

@@ -27,7 +27,8 @@ size_t round_up(size_t v) { return (v + 255) / 256 * 256; }
 
 // Rows that start on their element's boundary, and on a 4-channel vector's.
 bool rows_ok(const void* p, int64_t stride, int64_t C, int32_t dt) {
-    return p && stride >= C && aligned(p, (size_t)elem_size(dt));
+    // a wave's rows are addressed by 32-bit byte offsets
+    return p && stride >= C && stride <= (1 << 24) && aligned(p, (size_t)elem_size(dt));
 }
 bool rows_vec(const void* p, int64_t stride, int32_t dt) {
     return stride % 4 == 0 && aligned(p, (size_t)(4 * elem_size(dt)));

@@ -21,7 +21,8 @@ namespace gdnt {
 constexpr int kConvThreads = kConvWaves * 64;
 
 // The rows of one tensor around a wave's strip; row k counts from the strip's
-// first, from -3 on.  VEC: a buffer descriptor, a scalar offset for the row.
+// first, from -3 on.  VEC: a buffer descriptor, a scalar offset for the row
+// (32 bits reach over 63 rows of up to 2^24 elements).
 template <typename T, bool VEC> struct Strip {
     __amdgpu_buffer_rsrc_t rs;
     uint32_t row, at;  // bytes
@@ -251,8 +252,6 @@ __global__ __launch_bounds__(kConvThreads) void k_conv_backward(const ConvBwdArg
 
 template <typename T, typename YT, bool VEC> static hipError_t conv_t(const ConvBwdArgs& a, hipStream_t s) {
     const int nc = (int)((a.C + kConvCols - 1) / kConvCols);
-    // VEC addresses a strip's rows (at most 63) by 32-bit byte offsets
-    if (VEC && (a.x_stride | a.dy_stride | a.dx_stride) >> 24) return conv_t<T, YT, false>(a, s);
     const int own = conv_rows(a.n_rows, a.C);
     const int64_t nt = conv_tiles(a.n_rows, a.C), grid = nt * nc;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;

@@ -40,73 +40,86 @@ template <typename T> __device__ __forceinline__ Raw2<T> zero2() {
 }
 // The rows of one tensor that a wave works on.  `first`: the wave's first row,
 // `col` its first channel, `lane_at` the lane's own first element from there;
-// row r of the lane is r rows further down.  VEC: a buffer descriptor, so that
-// a row's place is a scalar offset and a lane's place one vector register for
-// all its rows.  The lane with an odd count's last channel loads a pair all
-// the same: that channel and the padding beside it in bf16 (rows start on
-// pairs, so the pair is in one dword), the channel before it and that one in
-// fp32; fix_last puts the pair right.
+// row r of the lane is r rows further down.  A buffer descriptor makes a row's
+// place a scalar offset and a lane's place one vector register for all rows
+// (32 bits: row strides end at 2^24 elements); it ends with the tensor.
+// VEC: rows start on a dword, a lane's two channels move together; else (bf16
+// at odd offsets, a single channel) one after the other, which takes twice the
+// instructions.  The lane with an odd count's last channel loads a pair all
+// the same: that channel and what is beside it, or with VEC in fp32 the one
+// before it and that one (the pair's end may be the tensor's); fix_last puts
+// the pair right.
 template <typename T, bool VEC> struct WaveRows {
     __amdgpu_buffer_rsrc_t rs;
     uint32_t row, at;  // bytes
-    T* p;
-    int64_t stride;
-    bool odd;  // uniform: a lane here has one channel
-    __device__ __forceinline__ WaveRows(const void* base, int64_t stride_, int64_t n_rows, int64_t first, int32_t C,
+    bool odd;          // uniform: a lane here has one channel
+    __device__ __forceinline__ WaveRows(const void* base, int64_t stride, int64_t n_rows, int64_t first, int32_t C,
                                         int64_t col, int64_t lane_at)
-        : row((uint32_t)stride_ * (uint32_t)sizeof(T)), at((uint32_t)lane_at * (uint32_t)sizeof(T)),
-          p(static_cast<T*>(const_cast<void*>(base)) + first * stride_ + col), stride(stride_),
+        : row((uint32_t)stride * (uint32_t)sizeof(T)), at((uint32_t)lane_at * (uint32_t)sizeof(T)),
           odd((C & 1) && C - col < 128) {
         // where rows are walked tile after tile, keeps the rows' offsets from being held in registers
         asm volatile("" : "+s"(row));
-        if constexpr (VEC) {
-            // up to the tensor's last element's dword
-            int64_t bytes = (((n_rows - 1 - first) * stride_ + C - col) * (int64_t)sizeof(T) + 3) & ~3ll;
-            bytes = bytes < 0 ? 0 : bytes > 0xfffffffcll ? 0xfffffffcll : bytes;
-            rs = __builtin_amdgcn_make_buffer_rsrc(p, 0, (uint32_t)bytes, 0x00020000);
-        } else {
-            p += lane_at;
-        }
+        int64_t bytes = ((n_rows - 1 - first) * stride + C - col) * (int64_t)sizeof(T);
+        if (VEC) bytes = (bytes + 3) & ~3ll;  // up to the last element's dword
+        bytes = bytes < 0 ? 0 : bytes > 0xfffffffcll ? 0xfffffffcll : bytes;
+        rs = __builtin_amdgcn_make_buffer_rsrc(static_cast<T*>(const_cast<void*>(base)) + first * stride + col, 0,
+                                               (uint32_t)bytes, 0x00020000);
     }
     __device__ __forceinline__ Raw2<T> load(int r, int nc) const {
         Raw2<T> v;
-        if constexpr (VEC) {
-            if constexpr (sizeof(T) == 2) v.v = __builtin_amdgcn_raw_buffer_load_b32(rs, at, r * row, 0);
-            else v.v = __builtin_bit_cast(float2, __builtin_amdgcn_raw_buffer_load_b64(rs, odd && nc == 1 ? at - 4 : at, r * row, 0));
+        if constexpr (sizeof(T) == 2) {
+            if constexpr (VEC) {
+                v.v = __builtin_amdgcn_raw_buffer_load_b32(rs, at, r * row, 0);
+            } else {
+                typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+                u16x2 e;  // each half loaded into its half of the register
+                e.x = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, at, r * row, 0);
+                e.y = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, at + 2, r * row, 0);
+                v.v = __builtin_bit_cast(uint32_t, e);
+            }
+        } else if constexpr (VEC) {
+            v.v = __builtin_bit_cast(float2, __builtin_amdgcn_raw_buffer_load_b64(rs, odd && nc == 1 ? at - 4 : at, r * row, 0));
         } else {
-            T e[2] = {T(0), T(0)};
-            if (nc > 0) e[0] = p[r * stride];
-            if (nc > 1) e[1] = p[r * stride + 1];
-            __builtin_memcpy(&v, e, sizeof(v));
+            v.v.x = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at, r * row, 0));
+            v.v.y = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at + 4, r * row, 0));
         }
         return v;
     }
     __device__ __forceinline__ void store(int r, int nc, float a, float b) const {
-        if constexpr (VEC) {
-            if constexpr (sizeof(T) == 2) {
-                const uint32_t v = gdn::f32x2_to_bf16x2(a, b);
-                if (nc == 2) __builtin_amdgcn_raw_buffer_store_b32(v, rs, at, r * row, 0);
-                if (odd && nc == 1) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)v, rs, at, r * row, 0);
-            } else {
-                typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-                const u32x2 v = {__float_as_uint(a), __float_as_uint(b)};
-                if (nc == 2) __builtin_amdgcn_raw_buffer_store_b64(v, rs, at, r * row, 0);
-                if (odd && nc == 1) __builtin_amdgcn_raw_buffer_store_b32(v.x, rs, at, r * row, 0);
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t v = gdn::f32x2_to_bf16x2(a, b);
+            if (nc == 2) {
+                if constexpr (VEC) {
+                    __builtin_amdgcn_raw_buffer_store_b32(v, rs, at, r * row, 0);
+                } else {
+                    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)v, rs, at, r * row, 0);
+                    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(v >> 16), rs, at + 2, r * row, 0);
+                }
             }
+            if (odd && nc == 1) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)v, rs, at, r * row, 0);
         } else {
-            if (nc > 0) p[r * stride] = from_f32<T>(a);
-            if (nc > 1) p[r * stride + 1] = from_f32<T>(b);
+            const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+            if (nc == 2) {
+                if constexpr (VEC) {
+                    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+                    __builtin_amdgcn_raw_buffer_store_b64((u32x2){x, y}, rs, at, r * row, 0);
+                } else {
+                    __builtin_amdgcn_raw_buffer_store_b32(x, rs, at, r * row, 0);
+                    __builtin_amdgcn_raw_buffer_store_b32(y, rs, at + 4, r * row, 0);
+                }
+            }
+            if (odd && nc == 1) __builtin_amdgcn_raw_buffer_store_b32(x, rs, at, r * row, 0);
         }
     }
 };
 
-// Rows as loaded by VEC in the column that ends with an odd count's last channel.
-template <typename T> __device__ __forceinline__ void fix_last(Raw2<T> (&v)[FR], int nc) {
+// Rows as loaded in the column that ends with an odd count's last channel.
+template <typename T, bool VEC> __device__ __forceinline__ void fix_last(Raw2<T> (&v)[FR], int nc) {
     if (nc != 1) return;
 #pragma unroll
     for (int r = 0; r < FR; ++r) {
         if constexpr (sizeof(T) == 2) v[r].v &= 0xffffu;
-        else v[r].v = make_float2(v[r].v.y, 0.0f);
+        else v[r].v = make_float2(VEC ? v[r].v.y : v[r].v.x, 0.0f);
     }
 }
 

@@ -98,10 +98,10 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void k_scan_forwa
             }
         }
     }
-    if (VEC && (A.C & 1) && col == n_cols - 1) {
-        fix_last(rx, nc);
-        fix_last(ra, nc);
-        fix_last(rb, nc);
+    if ((A.C & 1) && col == n_cols - 1) {
+        fix_last<T, VEC>(rx, nc);
+        fix_last<T, VEC>(ra, nc);
+        fix_last<T, VEC>(rb, nc);
     }
     float dt[2], kk[2];
 #pragma unroll
@@ -286,8 +286,6 @@ hipError_t launch_scan_rows(const ScanArgs& a, hipStream_t s) {
 }
 
 template <typename T, bool VEC> static hipError_t forward_t(const ScanArgs& a, hipStream_t s) {
-    // VEC addresses a wave's 16 rows by 32-bit byte offsets
-    if (VEC && (a.x_stride | a.ab_stride | a.h_stride) >> 24) return forward_t<T, false>(a, s);
     const int nc = (int)((a.C + kFwdCols - 1) / kFwdCols);
     const int64_t nt = (a.n_rows + kFwdRows - 1) / kFwdRows, grid = nt * nc;
     if (grid == 0) return hipSuccess;

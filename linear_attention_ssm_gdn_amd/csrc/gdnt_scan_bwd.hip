@@ -267,26 +267,32 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
                 getq(0, qx);
             }
             const WaveRows<T, VEC> X = rows(A.x, A.x_stride), Ag = rows(A.a, A.ab_stride), Bg = rows(A.b, A.ab_stride);
+            auto row = [&](int r) {
+                if constexpr (!CKPT) {
+                    ra[r] = Ag.load(r, nc);
+                    rb[r] = Bg.load(r, nc);
+                    rx[r] = X.load(r, nc);
+                }
+                rd[r] = D.load(r, nc);
+            };
+            if (whole && nc > 0) {  // no branch between the rows: all loads go out at once
 #pragma unroll
-            for (int r = 0; r < FR; ++r) {
-                rd[r] = zero2<T>();
-                if constexpr (!CKPT) { rx[r] = zero2<T>(); ra[r] = zero2<T>(); rb[r] = zero2<T>(); }
-                if ((whole || (my_in >> r & 1u)) && nc > 0) {
-                    if constexpr (!CKPT) {
-                        ra[r] = Ag.load(r, nc);
-                        rb[r] = Bg.load(r, nc);
-                        rx[r] = X.load(r, nc);
-                    }
-                    rd[r] = D.load(r, nc);
+                for (int r = 0; r < FR; ++r) row(r);
+            } else {
+#pragma unroll
+                for (int r = 0; r < FR; ++r) {
+                    rd[r] = zero2<T>();
+                    if constexpr (!CKPT) { rx[r] = zero2<T>(); ra[r] = zero2<T>(); rb[r] = zero2<T>(); }
+                    if ((my_in >> r & 1u) && nc > 0) row(r);
                 }
             }
         }
-        if (VEC && (A.C & 1) && col == n_cols - 1) {
-            fix_last(rd, nc);
+        if ((A.C & 1) && col == n_cols - 1) {
+            fix_last<T, VEC>(rd, nc);
             if constexpr (!CKPT) {
-                fix_last(rx, nc);
-                fix_last(ra, nc);
-                fix_last(rb, nc);
+                fix_last<T, VEC>(rx, nc);
+                fix_last<T, VEC>(ra, nc);
+                fix_last<T, VEC>(rb, nc);
             }
         }
         float dtb[2], kk[2], h[2];  // h: the kept state
@@ -547,9 +553,6 @@ template <typename T, bool VEC, bool CKPT> static hipError_t backward_t(const Sc
     const int nc = (int)(padded_channels(a.C) / kTileCols);
     const int64_t nt = n_tiles(a.n_rows), grid = nt * nc;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    // VEC addresses a wave's 32 rows by 32-bit byte offsets
-    if (VEC && ((CKPT ? 0 : a.x_stride | a.ab_stride) | a.dh_stride | a.dx_stride | a.dab_stride) >> 24)
-        return backward_t<T, false, CKPT>(a, s);
     if (grid > 0) {
         if (sizeof(T) == 2 && VEC && a.vec8)
             hipLaunchKernelGGL((k_scan_backward<T, VEC, CKPT, sizeof(T) == 2 && VEC>),

@@ -117,7 +117,7 @@ def test_forward_refusals(so, L):
                 dict(batch=B(FAKE, FAKE, None, -1, 0, 300)), dict(batch=B(FAKE, FAKE, None, 2, -1, 300)),
                 dict(batch=B(FAKE, FAKE, None, 2, 0, -1)), dict(batch=B(None, FAKE, None, 2, 0, 300)),
                 dict(batch=B(FAKE, None, None, 2, 0, 300)), dict(batch=B(FAKE, FAKE, None, 1 << 29, 0, 300)),
-                dict(x=None), dict(a=None), dict(b=None), dict(h=None), dict(xs=63), dict(abs=63), dict(hs=63),
+                dict(x=None), dict(a=None), dict(b=None), dict(h=None), dict(xs=(1 << 24) + 1), dict(xs=63), dict(abs=63), dict(hs=63),
                 dict(x=FAKE + 1), dict(h=FAKE + 1), dict(si=S(None, 64, 4)), dict(sto=S(None, 64, 4)),
                 dict(si=S(FAKE, 63, 4)), dict(sto=S(FAKE, 64, -1)), dict(si=S(FAKE + 2, 64, 4)),
                 dict(ckpt=FAKE), dict(states=FAKE, ckpt=FAKE + 64), dict(states=FAKE + 4), dict(ws=None),
@@ -147,7 +147,7 @@ def test_backward_refusals(so, L):
     for bad in (dict(dims=None), dict(params=P(FAKE, None)), dict(batch=None), dict(x=None), dict(a=None),
                 dict(b=None), dict(xs=10), dict(abs=10), dict(ckpt=FAKE), dict(x=None, a=None, b=None, ckpt=FAKE + 8),
                 dict(si=S(None, 64, 4)), dict(states=None), dict(states=FAKE + 4), dict(dh=None), dict(dhs=63),
-                dict(dx=None), dict(da=None), dict(db=None), dict(dxs=1), dict(dabs=1), dict(dA=None),
+                dict(dx=None), dict(da=None), dict(db=None), dict(dxs=1 << 25), dict(dxs=1), dict(dabs=1), dict(dA=None),
                 dict(dB=None), dict(ws=None), dict(ws=FAKE + 1), dict(wsb=0), dict(dx=FAKE + 1),
                 dict(batch=B(FAKE, FAKE, None, 2, 0, (1 << 31) - 1))):
         assert _backward(so, L, **bad) == 1, bad
@@ -169,7 +169,7 @@ def _conv(so, L, **kw):
 def test_conv_backward_refusals(so, L):
     B, P = L.GdnBatch, L.GdnConvPool
     for bad in (dict(dims=None), dict(w=None), dict(x=None), dict(dy=None), dict(dx=None), dict(dw=None),
-                dict(xs=127), dict(dys=127), dict(dxs=127), dict(dyt=2), dict(act=2), dict(batch=None),
+                dict(xs=127), dict(dys=127), dict(dxs=127), dict(dys=(1 << 24) + 1), dict(dyt=2), dict(act=2), dict(batch=None),
                 dict(conv=P(FAKE, 3 * 128, 2, 4, None)), dict(conv=P(FAKE, 128, 3, 4, None)),
                 dict(conv=P(FAKE, 3 * 128, 3, -1, None)), dict(conv=P(FAKE + 1, 3 * 128, 3, 4, None)),
                 dict(ws=None), dict(wsb=100), dict(ws=FAKE + 128), dict(dy=FAKE + 2),
