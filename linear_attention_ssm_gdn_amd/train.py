@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -34,8 +35,12 @@ class ScanDims:
     def state_torch(self) -> torch.dtype:
         return _TORCH_DT[self.state_dtype]
 
-    def c(self) -> L.GdntScanDims:
+    @functools.cached_property
+    def _c(self) -> L.GdntScanDims:
         return L.GdntScanDims(self.channels, _DT[self.act_dtype], _DT[self.state_dtype])
+
+    def c(self) -> L.GdntScanDims:
+        return self._c  # the library only reads it
 
 
 @dataclasses.dataclass
@@ -159,13 +164,14 @@ def _workspace(ws: Optional[torch.Tensor], size, dims, n_seqs: int, n_rows: int,
 
 def _call(fn: str, dev: torch.device, *args) -> None:
     """The C entry point on the current stream of `dev`, with `dev` current."""
-    f = getattr(L.load(), fn)
-    if dev.index is None or dev.index == torch.cuda.current_device():
-        st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
+    f, here = getattr(L.load(), fn), torch.cuda.current_device()
+    if dev.index is None or dev.index == here:
+        st = f(*args, torch._C._cuda_getCurrentRawStream(here))  # 2 us less than through a Stream object
     else:
         with torch.cuda.device(dev):
-            st = f(*args, torch.cuda.current_stream(dev).cuda_stream)
-    _check(fn, st)
+            st = f(*args, torch._C._cuda_getCurrentRawStream(dev.index))
+    if st:
+        _check(fn, st)
 
 
 def _p(t: Optional[torch.Tensor]):
