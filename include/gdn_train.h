@@ -25,11 +25,11 @@
  *   are negative, decreasing, beyond n_rows or before the end of an earlier
  *   valid sequence, or when it is longer than a max_seqlen > 0
  *   (GDN_DEVERR_BATCH).
- * - Sequences of length 0 are no-ops; a backward pass hands the gradient of
- *   their final state or window through to the initial one.
+ * - Sequences of length 0 are no-ops, whose page stays as it is; a backward
+ *   pass hands the gradient of their final state or window through to the
+ *   initial one, whatever has_init says.
  * - Any row stride from channels to 2^24 and any element-aligned pointer is
- *   accepted.
- *   Rows on whole vectors are faster: on 4 bytes for the recurrence (any
+ *   accepted.  Rows on whole vectors are faster: on 4 bytes for the recurrence (any
  *   fp32 rows; bf16 rows of even stride), on four elements and in channels a
  *   multiple of 4 for the conv and the one-launch form.  Others are read and
  *   written element by element.
@@ -108,8 +108,8 @@ int32_t gdnt_conv_workspace_bytes(const gdn_dims* dims, int32_t n_seqs, int64_t 
  * zeros, one with an Inf or NaN as NaNs.  Layout, with nb = ceil(n_rows/16)
  * and n4 = ceil(channels/64)*16: int8 q[nb][3][n4][16][4] (tensor x, a, b;
  * row and channel within the block innermost), then fp32 scale[nb][3][n4].
- * Batches with 0 < max_seqlen <= 8 that keep nothing are computed by one
- * launch, others by two. */
+ * Batches of at most 4096 sequences with 0 < max_seqlen <= 8 that keep
+ * nothing are computed by one launch, others by two. */
 int32_t gdnt_scan_forward(const gdnt_scan_dims* dims, const gdnt_scan_params* params,
                           const void* x, int64_t x_stride, const void* a, const void* b, int64_t ab_stride,
                           const gdn_batch* batch, gdn_state_pool state_in, gdn_state_pool state_out,
@@ -133,7 +133,8 @@ int32_t gdnt_scan_forward(const gdnt_scan_dims* dims, const gdnt_scan_params* pa
  * dx: [n_rows][dx_stride]; da, db: [n_rows][dab_stride] (act dtype);
  * d_a_log, d_dt_bias: [channels] fp32, over the sequences of this call,
  * overwritten (zeros for an empty batch); d_state0: [n_seqs][channels] fp32
- * or NULL, zeros where has_init is 0 and for padding and skipped sequences. */
+ * or NULL, zeros where has_init is 0 (of sequences with rows) and for padding
+ * and skipped sequences. */
 int32_t gdnt_scan_backward(const gdnt_scan_dims* dims, const gdnt_scan_params* params,
                            const void* x, int64_t x_stride, const void* a, const void* b, int64_t ab_stride,
                            const void* ckpt, const gdn_batch* batch, gdn_state_pool state_in, const float* states,
@@ -156,7 +157,7 @@ int32_t gdnt_scan_backward(const gdnt_scan_dims* dims, const gdnt_scan_params* p
  * dx: [n_rows][dx_stride] act dtype; d_conv_w: [C_conv][conv_w] fp32, over
  * the sequences of this call, overwritten (zeros for an empty batch);
  * d_window0: [n_seqs][conv_w-1][C_conv] fp32 or NULL, zeros where has_init is
- * 0 and for padding and skipped sequences. */
+ * 0 (of sequences with rows) and for padding and skipped sequences. */
 int32_t gdnt_conv_backward(const gdn_dims* dims, const void* conv_w, const void* x, int64_t x_stride,
                            const void* dy, int32_t dy_dtype, int64_t dy_stride,
                            const gdn_batch* batch, gdn_conv_pool conv, int32_t activation, const float* d_window,

@@ -116,7 +116,7 @@ def _rows2(name: str, t: torch.Tensor, rows: int, cols: int, dt: torch.dtype) ->
     st = t.stride()
     if t.shape != (rows, cols) or (cols > 1 and st[1] != 1):
         raise ValueError(f"{name} must be [{rows}][{cols}] with unit inner stride")
-    return st[0] if rows > 1 else max(st[0], cols)
+    return st[0] if rows > 1 else cols
 
 
 def _flat(name: str, t: Optional[torch.Tensor], shape: tuple, dt: torch.dtype) -> Optional[int]:
@@ -164,6 +164,8 @@ def _workspace(ws: Optional[torch.Tensor], size, dims, n_seqs: int, n_rows: int,
 
 def _call(fn: str, dev: torch.device, *args) -> None:
     """The C entry point on the current stream of `dev`, with `dev` current."""
+    if dev.type != "cuda":  # a kernel would fault on host memory
+        raise ValueError(f"{fn} takes tensors on a GPU, not on {dev}")
     f, here = getattr(L.load(), fn), torch.cuda.current_device()
     if dev.index is None or dev.index == here:
         st = f(*args, torch._C._cuda_getCurrentRawStream(here))  # 2 us less than through a Stream object

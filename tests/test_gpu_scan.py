@@ -148,6 +148,15 @@ def test_many_sequences():
     check_forward(c, h, so, ora)
 
 
+@pytest.mark.parametrize("n", [4096, 4097])
+def test_sequences_around_the_last_batch_of_one_launch(n):
+    g = gdn()
+    c = Case(np.random.default_rng(n).integers(0, 3, n).tolist(), 5, "f32", "f32", seed=n)
+    b = g.Batch(c.batch.cu_seqlens, c.batch.page_idx, None, 2, c.rows)
+    h, _, so = c.forward(batch=b)
+    check_forward(c, h, so, ora)
+
+
 def test_rows_beyond_four_gigabytes():
     """Row offsets that pass 32 bits: x, dh and dx with 3 MB between rows, against the same rows packed."""
     c = Case([300, 1400], 64, "bf16", "f32", seed=19)
@@ -173,6 +182,47 @@ def test_rows_beyond_four_gigabytes():
     assert all(torch.equal(p, q) for p, q in zip(out, ref))
     assert float(wide["dx"][:, 64:].abs().max()) == 0
     del want
+
+
+def test_a_checkpoint_beyond_four_gigabytes():
+    """The last sequence of a batch whose checkpoint passes 32 bits gives the bits it gives alone (it begins on a
+    kept state's row, so tiles and blocks are the same)."""
+    g = gdn()
+    C, n, first = 4096, 1000, 256 * 1400
+    dims = g.ScanDims(C)
+    assert g.gdnt_scan_saved_bytes(dims, first)[1] > 1 << 32
+    rows = lambda v: torch.cat((torch.zeros((first, C), dtype=v.dtype, device=DEV), v))
+    torch.manual_seed(3)
+    x, a, b, dh = (torch.randn(n, C, device=DEV).bfloat16() for _ in range(4))
+    params = g.ScanParams(torch.randn(C, device=DEV) * 0.1, torch.randn(C, device=DEV) - 3)
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device=DEV)
+    h0, d_state = torch.randn(2, C, device=DEV), torch.randn(2, C, device=DEV)
+
+    def step(x, a, b, dh, batch, ds):
+        pool, out = g.StatePool(h0), g.StatePool(torch.zeros_like(h0))
+        saved = g.ScanSaved.alloc(dims, batch.n_rows, DEV, ckpt=True)
+        h = g.gdnt_scan_forward(dims, params, x, a, b, batch, pool, out, saved=saved)
+        got = g.gdnt_scan_backward(dims, params, batch, pool, saved, dh, d_state=ds)
+        torch.cuda.synchronize()
+        return (h[-n:], out.buf[1], got.dx[-n:], got.da[-n:], got.db[-n:], got.d_state0[-1])
+    want = step(x, a, b, dh, g.Batch(i32(0, n), i32(1), None, 0, n), d_state[1:])
+    got = step(*(rows(v) for v in (x, a, b, dh)), g.Batch(i32(0, first, first + n), i32(0, 1), None, 0, first + n),
+               d_state)
+    for p, q in zip(got, want):
+        assert torch.equal(p, q)
+
+
+def test_one_row_of_any_stride():
+    """A single row has no stride to speak of: views of wider buffers, a's and b's strides apart."""
+    g = gdn()
+    c = Case([1], 24, "bf16", "f32", seed=4)
+    want = c.forward()
+    for k, width in (("x", 24), ("a", 40), ("b", 1 << 25)):
+        buf = torch.zeros((1, width), dtype=torch.bfloat16, device=DEV)
+        buf[:, :24].copy_(c.t[k])
+        c.t[k] = buf[:, :24]
+    got = c.forward()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[2].buf[c.pages], want[2].buf[c.pages])
 
 
 def test_bad_batches_in_the_backward_pass():

@@ -208,3 +208,20 @@ def test_the_binding_refuses_what_the_pointers_cannot_show(L):
         g.gdnt_conv_backward(cd, t(96, 4), t(4, 96), t(4, 96, dt=torch.float64), batch)
     with pytest.raises(ValueError):
         g.gdnt_conv_backward(cd, t(96, 3), t(4, 96), t(4, 96), batch)
+
+
+def test_the_binding_refuses_tensors_on_the_host(L):
+    """Valid in every other respect: the last check before a launch."""
+    import torch
+    import linear_attention_ssm_gdn_amd as g
+    t = lambda *s, dt=torch.float32: torch.zeros(*s, dtype=dt)
+    dims, params, pool = g.ScanDims(8, act_dtype="f32"), g.ScanParams(t(8), t(8)), g.StatePool(t(1, 8))
+    cu = torch.tensor([0, 4], dtype=torch.int32)
+    batch = g.Batch(cu, t(1, dt=torch.int32), None, 0, 4)
+    saved = g.ScanSaved(t(1, 8))
+    with pytest.raises(ValueError, match="on a GPU"):
+        g.gdnt_scan_forward(dims, params, t(4, 8), t(4, 8), t(4, 8), batch, pool)
+    with pytest.raises(ValueError, match="on a GPU"):
+        g.gdnt_scan_backward(dims, params, batch, pool, saved, t(4, 8), x=t(4, 8), a=t(4, 8), b=t(4, 8))
+    with pytest.raises(ValueError, match="on a GPU"):
+        g.gdnt_conv_backward(g.Dims(1, 1, 32, 32, act_dtype="f32"), t(96, 4), t(4, 96), t(4, 96), batch)
