@@ -44,7 +44,9 @@ __device__ __forceinline__ void chain_store(uint64_t* p, uint32_t hi, float lo) 
 
 // One wave, NCH channels a lane from word `at` on; `step` words to the tile
 // before, of which n_pred exist.  The state before the tile, into h.  Every
-// poll asks for all words at once: a trip to memory costs as much as a walk.
+// poll asks for all words at once: a trip to memory costs as much as a walk
+// (forward and backward over 32768 x 4096 in bf16: 910 us one tile at a time,
+// 838 four at once; six cost registers, 278 against 260 us forward).
 template <int NCH>
 __device__ __forceinline__ void look_back(const Chain& C, int64_t at, int64_t step, int64_t n_pred, float (&h)[NCH],
                                           int32_t* err) {

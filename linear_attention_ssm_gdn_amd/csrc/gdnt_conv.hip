@@ -14,6 +14,11 @@
 // sequence's first are its window: their sums are d_window0, and where a
 // sequence ends the open sums are the rows of its rolled window, where
 // d_window joins.
+//
+// Bound by memory: 32768 x 8192 in bf16 takes 340 us for 1.61 GB (4.7 TB/s, 93%
+// of a large copy's rate; 1.72 GB with what strips read twice, 5.0 TB/s) at 26
+// vector instructions an element.  VEC (rows on four elements): 373 us a call
+// there, 870 element by element; fp32 665 and 980; 2159 rows in bf16 44 and 78.
 #include "gdnt_device.hpp"
 
 namespace gdnt {

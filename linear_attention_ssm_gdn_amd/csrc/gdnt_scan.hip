@@ -10,6 +10,13 @@
 // tile are joined through LDS, the state comes from the tile before
 // (gdnt_chain.hpp), and each wave walks its rows again from registers: x, a
 // and b are read once.  Sequence boundaries may fall anywhere.
+//
+// Bound by memory: 32768 x 4096 in bf16 takes 250 us for 1.07 GB (4.3 TB/s,
+// 85% of what a large copy reaches), at 33 vector instructions an element
+// (52% of the issue slots) and with two workgroups on a compute unit, one
+// loading while the other walks; 301 us and 1.50 GB (5.0 TB/s) with the 8-bit
+// checkpoint, 64% of the slots.  30011 x 1001 in fp32 takes 130 us (3.7 TB/s):
+// its 8 columns leave the chain of 235 tiles in sight.
 #include "gdnt_chain.hpp"
 #include "gdnt_rows.hpp"
 
@@ -200,7 +207,9 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void k_scan_forwa
 }
 
 // A few rows a sequence (decode and short verify-like steps): one thread
-// walks four channels of one sequence, one launch, no row map.
+// walks four channels of one sequence, one launch, no row map.  64 sequences
+// of one row by 4096 channels take 4.2 us, a launch's own time: 4 MB are 0.8
+// us of memory.
 template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void k_scan_rows(const ScanArgs A, int n_x) {
     const int seq = (int)(blockIdx.x / n_x);
