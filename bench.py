@@ -320,13 +320,13 @@ def measure(torch, wload, steps, warmup, min_warm_s=0.0):
 
 # --------------------------------------------------------------- traffic file
 def kernel_source_hash() -> str:
-    """Hash of the device sources (kernels, their launchers and headers; the
-    host-side argument checks and path selection do not change a kernel's
-    traffic)."""
+    """Hash of the device sources of the kernels timed here (with their
+    launchers and headers; the host-side argument checks and path selection
+    do not change a kernel's traffic, nor do the gdnt_ sources)."""
     h = hashlib.sha256()
     csrc = os.path.join(ROOT, "linear_attention_ssm_gdn_amd", "csrc")
     for f in sorted(os.listdir(csrc)):
-        if not f.endswith((".hip", ".hpp", ".h")):
+        if not f.endswith((".hip", ".hpp", ".h")) or f.startswith("gdnt_"):
             continue
         with open(os.path.join(csrc, f), "rb") as fh:
             h.update(f.encode() + fh.read())
