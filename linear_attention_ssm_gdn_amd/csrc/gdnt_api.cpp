@@ -39,11 +39,6 @@ bool rows_ok(const void* p, int64_t stride, int64_t C, int32_t dt) {
 bool rows_vec(const void* p, int64_t stride, int32_t dt) {
     return stride % 4 == 0 && aligned(p, (size_t)(4 * elem_size(dt)));
 }
-// Rows that start on a dword.
-bool rows_dword(const void* p, int64_t stride, int32_t dt) {
-    return stride * elem_size(dt) % 4 == 0 && aligned(p, 4);
-}
-
 int32_t check_dims(const gdnt_scan_dims* d) {
     if (!d || d->channels <= 0 || d->channels > (1 << 24)) return GDN_ERR_ARG;
     if (!dtype_ok(d->act_dtype) || !dtype_ok(d->state_dtype)) return GDN_ERR_ARG;
@@ -174,8 +169,6 @@ GDN_EXPORT int32_t gdnt_scan_forward(const gdnt_scan_dims* dims, const gdnt_scan
     A.vec = C % 4 == 0 && rows_vec(x, x_stride, dt) && rows_vec(a, ab_stride, dt) && rows_vec(b, ab_stride, dt) &&
             rows_vec(h, h_stride, dt) && rows_vec(state_in.base, state_in.page_stride, sdt) &&
             rows_vec(state_out.base, state_out.page_stride, sdt);
-    A.vec2 = C > 1 && rows_dword(x, x_stride, dt) && rows_dword(a, ab_stride, dt) && rows_dword(b, ab_stride, dt) &&
-             rows_dword(h, h_stride, dt);
     return from_hip(rows ? gdnt::launch_scan_rows(A, (hipStream_t)stream)
                          : gdnt::launch_scan_forward(A, (hipStream_t)stream));
 }
@@ -214,9 +207,6 @@ GDN_EXPORT int32_t gdnt_scan_backward(const gdnt_scan_dims* dims, const gdnt_sca
     A.dh = dh; A.dh_stride = dh_stride; A.d_state = d_state;
     A.dx = dx; A.dx_stride = dx_stride; A.da = da; A.db = db; A.dab_stride = dab_stride;
     A.d_a_log = d_a_log; A.d_dt_bias = d_dt_bias; A.d_state0 = d_state0;
-    A.vec2 = C > 1 && rows_dword(dh, dh_stride, dt) && rows_dword(dx, dx_stride, dt) &&
-             rows_dword(da, dab_stride, dt) && rows_dword(db, dab_stride, dt) &&
-             (ckpt || (rows_dword(x, x_stride, dt) && rows_dword(a, ab_stride, dt) && rows_dword(b, ab_stride, dt)));
     auto on16 = [&](const void* p, int64_t stride) { return stride * elem_size(dt) % 16 == 0 && aligned(p, 16); };
     A.vec8 = C % 8 == 0 && on16(dh, dh_stride) &&
              (ckpt || (on16(x, x_stride) && on16(a, ab_stride) && on16(b, ab_stride)));

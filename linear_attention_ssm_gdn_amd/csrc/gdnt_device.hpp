@@ -45,6 +45,8 @@ template <typename T, bool VEC> __device__ __forceinline__ Raw4<T> load4(const T
     Raw4<T> r = zero4<T>();
     if constexpr (VEC) {
         r.v = *reinterpret_cast<const decltype(r.v)*>(p);
+    } else if (nc == 4) {
+        __builtin_memcpy(&r.v, p, sizeof(r.v));
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -55,6 +57,9 @@ template <typename T, bool VEC> __device__ __forceinline__ Raw4<T> load4(const T
 template <bool VEC> __device__ __forceinline__ void store4(bf16_t* p, const float (&f)[4], int nc) {
     if constexpr (VEC) {
         *reinterpret_cast<uint2*>(p) = make_uint2(gdn::f32x2_to_bf16x2(f[0], f[1]), gdn::f32x2_to_bf16x2(f[2], f[3]));
+    } else if (nc == 4) {
+        const uint2 v = make_uint2(gdn::f32x2_to_bf16x2(f[0], f[1]), gdn::f32x2_to_bf16x2(f[2], f[3]));
+        __builtin_memcpy(p, &v, sizeof(v));
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -64,6 +69,9 @@ template <bool VEC> __device__ __forceinline__ void store4(bf16_t* p, const floa
 template <bool VEC> __device__ __forceinline__ void store4(float* p, const float (&f)[4], int nc) {
     if constexpr (VEC) {
         *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    } else if (nc == 4) {
+        const float4 v = make_float4(f[0], f[1], f[2], f[3]);
+        __builtin_memcpy(p, &v, sizeof(v));
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)

@@ -43,84 +43,62 @@ template <typename T> __device__ __forceinline__ Raw2<T> zero2() {
 // row r of the lane is r rows further down.  A buffer descriptor makes a row's
 // place a scalar offset and a lane's place one vector register for all rows
 // (32 bits: row strides end at 2^24 elements); it ends with the tensor.
-// VEC: rows start on a dword, a lane's two channels move together; else (bf16
-// at odd offsets, a single channel) one after the other, which takes twice the
-// instructions: over 16692 rows the bf16 forward pass takes 160 us with 4094
-// channels and 240 with 4095, forward and backward 577 and 1146 us.  The lane with an odd count's last channel loads a pair all
-// the same: that channel and what is beside it, or with VEC in fp32 the one
-// before it and that one (the pair's end may be the tensor's); fix_last puts
-// the pair right.
-template <typename T, bool VEC> struct WaveRows {
+// PAIR: a lane's two channels move together, wherever the row starts (bf16
+// rows at odd offsets as dwords that no dword boundary holds: @ODD@).  Else there is only
+// one channel.  The lane with an odd count's last channel loads the one before
+// it and that one, so as to end with the row; fix_last puts the pair right.
+// The descriptor of such a column begins one channel earlier: its first lane
+// may be the one.
+template <typename T, bool PAIR> struct WaveRows {
     __amdgpu_buffer_rsrc_t rs;
     uint32_t row, at;  // bytes
     bool odd;          // uniform: a lane here has one channel
     __device__ __forceinline__ WaveRows(const void* base, int64_t stride, int64_t n_rows, int64_t first, int32_t C,
                                         int64_t col, int64_t lane_at)
-        : row((uint32_t)stride * (uint32_t)sizeof(T)), at((uint32_t)lane_at * (uint32_t)sizeof(T)),
-          odd((C & 1) && C - col < 128) {
+        : row((uint32_t)stride * (uint32_t)sizeof(T)), odd((C & 1) && C - col < 128) {
+        if (PAIR && odd) { col -= 1; lane_at += 1; }
+        at = (uint32_t)lane_at * (uint32_t)sizeof(T);
         // where rows are walked tile after tile, keeps the rows' offsets from being held in registers
         asm volatile("" : "+s"(row));
         int64_t bytes = ((n_rows - 1 - first) * stride + C - col) * (int64_t)sizeof(T);
-        if (VEC) bytes = (bytes + 3) & ~3ll;  // up to the last element's dword
         bytes = bytes < 0 ? 0 : bytes > 0xfffffffcll ? 0xfffffffcll : bytes;
         rs = __builtin_amdgcn_make_buffer_rsrc(static_cast<T*>(const_cast<void*>(base)) + first * stride + col, 0,
                                                (uint32_t)bytes, 0x00020000);
     }
     __device__ __forceinline__ Raw2<T> load(int r, int nc) const {
         Raw2<T> v;
+        const uint32_t from = PAIR && odd && nc == 1 ? at - (uint32_t)sizeof(T) : at;
         if constexpr (sizeof(T) == 2) {
-            if constexpr (VEC) {
-                v.v = __builtin_amdgcn_raw_buffer_load_b32(rs, at, r * row, 0);
-            } else {
-                typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-                u16x2 e;  // each half loaded into its half of the register
-                e.x = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, at, r * row, 0);
-                e.y = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, at + 2, r * row, 0);
-                v.v = __builtin_bit_cast(uint32_t, e);
-            }
-        } else if constexpr (VEC) {
-            v.v = __builtin_bit_cast(float2, __builtin_amdgcn_raw_buffer_load_b64(rs, odd && nc == 1 ? at - 4 : at, r * row, 0));
+            if constexpr (PAIR) v.v = __builtin_amdgcn_raw_buffer_load_b32(rs, from, r * row, 0);
+            else v.v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, from, r * row, 0);
+        } else if constexpr (PAIR) {
+            v.v = __builtin_bit_cast(float2, __builtin_amdgcn_raw_buffer_load_b64(rs, from, r * row, 0));
         } else {
-            v.v.x = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at, r * row, 0));
-            v.v.y = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at + 4, r * row, 0));
+            v.v = make_float2(__uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, from, r * row, 0)), 0.0f);
         }
         return v;
     }
     __device__ __forceinline__ void store(int r, int nc, float a, float b) const {
         if constexpr (sizeof(T) == 2) {
             const uint32_t v = gdn::f32x2_to_bf16x2(a, b);
-            if (nc == 2) {
-                if constexpr (VEC) {
-                    __builtin_amdgcn_raw_buffer_store_b32(v, rs, at, r * row, 0);
-                } else {
-                    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)v, rs, at, r * row, 0);
-                    __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(v >> 16), rs, at + 2, r * row, 0);
-                }
-            }
+            if (PAIR && nc == 2) __builtin_amdgcn_raw_buffer_store_b32(v, rs, at, r * row, 0);
             if (odd && nc == 1) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)v, rs, at, r * row, 0);
         } else {
             const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
-            if (nc == 2) {
-                if constexpr (VEC) {
-                    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-                    __builtin_amdgcn_raw_buffer_store_b64((u32x2){x, y}, rs, at, r * row, 0);
-                } else {
-                    __builtin_amdgcn_raw_buffer_store_b32(x, rs, at, r * row, 0);
-                    __builtin_amdgcn_raw_buffer_store_b32(y, rs, at + 4, r * row, 0);
-                }
-            }
+            typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+            if (PAIR && nc == 2) __builtin_amdgcn_raw_buffer_store_b64((u32x2){x, y}, rs, at, r * row, 0);
             if (odd && nc == 1) __builtin_amdgcn_raw_buffer_store_b32(x, rs, at, r * row, 0);
         }
     }
 };
 
 // Rows as loaded in the column that ends with an odd count's last channel.
-template <typename T, bool VEC> __device__ __forceinline__ void fix_last(Raw2<T> (&v)[FR], int nc) {
-    if (nc != 1) return;
+template <typename T, bool PAIR> __device__ __forceinline__ void fix_last(Raw2<T> (&v)[FR], int nc) {
+    if (!PAIR || nc != 1) return;
 #pragma unroll
     for (int r = 0; r < FR; ++r) {
-        if constexpr (sizeof(T) == 2) v[r].v &= 0xffffu;
-        else v[r].v = make_float2(VEC ? v[r].v.y : v[r].v.x, 0.0f);
+        if constexpr (sizeof(T) == 2) v[r].v >>= 16;
+        else v[r].v = make_float2(v[r].v.y, 0.0f);
     }
 }
 

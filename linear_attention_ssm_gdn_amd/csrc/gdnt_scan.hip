@@ -309,8 +309,8 @@ template <typename T, bool VEC> static hipError_t forward_t(const ScanArgs& a, h
 hipError_t launch_scan_forward(const ScanArgs& a, hipStream_t s) {
     const hipError_t e = launch_map(scan_map_args(a), s);
     if (e != hipSuccess) return e;
-    if (a.act_dtype == GDN_BF16) return a.vec2 ? forward_t<bf16_t, true>(a, s) : forward_t<bf16_t, false>(a, s);
-    return a.vec2 ? forward_t<float, true>(a, s) : forward_t<float, false>(a, s);
+    if (a.act_dtype == GDN_BF16) return a.C > 1 ? forward_t<bf16_t, true>(a, s) : forward_t<bf16_t, false>(a, s);
+    return a.C > 1 ? forward_t<float, true>(a, s) : forward_t<float, false>(a, s);
 }
 
 }  // namespace gdnt

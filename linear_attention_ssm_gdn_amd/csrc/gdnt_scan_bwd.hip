@@ -572,8 +572,8 @@ template <typename T, bool VEC, bool CKPT> static hipError_t backward_t(const Sc
 }
 
 template <typename T> static hipError_t backward_d(const ScanArgs& a, hipStream_t s) {
-    if (a.q) return a.vec2 ? backward_t<T, true, true>(a, s) : backward_t<T, false, true>(a, s);
-    return a.vec2 ? backward_t<T, true, false>(a, s) : backward_t<T, false, false>(a, s);
+    if (a.q) return a.C > 1 ? backward_t<T, true, true>(a, s) : backward_t<T, false, true>(a, s);
+    return a.C > 1 ? backward_t<T, true, false>(a, s) : backward_t<T, false, false>(a, s);
 }
 
 hipError_t launch_scan_backward(const ScanArgs& a, hipStream_t s) {

@@ -49,6 +49,17 @@ def test_backward_of_many_tiles(C, ckpt):
     check_grads(c, c.backward(saved, from_ckpt=True), ora, x=v[0], a=v[1], b=v[2], before=rb)
 
 
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("C", [65, 129, 193, 255])
+def test_a_last_channel_of_its_own_column(C, act):
+    """Odd widths whose last channel begins a tile's column (and one in a column's last lane), rows on odd offsets."""
+    c = Case([300, 0, 5, 130], C, act, "f32", tail=20, pad=C % 4 - 1, seed=C)
+    saved = c.saved()
+    h, _, so = c.forward(saved)
+    check_forward(c, h, so, ora)
+    check_grads(c, c.backward(saved), ora)
+
+
 @pytest.mark.parametrize("act,state", [("bf16", "bf16"), ("f32", "f32")])
 def test_other_types_padding_gaps_tails_and_strides(act, state):
     """Padding sequences (their rows NaN: unread), rows before the first and behind the last sequence, padded rows
