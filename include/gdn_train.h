@@ -29,10 +29,10 @@
  *   pass hands the gradient of their final state or window through to the
  *   initial one, whatever has_init says.
  * - Any row stride from channels to 2^24 and any element-aligned pointer is
- *   accepted.  Rows on whole vectors are faster: on 4 bytes for the recurrence (any
- *   fp32 rows; bf16 rows of even stride), on four elements and in channels a
- *   multiple of 4 for the conv and the one-launch form.  Others are read and
- *   written element by element.
+ *   accepted.  Rows on whole vectors are faster: on 16 bytes and in channels a
+ *   multiple of 8 for the backward pass of the recurrence in bf16 (by 1.4), on
+ *   four elements and in channels a multiple of 4 for the conv and the
+ *   one-launch form (by 1.1 to 1.2).
  * - Inputs and outputs of one call must not overlap, but a state pool may be
  *   both state_in and state_out.
  * - workspace: 256-byte aligned device memory of at least the queried size,

@@ -31,7 +31,7 @@ size_t round_up(size_t v) { return (v + 255) / 256 * 256; }
 
 // Rows that start on their element's boundary, and on a 4-channel vector's
 // (the one-launch form takes 62 us over 1024 x 8 rows of 4096 bf16 channels on
-// the latter, 107 element by element; 64 rows take a launch's time either way).
+// the latter, 70 elsewhere; 64 rows take a launch's time either way).
 bool rows_ok(const void* p, int64_t stride, int64_t C, int32_t dt) {
     // a wave's rows are addressed by 32-bit byte offsets
     return p && stride >= C && stride <= (1 << 24) && aligned(p, (size_t)elem_size(dt));

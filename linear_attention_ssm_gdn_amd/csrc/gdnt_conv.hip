@@ -17,8 +17,9 @@
 //
 // Bound by memory: 32768 x 8192 in bf16 takes 340 us for 1.61 GB (4.7 TB/s, 93%
 // of a large copy's rate; 1.72 GB with what strips read twice, 5.0 TB/s) at 26
-// vector instructions an element.  VEC (rows on four elements): 373 us a call
-// there, 870 element by element; fp32 665 and 980; 2159 rows in bf16 44 and 78.
+// vector instructions an element.  VEC (rows on four elements) takes 372 us a
+// call there; others, through 64-bit addresses, 443 (fp32 662 and 790; 2159 rows
+// in bf16 44 and 48).
 #include "gdnt_device.hpp"
 
 namespace gdnt {

@@ -40,7 +40,8 @@ template <typename T> __device__ __forceinline__ Raw4<T> zero4() {
     return r;
 }
 
-// p: the first of the four channels; nc: how many of them exist (VEC: 4).
+// p: the first of the four channels; nc: how many of them exist.  VEC: four,
+// and p on a vector's boundary; else p on an element's.
 template <typename T, bool VEC> __device__ __forceinline__ Raw4<T> load4(const T* p, int nc) {
     Raw4<T> r = zero4<T>();
     if constexpr (VEC) {

@@ -49,7 +49,6 @@ struct ScanArgs {
     int32_t* map; uint32_t* ticket; uint64_t* chain; float* part;
     int32_t C, act_dtype, state_dtype;
     bool vec;                            // every row starts aligned for 4-channel vectors and C % 4 == 0
-    bool vec2;                           // every row starts on a dword (any C but 1)
     bool vec8;                           // backward: every row that is read starts on 16 bytes and C % 8 == 0
     int32_t* err;
 };

@@ -43,21 +43,21 @@ template <typename T> __device__ __forceinline__ Raw2<T> zero2() {
 // row r of the lane is r rows further down.  A buffer descriptor makes a row's
 // place a scalar offset and a lane's place one vector register for all rows
 // (32 bits: row strides end at 2^24 elements); it ends with the tensor.
-// PAIR: a lane's two channels move together, wherever the row starts (bf16
-// rows at odd offsets as dwords that no dword boundary holds: @ODD@).  Else there is only
-// one channel.  The lane with an odd count's last channel loads the one before
-// it and that one, so as to end with the row; fix_last puts the pair right.
-// The descriptor of such a column begins one channel earlier: its first lane
-// may be the one.
+// PAIR: a lane's two channels move together, wherever the row starts, for bf16
+// at odd offsets as dwords across dword boundaries (forward and backward over
+// 16692 rows take 590 us with 4095 bf16 channels, 576 with 4094; channel by
+// channel it was 1146).  Else there is only one channel.  The lane with an odd
+// count's last channel loads a pair all the same, with what is behind it (the
+// descriptor's end, or what fills the row); last_alone then loads that channel
+// alone, in the one column that has it.
 template <typename T, bool PAIR> struct WaveRows {
     __amdgpu_buffer_rsrc_t rs;
     uint32_t row, at;  // bytes
     bool odd;          // uniform: a lane here has one channel
     __device__ __forceinline__ WaveRows(const void* base, int64_t stride, int64_t n_rows, int64_t first, int32_t C,
                                         int64_t col, int64_t lane_at)
-        : row((uint32_t)stride * (uint32_t)sizeof(T)), odd((C & 1) && C - col < 128) {
-        if (PAIR && odd) { col -= 1; lane_at += 1; }
-        at = (uint32_t)lane_at * (uint32_t)sizeof(T);
+        : row((uint32_t)stride * (uint32_t)sizeof(T)), at((uint32_t)lane_at * (uint32_t)sizeof(T)),
+          odd((C & 1) && C - col < 128) {
         // where rows are walked tile after tile, keeps the rows' offsets from being held in registers
         asm volatile("" : "+s"(row));
         int64_t bytes = ((n_rows - 1 - first) * stride + C - col) * (int64_t)sizeof(T);
@@ -65,18 +65,27 @@ template <typename T, bool PAIR> struct WaveRows {
         rs = __builtin_amdgcn_make_buffer_rsrc(static_cast<T*>(const_cast<void*>(base)) + first * stride + col, 0,
                                                (uint32_t)bytes, 0x00020000);
     }
-    __device__ __forceinline__ Raw2<T> load(int r, int nc) const {
+    __device__ __forceinline__ Raw2<T> load(int r) const {
         Raw2<T> v;
-        const uint32_t from = PAIR && odd && nc == 1 ? at - (uint32_t)sizeof(T) : at;
-        if constexpr (sizeof(T) == 2) {
-            if constexpr (PAIR) v.v = __builtin_amdgcn_raw_buffer_load_b32(rs, from, r * row, 0);
-            else v.v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, from, r * row, 0);
-        } else if constexpr (PAIR) {
-            v.v = __builtin_bit_cast(float2, __builtin_amdgcn_raw_buffer_load_b64(rs, from, r * row, 0));
-        } else {
-            v.v = make_float2(__uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, from, r * row, 0)), 0.0f);
-        }
+        if constexpr (!PAIR) v = load_one(r);
+        else if constexpr (sizeof(T) == 2) v.v = __builtin_amdgcn_raw_buffer_load_b32(rs, at, r * row, 0);
+        else v.v = __builtin_bit_cast(float2, __builtin_amdgcn_raw_buffer_load_b64(rs, at, r * row, 0));
         return v;
+    }
+    __device__ __forceinline__ Raw2<T> load_one(int r) const {
+        Raw2<T> v;
+        if constexpr (sizeof(T) == 2) v.v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, at, r * row, 0);
+        else v.v = make_float2(__uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rs, at, r * row, 0)), 0.0f);
+        return v;
+    }
+    // rows: those of the lane that belong to a sequence, as bits
+    __device__ __forceinline__ void last_alone(Raw2<T> (&v)[FR], uint32_t rows, int nc) const {
+        if (!PAIR || !odd || nc != 1) return;
+#pragma unroll
+        for (int r = 0; r < FR; ++r)
+            if (rows >> r & 1u) v[r] = load_one(r);
+        // nothing left under way: where the ways join, waits count the first loads only
+        __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0)
     }
     __device__ __forceinline__ void store(int r, int nc, float a, float b) const {
         if constexpr (sizeof(T) == 2) {
@@ -91,16 +100,6 @@ template <typename T, bool PAIR> struct WaveRows {
         }
     }
 };
-
-// Rows as loaded in the column that ends with an odd count's last channel.
-template <typename T, bool PAIR> __device__ __forceinline__ void fix_last(Raw2<T> (&v)[FR], int nc) {
-    if (!PAIR || nc != 1) return;
-#pragma unroll
-    for (int r = 0; r < FR; ++r) {
-        if constexpr (sizeof(T) == 2) v[r].v >>= 16;
-        else v[r].v = make_float2(v[r].v.y, 0.0f);
-    }
-}
 
 // A block of the checkpoint (16 rows by 4 channels) is two neighbouring
 // lanes' values; each lane writes and reads eight whole rows of it (32 of its

@@ -15,8 +15,10 @@
 // 85% of what a large copy reaches), at 33 vector instructions an element
 // (52% of the issue slots) and with two workgroups on a compute unit, one
 // loading while the other walks; 301 us and 1.50 GB (5.0 TB/s) with the 8-bit
-// checkpoint, 64% of the slots.  30011 x 1001 in fp32 takes 130 us (3.7 TB/s):
-// its 8 columns leave the chain of 235 tiles in sight.
+// checkpoint, 64% of the slots.  fp32 fits in the same 128 registers
+// (two spilled with the checkpoint): 16692 x 4096 take 216 us, 266 with one
+// workgroup on a compute unit.  30011 x 1001 in fp32 takes 130 us (3.7 TB/s): its 8
+// columns leave the chain of 235 tiles in sight.
 #include "gdnt_chain.hpp"
 #include "gdnt_rows.hpp"
 
@@ -62,8 +64,8 @@ __device__ __forceinline__ void put_ckpt(const Raw2<T> (&v)[FR], int8_t* q, floa
     }
 }
 
-template <typename T, bool VEC, bool CKPT>
-__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void k_scan_forward(const ScanArgs A, int n_cols,
+template <typename T, bool PAIR, bool CKPT>
+__global__ __launch_bounds__(kThreads, 4) void k_scan_forward(const ScanArgs A, int n_cols,
                                                                                     int64_t n_tiles) {
     __shared__ float2 s_a[kWaves][64], s_u[kWaves][64], s_h[64];
     __shared__ uint32_t s_ticket;
@@ -83,32 +85,32 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2) void k_scan_forwa
     auto seq_of = [&](int r) { return __builtin_amdgcn_readlane(m16, r) >> 2; };
 
     const int64_t cb = (int64_t)col * kFwdCols;
-    const WaveRows<T, VEC> X(A.x, A.x_stride, A.n_rows, r0, A.C, cb, lane * 2),
+    const WaveRows<T, PAIR> X(A.x, A.x_stride, A.n_rows, r0, A.C, cb, lane * 2),
         Ag(A.a, A.ab_stride, A.n_rows, r0, A.C, cb, lane * 2), Bg(A.b, A.ab_stride, A.n_rows, r0, A.C, cb, lane * 2),
         H(A.h, A.h_stride, A.n_rows, r0, A.C, cb, lane * 2);
     Raw2<T> rx[FR], ra[FR], rb[FR];
     if (in == 0xffffu && nc > 0) {
 #pragma unroll
         for (int r = 0; r < FR; ++r) {
-            ra[r] = Ag.load(r, nc);
-            rx[r] = X.load(r, nc);
-            rb[r] = Bg.load(r, nc);
+            ra[r] = Ag.load(r);
+            rx[r] = X.load(r);
+            rb[r] = Bg.load(r);
         }
     } else {
 #pragma unroll
         for (int r = 0; r < FR; ++r) {
             rx[r] = zero2<T>(); ra[r] = zero2<T>(); rb[r] = zero2<T>();
             if ((in >> r & 1u) && nc > 0) {
-                ra[r] = Ag.load(r, nc);
-                rx[r] = X.load(r, nc);
-                rb[r] = Bg.load(r, nc);
+                ra[r] = Ag.load(r);
+                rx[r] = X.load(r);
+                rb[r] = Bg.load(r);
             }
         }
     }
     if ((A.C & 1) && col == n_cols - 1) {
-        fix_last<T, VEC>(rx, nc);
-        fix_last<T, VEC>(ra, nc);
-        fix_last<T, VEC>(rb, nc);
+        X.last_alone(rx, in, nc);
+        Ag.last_alone(ra, in, nc);
+        Bg.last_alone(rb, in, nc);
     }
     float dt[2], kk[2];
 #pragma unroll
@@ -294,15 +296,15 @@ hipError_t launch_scan_rows(const ScanArgs& a, hipStream_t s) {
     return a.vec ? rows_t<float, true>(a, s) : rows_t<float, false>(a, s);
 }
 
-template <typename T, bool VEC> static hipError_t forward_t(const ScanArgs& a, hipStream_t s) {
+template <typename T, bool PAIR> static hipError_t forward_t(const ScanArgs& a, hipStream_t s) {
     const int nc = (int)((a.C + kFwdCols - 1) / kFwdCols);
     const int64_t nt = (a.n_rows + kFwdRows - 1) / kFwdRows, grid = nt * nc;
     if (grid == 0) return hipSuccess;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
     if (a.q)
-        hipLaunchKernelGGL((k_scan_forward<T, VEC, true>), dim3((unsigned)grid), dim3(kThreads), 0, s, a, nc, nt);
+        hipLaunchKernelGGL((k_scan_forward<T, PAIR, true>), dim3((unsigned)grid), dim3(kThreads), 0, s, a, nc, nt);
     else
-        hipLaunchKernelGGL((k_scan_forward<T, VEC, false>), dim3((unsigned)grid), dim3(kThreads), 0, s, a, nc, nt);
+        hipLaunchKernelGGL((k_scan_forward<T, PAIR, false>), dim3((unsigned)grid), dim3(kThreads), 0, s, a, nc, nt);
     return hipGetLastError();
 }
 

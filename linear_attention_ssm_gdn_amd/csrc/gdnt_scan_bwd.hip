@@ -107,7 +107,7 @@ __device__ __forceinline__ const __attribute__((address_space(4))) ScanArgs* rar
 // while this one is computed.  For bf16 rows on 16 bytes and channels a
 // multiple of 8: forward and backward over 16692 rows take 414 us with 4096
 // channels, 577 with 4094, which go without (fp32 rows would not fit in LDS).
-template <typename T, bool VEC, bool CKPT, bool PIPE>
+template <typename T, bool PAIR, bool CKPT, bool PIPE>
 __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A, int n_cols, int64_t n_tiles) {
     __shared__ float2 s_a[kWaves][32], s_u[kWaves][32], s_ra[kWaves][32], s_ru[kWaves][32], s_h[32];
     __shared__ float2 s_s1[kWaves][32], s_s2[kWaves][32];
@@ -224,10 +224,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
         auto seq_of = [&](int r) { return __shfl(m32, half * FR + r) >> 2; };  // all lanes together
 
         auto rows = [&](const void* base, int64_t stride) {
-            return WaveRows<T, VEC>(base, stride, A.n_rows, r0, A.C, cb, half * FR * stride + hl * 2);
+            return WaveRows<T, PAIR>(base, stride, A.n_rows, r0, A.C, cb, half * FR * stride + hl * 2);
         };
         const bool whole = in == 0xffffffffu;
-        const WaveRows<T, VEC> D = rows(A.dh, A.dh_stride);
+        const WaveRows<T, PAIR> D = rows(A.dh, A.dh_stride);
         Raw2<T> rd[FR], rx[FR], ra[FR], rb[FR];
         Ckpt2 qx, qa, qb;
         if (PIPE && whole) {
@@ -273,14 +273,14 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
                 getq(2, qb);
                 getq(0, qx);
             }
-            const WaveRows<T, VEC> X = rows(A.x, A.x_stride), Ag = rows(A.a, A.ab_stride), Bg = rows(A.b, A.ab_stride);
+            const WaveRows<T, PAIR> X = rows(A.x, A.x_stride), Ag = rows(A.a, A.ab_stride), Bg = rows(A.b, A.ab_stride);
             auto row = [&](int r) {
                 if constexpr (!CKPT) {
-                    ra[r] = Ag.load(r, nc);
-                    rb[r] = Bg.load(r, nc);
-                    rx[r] = X.load(r, nc);
+                    ra[r] = Ag.load(r);
+                    rb[r] = Bg.load(r);
+                    rx[r] = X.load(r);
                 }
-                rd[r] = D.load(r, nc);
+                rd[r] = D.load(r);
             };
             if (whole && nc > 0) {  // no branch between the rows: all loads go out at once
 #pragma unroll
@@ -293,13 +293,13 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
                     if ((my_in >> r & 1u) && nc > 0) row(r);
                 }
             }
-        }
-        if ((A.C & 1) && col == n_cols - 1) {
-            fix_last<T, VEC>(rd, nc);
-            if constexpr (!CKPT) {
-                fix_last<T, VEC>(rx, nc);
-                fix_last<T, VEC>(ra, nc);
-                fix_last<T, VEC>(rb, nc);
+            if ((A.C & 1) && col == n_cols - 1) {
+                D.last_alone(rd, my_in, nc);
+                if constexpr (!CKPT) {
+                    Ag.last_alone(ra, my_in, nc);
+                    Bg.last_alone(rb, my_in, nc);
+                    X.last_alone(rx, my_in, nc);
+                }
             }
         }
         float dtb[2], kk[2], h[2];  // h: the kept state
@@ -479,7 +479,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
             else again(qx.w[r & 7]);
         }
         // third walk: the gradients, from the last row to the first
-        const WaveRows<T, VEC> DX = rows(A.dx, A.dx_stride), DA = rows(A.da, A.dab_stride), DB = rows(A.db, A.dab_stride);
+        const WaveRows<T, PAIR> DX = rows(A.dx, A.dx_stride), DA = rows(A.da, A.dab_stride), DB = rows(A.db, A.dab_stride);
         const float kg[2] = {kk[0] / kLog2e, kk[1] / kLog2e};
         float s1[2] = {}, s2[2] = {};  // sums of dg y and of dg sigmoid(z)
 #pragma unroll
@@ -556,16 +556,16 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
 // With the stage, one workgroup for each of MI355X's 256 compute units: they draw tiles.
 constexpr int64_t kGroups = 256;
 
-template <typename T, bool VEC, bool CKPT> static hipError_t backward_t(const ScanArgs& a, hipStream_t s) {
+template <typename T, bool PAIR, bool CKPT> static hipError_t backward_t(const ScanArgs& a, hipStream_t s) {
     const int nc = (int)(padded_channels(a.C) / kTileCols);
     const int64_t nt = n_tiles(a.n_rows), grid = nt * nc;
     if (grid > 0x7fffffff) return hipErrorInvalidValue;
     if (grid > 0) {
-        if (sizeof(T) == 2 && VEC && a.vec8)
-            hipLaunchKernelGGL((k_scan_backward<T, VEC, CKPT, sizeof(T) == 2 && VEC>),
+        if (sizeof(T) == 2 && PAIR && a.vec8)
+            hipLaunchKernelGGL((k_scan_backward<T, PAIR, CKPT, sizeof(T) == 2 && PAIR>),
                                dim3((unsigned)(grid < kGroups ? grid : kGroups)), dim3(kThreads), 0, s, a, nc, nt);
         else
-            hipLaunchKernelGGL((k_scan_backward<T, VEC, CKPT, false>), dim3((unsigned)grid), dim3(kThreads), 0, s, a,
+            hipLaunchKernelGGL((k_scan_backward<T, PAIR, CKPT, false>), dim3((unsigned)grid), dim3(kThreads), 0, s, a,
                                nc, nt);
     }
     return launch_sum_tiles(a.part, nt, a.C, 2, a.d_a_log, a.d_dt_bias, s);
