@@ -293,7 +293,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
                     if ((my_in >> r & 1u) && nc > 0) row(r);
                 }
             }
-            if ((A.C & 1) && col == n_cols - 1) {
+            if (!PIPE && (A.C & 1) && col == n_cols - 1) {
                 D.last_alone(rd, my_in, nc);
                 if constexpr (!CKPT) {
                     Ag.last_alone(ra, my_in, nc);

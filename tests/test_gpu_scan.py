@@ -60,6 +60,18 @@ def test_a_last_channel_of_its_own_column(C, act):
     check_grads(c, c.backward(saved), ora)
 
 
+@pytest.mark.parametrize("rows", [1, 31, 32, 273])
+@pytest.mark.parametrize("pad,offset", [(0, 1), (1, 0), (1, 1)])
+def test_pairs_that_end_with_the_tensor(rows, pad, offset):
+    """bf16 rows on odd offsets, the last row's last pair the tensor's end."""
+    for C in (66, 128, 67):
+        c = Case([rows], C, "bf16", "f32", pad=pad, offset=offset, seed=rows)
+        saved = c.saved()
+        h, _, so = c.forward(saved)
+        check_forward(c, h, so, ora)
+        check_grads(c, c.backward(saved), ora)
+
+
 @pytest.mark.parametrize("act,state", [("bf16", "bf16"), ("f32", "f32")])
 def test_other_types_padding_gaps_tails_and_strides(act, state):
     """Padding sequences (their rows NaN: unread), rows before the first and behind the last sequence, padded rows
