@@ -441,6 +441,59 @@ def test_two_streams_with_workspaces_of_their_own():
         assert torch.equal(h, want[0] if c is c1 else want[1])
 
 
+def test_backward_calls_on_two_streams_at_once():
+    """More tiles than the GPU holds workgroups, from both calls, with what each waits for in the other's way."""
+    g = gdn()
+    cs = [Case([5000, 3000, 200], 4096, "bf16", "f32", seed=s) for s in (51, 52)]
+    saved = [c.saved(ckpt=True) for c in cs]
+    for c, sv in zip(cs, saved):
+        c.forward(sv)
+    want = [c.backward(sv, from_ckpt=bool(i)) for i, (c, sv) in enumerate(zip(cs, saved))]
+    pools = [g.StatePool(c.h0.to(DEV)) for c in cs]
+    ds = [torch.from_numpy(c.d_state).to(DEV) for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        for i, (c, s) in enumerate(zip(cs, streams)):
+            with torch.cuda.stream(s):
+                xab = {} if i else {k: c.t[k] for k in "xab"}
+                got.append((i, g.gdnt_scan_backward(c.dims, c.params, c.batch, pools[i], saved[i], c.t["dh"],
+                                                    d_state=ds[i], **xab)))
+    torch.cuda.synchronize()
+    for i, out in got:
+        assert all(torch.equal(p, q) for p, q in zip(out, want[i]))
+
+
+def test_decode_steps_replayed_from_a_graph_in_place():
+    """The one-launch form with states in place: each replay goes on from the states the last one left."""
+    g = gdn()
+    c = Case([1] * 9 + [0, 2], 260, "bf16", "f32", skip=(4,), seed=43)
+    b = g.Batch(c.batch.cu_seqlens, c.batch.page_idx, None, 2, c.rows)
+    pool, ref = g.StatePool(c.h0.to(DEV)), g.StatePool(c.h0.to(DEV))
+    h, want = c.empty_rows(), c.empty_rows()
+    step = lambda p, out: g.gdnt_scan_forward(c.dims, c.params, c.t["x"], c.t["a"], c.t["b"], b, p, h=out)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step(pool, h)
+    step(ref, want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(pool, h)
+    own = torch.from_numpy(c.owned).to(DEV)
+    gen = torch.Generator().manual_seed(2)
+    for _ in range(4):
+        for name in ("x", "a", "b"):
+            c.t[name].copy_(torch.randn(c.rows, c.C, generator=gen).to(torch.bfloat16))
+        step(ref, want)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(pool.buf, ref.buf) and torch.equal(h[own], want[own])
+        assert torch.isnan(h[~own]).all()
+
+
 def test_a_training_step_replayed_from_a_graph():
     """Forward with a checkpoint and backward captured once and replayed over changing inputs, eager work and
     synchronisations between: every replay equals the eager calls bit for bit."""
