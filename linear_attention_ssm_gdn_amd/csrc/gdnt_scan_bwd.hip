@@ -503,7 +503,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
                 const float dg = mine ? mu[i] * hp[r][i] : 0.0f;
                 const float ds = dg * sg[r][i];
                 dx[i] = be[r][i] * lam[i];
-                db[i] = dx[i] * get_x(r, i) * (1.0f - be[r][i]);
+                // in this order nothing overflows on the way: beta lambda (1 - beta) is smaller than lambda
+                db[i] = dx[i] * (1.0f - be[r][i]) * get_x(r, i);
                 da[i] = ds * kg[i];
                 s1[i] = fmaf(dg, y[r][i], s1[i]);
                 s2[i] += ds;
