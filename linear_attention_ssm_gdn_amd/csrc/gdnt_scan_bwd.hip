@@ -31,20 +31,29 @@ constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * 64;
 static_assert(kWaves * 2 * FR == kTileRows && 32 * 2 == kTileCols, "tile shape");
 
+// The largest scale whose 127-fold is finite: that of a block around the
+// largest fp32 number is one step above it.
+constexpr float kTopScale = 0x1.020406p+121f;
+
 // The lane's 16 rows by two channels of one tensor of the checkpoint.
+// A value is taken by half: byte * (sc / 2) - 64 sc, the byte unsigned (offset
+// by 128), in one fused operation.  64 sc is exact and finite for every scale,
+// while 128 sc is not for a block that holds the largest numbers, and halving
+// and doubling change no digit, so what is rounded is q * scale / 2.
 struct Ckpt2 {
     uint32_t w[FR / 2];
-    float sc, off;  // value = byte * sc + off, the byte unsigned (offset by 128)
-    // eight whole rows of the block, as this lane stored them; sc is set
+    float sc, off;
+    // eight whole rows of the block, as this lane stored them; sc is set to the scale
     __device__ __forceinline__ void set(uint4 lo, uint4 hi, int lane) {
         const uint32_t v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        sc = 0.5f * (sc > kTopScale ? kTopScale : sc);  // a NaN stays
         off = -128.0f * sc;
 #pragma unroll
         for (int r = 0; r < FR / 2; ++r) w[r] = swap_halves(v[r], lane) ^ 0x80808080u;
     }
-    __device__ __forceinline__ float get(int r, int i) const {
+    __device__ __forceinline__ float half(int r, int i) const {
         const uint32_t b = (w[r & 7] >> ((r >> 3) * 16 + i * 8)) & 0xffu;
-        return fmaf((float)b, sc, off);  // 128 * sc is exact: one rounding, that of q * sc
+        return fmaf((float)b, sc, off);
     }
 };
 
@@ -320,7 +329,8 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
             kk[i] = i < nc ? -expf(al) * kLog2e : 0.0f;
             h[i] = cont && i < nc ? h[i] : 0.0f;
         }
-        auto get_x = [&](int r, int i) { return CKPT ? qx.get(r, i) : rx[r].get(i); };
+        // x, or half of it beside twice beta: the product is beta x either way
+        auto get_x = [&](int r, int i) { return CKPT ? qx.half(r, i) : rx[r].get(i); };
 
         // the state a sequence starts from (seq -1: none)
         auto initial = [&](int seq, float (&h0)[2]) {
@@ -336,7 +346,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
             return R->d_state && i < nc ? R->d_state[(int64_t)seq * R->C + c0 + i] : 0.0f;
         };
 
-        // first walk: y = g log2(e), sigmoid(z), beta, and the rows' run.  Rows of
+        // first walk: y = g log2(e), sigmoid(z), beta (twice it from the checkpoint), and the rows' run.  Rows of
         // no sequence run along on zeros (see the forward pass).
         float y[FR][2], sg[FR][2], be[FR][2];
         // The run from the last row to the first, mu -> fa mu + fu, is gathered on the
@@ -349,11 +359,12 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 float t;
-                const float z = (CKPT ? qa.get(r, i) : ra[r].get(i)) + dtb[i];
+                const float z = CKPT ? fmaf(2.0f, qa.half(r, i), dtb[i]) : ra[r].get(i) + dtb[i];
                 y[r][i] = kk[i] * softplus_t(spc, z, t);
                 const float s = rcp(1.0f + t);
                 sg[r][i] = z >= 0.0f ? s : t * s;
-                be[r][i] = sigmoid_hw(CKPT ? qb.get(r, i) : rb[r].get(i));
+                if constexpr (CKPT) be[r][i] = rcp(fmaf(0.5f, exp2_hw(qb.half(r, i) * (-2.0f * kLog2e)), 0.5f));
+                else be[r][i] = sigmoid_hw(rb[r].get(i));
                 const float al = exp2_hw(y[r][i]), u = be[r][i] * get_x(r, i);
                 eu[i] = fmaf(al, eu[i], u);
                 ea[i] *= al;
@@ -502,9 +513,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
                 mu[i] = exp2_hw(y[r][i]) * lam[i];
                 const float dg = mine ? mu[i] * hp[r][i] : 0.0f;
                 const float ds = dg * sg[r][i];
-                dx[i] = be[r][i] * lam[i];
+                const float beta = CKPT ? 0.5f * be[r][i] : be[r][i];
+                dx[i] = beta * lam[i];
                 // in this order nothing overflows on the way: beta lambda (1 - beta) is smaller than lambda
-                db[i] = dx[i] * (1.0f - be[r][i]) * get_x(r, i);
+                db[i] = dx[i] * ((CKPT ? 2.0f : 1.0f) - be[r][i]) * get_x(r, i);
                 da[i] = ds * kg[i];
                 s1[i] = fmaf(dg, y[r][i], s1[i]);
                 s2[i] += ds;

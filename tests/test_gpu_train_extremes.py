@@ -8,6 +8,7 @@ import torch
 
 import oracle.train as ora
 from gpu_util import DEV, gdn, host
+from test_gpu_scan import decode
 from train_util import DT, Case, check_forward, check_grads
 
 pytestmark = pytest.mark.gpu
@@ -17,13 +18,21 @@ def largest(act, sign):
     return sign * torch.finfo(DT[act]).max
 
 
-def check_step(c):
-    """Forward and backward against the oracle."""
-    saved = c.saved()
+def check_step(c, ckpt=False):
+    """Forward and backward against the oracle, from the activations or at the values the 8 bits stand for."""
+    saved = c.saved(ckpt=ckpt)
     h, _, so = c.forward(saved)
     check_forward(c, h, so, ora)
-    out = c.backward(saved)
-    check_grads(c, out, ora)
+    out = c.backward(saved, from_ckpt=ckpt)
+    if not ckpt:
+        check_grads(c, out, ora)
+        return
+    v, _, _ = decode(c, saved)
+    assert np.isfinite(v[:, c.owned]).all()
+    with np.errstate(invalid="ignore", over="ignore"):
+        before = ora.scan(c.f64("x"), c.f64("a"), c.f64("b"), c.a_log, c.dt_bias, c.spans, c.seq_h0())[2]
+        rb = ora.rebuilt(v[0], v[1], v[2], c.a_log, c.dt_bias, c.spans, before)
+    check_grads(c, out, ora, x=v[0], a=v[1], b=v[2], before=rb)
 
 
 @pytest.mark.parametrize("C", [64, 66])
@@ -39,3 +48,17 @@ def test_products_with_the_largest_x(act, C):
         c.t["dh"][r + 1:end, ch] = 0.0
         c.d_state[int(r > 299), ch] = 0.0
     check_step(c)
+
+
+@pytest.mark.parametrize("C", [64, 66])
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("name,sign", [("x", -1), ("x", 1), ("a", -1), ("b", -1), ("b", 1)])
+def test_checkpoint_of_the_largest_numbers(name, sign, act, C):
+    """The lowest and the largest number of the type in 8 bits: its block's other values are stored as zeros, all of
+    them finite, and the gradients are those at the stored values (64 channels: whole tiles loaded ahead in bf16)."""
+    c = Case([300, 290], C, act, "f32", seed=61)
+    for r, ch in ((5, 2), (200, 33), (303, C - 1)):
+        c.t[name][r, ch] = largest(act, sign)
+        if name == "x":
+            c.t["b"][r, ch] = -60.0  # an update of 3e12, so that h and what follows from it stay in range
+    check_step(c, True)
