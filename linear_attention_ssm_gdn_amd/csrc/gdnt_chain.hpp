@@ -15,7 +15,13 @@
 namespace gdnt {
 
 // A run that contains a first row (in the direction of the recurrence) is
-// marked by a negative `a`: nothing before it matters.
+// marked by a negative `a`: nothing before it matters.  The mark comes from the
+// row map alone, never from the sign of what was computed: a NaN gate's sign
+// says nothing, and a tile's channels have to agree (end_known).
+__device__ __forceinline__ float marked(float a, bool first) {
+    const float m = fmaxf(a, kTiny);  // a decay, so a >= 0; a NaN becomes kTiny, and is in u as well
+    return first ? -m : m;
+}
 __device__ __forceinline__ float walk(float a, float u, float h) { return a < 0.0f ? u : fmaf(a, h, u); }
 // first `p`, then `q`, into q.  |a| stays a normal number, so an Inf passes
 // through a run whose decays underflow as Inf, not as NaN; a finite state is

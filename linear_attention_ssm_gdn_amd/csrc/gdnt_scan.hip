@@ -152,12 +152,11 @@ __global__ __launch_bounds__(kThreads, 4) void k_scan_forward(const ScanArgs A, 
             for (int i = 0; i < 2; ++i) {
                 if (init && i < nc) u[r][i] = fmaf(al[r][i], load_state(A.st_in, at + i, A.state_dtype), u[r][i]);
                 eu[i] = u[r][i];
-                ea[i] = -1.0f;
             }
         }
     }
 #pragma unroll
-    for (int i = 0; i < 2; ++i) ea[i] = copysignf(fmaxf(fabsf(ea[i]), kTiny), ea[i]);
+    for (int i = 0; i < 2; ++i) ea[i] = marked(ea[i], firsts != 0);
     s_a[wave][lane] = make_float2(ea[0], ea[1]);
     s_u[wave][lane] = make_float2(eu[0], eu[1]);
     __syncthreads();

@@ -385,18 +385,15 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
                 initial(seq_of(r), h0);
                 if (my_firsts >> r & 1u) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        eu[i] = fmaf(exp2_hw(y[r][i]), h0[i], be[r][i] * get_x(r, i));
-                        ea[i] = -1.0f;
-                    }
+                    for (int i = 0; i < 2; ++i) eu[i] = fmaf(exp2_hw(y[r][i]), h0[i], be[r][i] * get_x(r, i));
                 }
             }
         }
         float xa[2], xu[2], ya[2], yu[2];  // the run of the wave's other half
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            ea[i] = copysignf(fmaxf(fabsf(ea[i]), kTiny), ea[i]);
-            fa[i] = ended ? -1.0f : fmaxf(fa[i], kTiny);
+            ea[i] = marked(ea[i], (my_firsts & 0xffffu) != 0);
+            fa[i] = marked(fa[i], ended);
             xa[i] = __shfl_xor(ea[i], 32);
             xu[i] = __shfl_xor(eu[i], 32);
             ya[i] = __shfl_xor(fa[i], 32);

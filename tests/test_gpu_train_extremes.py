@@ -62,3 +62,62 @@ def test_checkpoint_of_the_largest_numbers(name, sign, act, C):
         if name == "x":
             c.t["b"][r, ch] = -60.0  # an update of 3e12, so that h and what follows from it stay in range
     check_step(c, True)
+
+
+def nan_of(dt, sign):
+    """A quiet NaN of the type with its sign bit as asked."""
+    if dt == torch.bfloat16:
+        return torch.tensor([0x7FC0 - (1 << 15 if sign < 0 else 0)], dtype=torch.int16).view(dt)[0]
+    return torch.tensor([0x7FC00000 - (1 << 31 if sign < 0 else 0)], dtype=torch.int32).view(dt)[0]
+
+
+def put(c, name, rows, channels, value):
+    """`value` at the given places of one input of c; parameters and states have a channel alone to place it in."""
+    for ch in channels:
+        if name == "state":
+            c.h0[int(c.pages[1]), ch] = value
+        elif name in ("a_log", "dt_bias"):
+            getattr(c.params, name)[ch] = value
+            getattr(c, name)[ch] = float(value)
+        elif name == "d_state":
+            c.d_state[1, ch] = float(value)
+        else:
+            for r in rows:
+                c.t[name][r, ch] = value
+
+
+def same(p, q):
+    """Bit for bit, NaNs for NaNs."""
+    p, q = p.detach().cpu(), q.detach().cpu()
+    return bool(((p == q) | (torch.isnan(p) & torch.isnan(q))).all())
+
+
+def results(c, ckpt):
+    saved = c.saved(ckpt=ckpt)
+    h, _, so = c.forward(saved)
+    return h, so.buf, saved.states, *c.backward(saved, from_ckpt=ckpt)
+
+
+# The tiles of the forward pass are 128 rows, a wave's 16: the second sequence begins at row 200, inside a tile that
+# goes on from the first one and in the same 16 rows as row 203, and goes on into the next tiles; 300 and 410 lie in
+# tiles without a first row.
+NAN_LENS, NAN_ROWS = [200, 400, 90], (203, 300, 410)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ["x", "a", "b", "a_log", "dt_bias", "state", "dh", "d_state"])
+def test_a_nan_stays_in_its_sequence_and_channel(name, act, sign):
+    """Everything else keeps its bits; in the channel itself NaNs stand where the formulas have them, both ways."""
+    C, channels = 72, (6, 33, 70)
+    where = (203,) if sign > 0 else (300,)
+    for rows in (where, NAN_ROWS):
+        c, clean = (Case(NAN_LENS, C, act, "f32", seed=63) for _ in range(2))
+        put(c, name, rows, channels, nan_of(DT[act] if name in ("x", "a", "b", "dh") else torch.float32, sign))
+        rest = [k for k in range(C) if k not in channels]
+        for got, want in zip(results(c, False), results(clean, False)):
+            assert same(got[..., rest], want[..., rest])
+        saved = c.saved()
+        h, _, so = c.forward(saved)
+        check_forward(c, h, so, ora)
+        check_grads(c, c.backward(saved), ora)
