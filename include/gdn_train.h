@@ -36,7 +36,8 @@
  * - Inputs and outputs of one call must not overlap, but a state pool may be
  *   both state_in and state_out.
  * - workspace: 256-byte aligned device memory of at least the queried size,
- *   ignored on entry, scratch on return.  Calls that share one workspace
+ *   ignored on entry, scratch on return.  The size queried for a number of
+ *   rows serves every call with the same dims and no more rows.  Calls that share one workspace
  *   must be ordered (same stream, or events); graphs captured over one
  *   workspace likewise.
  * - All arithmetic is fp32 (sums over rows of a parameter's gradient: fp32
@@ -78,7 +79,7 @@ typedef struct gdnt_scan_params {
 /* ------------------------------------------------------------ queries */
 
 /* Bytes of workspace gdnt_scan_forward and gdnt_scan_backward need for a
- * batch of this shape (the same for both; host-only). */
+ * batch of up to n_rows rows (the same for both; host-only). */
 int32_t gdnt_scan_workspace_bytes(const gdnt_scan_dims* dims, int32_t n_seqs, int64_t n_rows, size_t* out_bytes);
 
 /* Bytes of what a forward call keeps for its backward call (host-only):
@@ -86,7 +87,8 @@ int32_t gdnt_scan_workspace_bytes(const gdnt_scan_dims* dims, int32_t n_seqs, in
  * *ckpt_bytes for the 8-bit checkpoint.  Either pointer may be NULL. */
 int32_t gdnt_scan_saved_bytes(const gdnt_scan_dims* dims, int64_t n_rows, size_t* states_bytes, size_t* ckpt_bytes);
 
-/* Bytes of workspace gdnt_conv_backward needs (host-only). */
+/* Bytes of workspace gdnt_conv_backward needs for a batch of up to n_rows
+ * rows (host-only). */
 int32_t gdnt_conv_workspace_bytes(const gdn_dims* dims, int32_t n_seqs, int64_t n_rows, size_t* out_bytes);
 
 /* ------------------------------------------- gated linear recurrence */

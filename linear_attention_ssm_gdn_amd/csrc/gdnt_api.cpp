@@ -78,6 +78,12 @@ ScanWs scan_ws(int64_t n_rows, int64_t C) {
     return w;
 }
 
+// Conv workspace: row map, partial sums of `tiles` tiles.
+size_t conv_ws(int64_t n_rows, int64_t C, int64_t tiles) {
+    return round_up((size_t)n_tiles(n_rows) * gdnt::kTileRows * sizeof(int32_t) +
+                    (size_t)tiles * 4 * (size_t)padded_channels(C) * sizeof(float));
+}
+
 size_t states_bytes(int64_t n_rows, int64_t C) { return (size_t)n_tiles(n_rows) * (size_t)C * sizeof(float); }
 int64_t ckpt_blocks(int64_t n_rows, int64_t C) {
     return (n_rows + GDNT_CKPT_ROWS - 1) / GDNT_CKPT_ROWS * 3 * (padded_channels(C) / GDNT_CKPT_CHANNELS);
@@ -133,8 +139,7 @@ GDN_EXPORT int32_t gdnt_conv_workspace_bytes(const gdn_dims* dims, int32_t n_seq
     if (!out_bytes || n_seqs < 0) return GDN_ERR_ARG;
     const int64_t C = 2 * (int64_t)dims->h_k * dims->d_k + (int64_t)dims->h_v * dims->d_v;
     if ((st = check_size(n_rows, C)) != GDN_OK) return st;
-    *out_bytes = round_up((size_t)n_tiles(n_rows) * gdnt::kTileRows * sizeof(int32_t) +
-                          (size_t)gdnt::conv_tiles(n_rows, C) * 4 * (size_t)padded_channels(C) * sizeof(float));
+    *out_bytes = conv_ws(n_rows, C, gdnt::conv_tiles_up_to(n_rows, C));
     return GDN_OK;
 }
 
@@ -236,9 +241,7 @@ GDN_EXPORT int32_t gdnt_conv_backward(const gdn_dims* dims, const void* conv_w, 
             return GDN_ERR_ARG;
         if (!workspace || !aligned(workspace, 256)) return GDN_ERR_ARG;
     }
-    size_t need = 0;
-    if ((st = gdnt_conv_workspace_bytes(dims, bt.n_seqs, bt.n_rows, &need)) != GDN_OK) return st;
-    if (ws_bytes < need) return GDN_ERR_ARG;
+    if (ws_bytes < conv_ws(bt.n_rows, C, gdnt::conv_tiles(bt.n_rows, C))) return GDN_ERR_ARG;
     gdnt::ConvBwdArgs A{};
     A.x = x; A.x_stride = x_stride; A.dy = dy; A.dy_stride = dy_stride; A.n_rows = bt.n_rows;
     A.cu = bt.cu_seqlens; A.page_idx = bt.page_idx; A.has_init = bt.has_init; A.n_seqs = bt.n_seqs;

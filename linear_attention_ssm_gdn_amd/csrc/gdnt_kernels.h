@@ -77,15 +77,29 @@ constexpr int kConvCols = 256;
 // rows of one are walked one after the other: 57, 25, 13 rows take 374, 398,
 // 474 us over 32768 x 8192 channels (18400 strips of 57), 55, 47, 54 us over
 // 2159 x 8192 (1216, 2784, 5344 strips) and 54, 39, 31 us over 2066 x 672.
+constexpr int kConvOwn[3] = {57, 25, 13};
+// The fewest rows (of this many columns) for which there are enough strips of `own` rows.
+inline int64_t conv_rows_from(int own, int64_t nc) { return ((2048 + nc - 1) / nc - 1) * own + 1; }
 inline int conv_rows(int64_t n_rows, int64_t C) {
     const int64_t nc = (C + kConvCols - 1) / kConvCols;
-    for (int own : {57, 25})
-        if ((n_rows + own - 1) / own * nc >= 2048) return own;
-    return 13;
+    for (int i = 0; i < 2; ++i)
+        if (n_rows >= conv_rows_from(kConvOwn[i], nc)) return kConvOwn[i];
+    return kConvOwn[2];
 }
 inline int64_t conv_tiles(int64_t n_rows, int64_t C) {
     const int64_t rows = kConvWaves * conv_rows(n_rows, C);
     return (n_rows + rows - 1) / rows;
+}
+// The most tiles that a batch of up to n_rows rows has: a batch just too small
+// for longer strips has more of them than one just large enough.
+inline int64_t conv_tiles_up_to(int64_t n_rows, int64_t C) {
+    const int64_t nc = (C + kConvCols - 1) / kConvCols;
+    int64_t most = conv_tiles(n_rows, C);
+    for (int i = 0; i < 2; ++i) {
+        const int64_t below = conv_rows_from(kConvOwn[i], nc) - 1;
+        if (below < n_rows && conv_tiles(below, C) > most) most = conv_tiles(below, C);
+    }
+    return most;
 }
 
 hipError_t launch_map(const MapArgs& a, hipStream_t s);
