@@ -40,6 +40,8 @@
  *   rows serves every call with the same dims and no more rows.  Calls that share one workspace
  *   must be ordered (same stream, or events); graphs captured over one
  *   workspace likewise.
+ * - An infinite a or b stands for its limit (e^g and beta are 0 or 1, with no
+ *   gradient through them).
  * - All arithmetic is fp32 (sums over rows of a parameter's gradient: fp32
  *   within 256 rows, fp64 across them); results do not depend on timing.  A
  *   state that is not finite stays so to the end of its sequence, whether as

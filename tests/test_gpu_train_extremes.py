@@ -121,3 +121,25 @@ def test_a_nan_stays_in_its_sequence_and_channel(name, act, sign):
         h, _, so = c.forward(saved)
         check_forward(c, h, so, ora)
         check_grads(c, c.backward(saved), ora)
+
+
+@pytest.mark.parametrize("ckpt", [False, True])
+@pytest.mark.parametrize("C", [64, 66])
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_the_largest_decay_gates(act, C, ckpt):
+    """a at the largest number forgets the state: every gradient is a number, d_a_log (0 times a g beyond fp32) too."""
+    c = Case([300, 290], C, act, "f32", seed=64)
+    for r, ch in ((5, 2), (200, 33), (303, C - 1)):
+        c.t["a"][r, ch] = largest(act, 1)
+    check_step(c, ckpt)
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_infinite_gates_are_their_limits(act):
+    """An infinite a or b gives what a gate far out gives, bit for bit, in h, the states and every gradient."""
+    far, inf = (Case([300, 290], 72, act, "f32", seed=65) for _ in range(2))
+    for name, r, ch, sign in (("a", 5, 2, 1), ("a", 203, 33, -1), ("b", 300, 8, 1), ("b", 400, 71, -1)):
+        far.t[name][r, ch] = 1e6 * sign
+        inf.t[name][r, ch] = float("inf") * sign
+    for p, q in zip(results(far, False), results(inf, False)):
+        assert same(p, q)
