@@ -64,7 +64,9 @@ extern "C" {
 #define GDNT_CKPT_CHANNELS 4
 
 /* Sticky device error bit beside those of gdn.h: a wait inside a kernel ran
- * into its bound and the call's results are not valid. */
+ * into its bound and the call's results are not valid.  What the wait was for
+ * counts as NaN, so the rows, states and gradients that hang on it are NaNs,
+ * also where err is NULL. */
 #define GDNT_DEVERR_TIMEOUT 32u
 
 typedef struct gdnt_scan_dims {

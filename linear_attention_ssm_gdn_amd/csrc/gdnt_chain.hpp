@@ -94,9 +94,10 @@ __device__ __forceinline__ void look_back(const Chain& C, int64_t at, int64_t st
         }
         __builtin_amdgcn_s_sleep(2);
     }
+    // not a number from here on: whoever does not look at err sees it in the results
     raise(err, GDNT_DEVERR_TIMEOUT);
 #pragma unroll
-    for (int i = 0; i < NCH; ++i) h[i] = 0.0f;
+    for (int i = 0; i < NCH; ++i) h[i] = __uint_as_float(0x7fc00000u);
 }
 
 // A tile with a first row in it, or that continues nothing, knows its end from
