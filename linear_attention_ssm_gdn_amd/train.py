@@ -5,6 +5,13 @@ As in ops.py every function checks its tensors, turns them into device
 pointers, strides and sizes, calls the C entry point on the current HIP
 stream of the tensors' device and raises on a non-OK status.  Outputs and
 workspaces that are not given are allocated.
+
+Autograd records nothing here: the backward pass is called by hand, or from
+the backward of a torch.autograd.Function whose forward calls the forward
+pass.  A call whose history would be lost in silence is refused: gradients
+enabled, and a tensor that requires one among the inputs of the forward pass
+(or among the gradients given to a backward pass, which has none of its own).
+Call it under torch.no_grad() or with detached tensors.
 """
 from __future__ import annotations
 
@@ -133,6 +140,12 @@ def _err(err: Optional[torch.Tensor]) -> Optional[int]:
     return _p(err)
 
 
+def _no_history(fn: str, *tensors: Optional[torch.Tensor]) -> None:
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
+        raise ValueError(f"{fn} records nothing for autograd, but one of its tensors requires a gradient: call it "
+                         "under torch.no_grad() or with detached tensors, and the backward pass by hand")
+
+
 def _check_batch(batch: Batch, dev: torch.device) -> None:
     n = batch.n_seqs
     _on(dev, cu_seqlens=batch.cu_seqlens, page_idx=batch.page_idx, has_init=batch.has_init)
@@ -197,6 +210,7 @@ def gdnt_scan_forward(dims: ScanDims, params: ScanParams, x: torch.Tensor, a: to
     it where it has a ckpt."""
     dev, n, C = x.device, batch.n_rows, dims.channels
     state_out = state_in if state_out is None else state_out
+    _no_history("gdnt_scan_forward", x, a, b, params.a_log, params.dt_bias, state_in.buf, state_out.buf, h)
     if h is None:
         h = torch.empty((n, C), dtype=dims.act_torch, device=dev)
     _on(dev, a=a, b=b, h=h, state_in=state_in.buf, state_out=state_out.buf, a_log=params.a_log,
@@ -231,6 +245,7 @@ def gdnt_scan_backward(dims: ScanDims, params: ScanParams, batch: Batch, state_i
     the final states.  Rows of no sequence and of padding are left as they
     are in every output: give zeroed ones where something reads them."""
     dev, n, C, s = dh.device, batch.n_rows, dims.channels, batch.n_seqs
+    _no_history("gdnt_scan_backward", dh, d_state)
     given = [t is not None for t in (x, a, b)]
     if any(given) and not all(given):
         raise ValueError("x, a and b go together")
@@ -277,6 +292,7 @@ def gdnt_conv_backward(dims: Dims, conv_w: torch.Tensor, x: torch.Tensor, dy: to
     of the rolled windows.  Rows of no sequence and of padding are left as
     they are in dx: give a zeroed one where something reads them."""
     dev, n, C, s, k = x.device, batch.n_rows, dims.c_conv, batch.n_seqs, dims.conv_w - 1
+    _no_history("gdnt_conv_backward", dy, d_window)
     if dy.dtype not in _NAMES:
         raise ValueError(f"dy must be fp32 or bf16, not {dy.dtype}")
     if out is None:
