@@ -33,6 +33,9 @@
  *   multiple of 8 for the backward pass of the recurrence in bf16 (by 1.4), on
  *   four elements and in channels a multiple of 4 for the conv and the
  *   one-launch form (by 1.1 to 1.2).
+ * - GDN_ERR_ARG, also from the queries, where a kernel would need more threads
+ *   than one launch has (2^32): with 128 or fewer channels beyond 2^30 rows, in
+ *   general where blocks of 128 rows by 128 channels (or 256 by 64) number 2^23.
  * - Inputs and outputs of one call must not overlap, but a state pool may be
  *   both state_in and state_out.
  * - workspace: 256-byte aligned device memory of at least the queried size,

@@ -53,10 +53,20 @@ int32_t check_batch(const gdn_batch* b) {
     return GDN_OK;
 }
 
-// Tiles by channel columns: a launch's workgroups.
-int32_t check_size(int64_t n_rows, int64_t C) {
-    if (n_rows < 0 || n_rows > INT32_MAX - 2 * gdnt::kTileRows) return GDN_ERR_ARG;
-    return n_tiles(n_rows) * (padded_channels(C) / gdnt::kTileCols) <= (1 << 28) ? GDN_OK : GDN_ERR_ARG;
+// HIP launches fewer than 2^32 threads in a dimension.
+int32_t check_launch(int64_t groups, int64_t threads) {
+    return groups <= (int64_t)UINT32_MAX / threads ? GDN_OK : GDN_ERR_ARG;
+}
+int32_t check_rows(int64_t n_rows) {
+    return n_rows >= 0 && n_rows <= INT32_MAX - 2 * gdnt::kTileRows ? GDN_OK : GDN_ERR_ARG;
+}
+int32_t check_scan_size(int64_t n_rows, int64_t C) {
+    const int32_t st = check_rows(n_rows);
+    return st != GDN_OK ? st : check_launch(gdnt::scan_groups(n_rows, C), gdnt::kScanThreads);
+}
+int32_t check_conv_size(int64_t n_rows, int64_t C) {
+    const int32_t st = check_rows(n_rows);
+    return st != GDN_OK ? st : check_launch(gdnt::conv_groups(n_rows, C), gdnt::kConvWaves * 64);
 }
 
 int32_t check_pool(const gdnt_scan_dims* d, const gdn_state_pool& s) {
@@ -118,7 +128,7 @@ GDN_EXPORT int32_t gdnt_scan_workspace_bytes(const gdnt_scan_dims* dims, int32_t
     int32_t st;
     if ((st = check_dims(dims)) != GDN_OK) return st;
     if (!out_bytes || n_seqs < 0) return GDN_ERR_ARG;
-    if ((st = check_size(n_rows, dims->channels)) != GDN_OK) return st;
+    if ((st = check_scan_size(n_rows, dims->channels)) != GDN_OK) return st;
     *out_bytes = scan_ws(n_rows, dims->channels).total;
     return GDN_OK;
 }
@@ -126,7 +136,7 @@ GDN_EXPORT int32_t gdnt_scan_workspace_bytes(const gdnt_scan_dims* dims, int32_t
 GDN_EXPORT int32_t gdnt_scan_saved_bytes(const gdnt_scan_dims* dims, int64_t n_rows, size_t* states, size_t* ckpt) {
     int32_t st;
     if ((st = check_dims(dims)) != GDN_OK) return st;
-    if ((st = check_size(n_rows, dims->channels)) != GDN_OK) return st;
+    if ((st = check_scan_size(n_rows, dims->channels)) != GDN_OK) return st;
     if (states) *states = states_bytes(n_rows, dims->channels);
     if (ckpt) *ckpt = (size_t)ckpt_blocks(n_rows, dims->channels) * (GDNT_CKPT_ROWS * GDNT_CKPT_CHANNELS + sizeof(float));
     return GDN_OK;
@@ -138,7 +148,7 @@ GDN_EXPORT int32_t gdnt_conv_workspace_bytes(const gdn_dims* dims, int32_t n_seq
     if ((st = gdn::dims_status(dims)) != GDN_OK) return st;
     if (!out_bytes || n_seqs < 0) return GDN_ERR_ARG;
     const int64_t C = 2 * (int64_t)dims->h_k * dims->d_k + (int64_t)dims->h_v * dims->d_v;
-    if ((st = check_size(n_rows, C)) != GDN_OK) return st;
+    if ((st = check_conv_size(n_rows, C)) != GDN_OK) return st;
     *out_bytes = conv_ws(n_rows, C, gdnt::conv_tiles_up_to(n_rows, C));
     return GDN_OK;
 }
@@ -152,7 +162,7 @@ GDN_EXPORT int32_t gdnt_scan_forward(const gdnt_scan_dims* dims, const gdnt_scan
     if ((st = check_dims(dims)) != GDN_OK) return st;
     if (!params || !params->a_log || !params->dt_bias) return GDN_ERR_ARG;
     if ((st = check_batch(batch)) != GDN_OK) return st;
-    if ((st = check_size(batch->n_rows, dims->channels)) != GDN_OK) return st;
+    if ((st = check_scan_size(batch->n_rows, dims->channels)) != GDN_OK) return st;
     if (ckpt && (!states || !aligned(ckpt, 256))) return GDN_ERR_ARG;
     if (states && !aligned(states, 16)) return GDN_ERR_ARG;
     if (batch->n_seqs == 0) return GDN_OK;
@@ -163,6 +173,7 @@ GDN_EXPORT int32_t gdnt_scan_forward(const gdnt_scan_dims* dims, const gdnt_scan
                               !rows_ok(b, ab_stride, C, dt) || !rows_ok(h, h_stride, C, dt)))
         return GDN_ERR_ARG;
     const bool rows = batch->max_seqlen > 0 && batch->max_seqlen <= kRowsMax && batch->n_seqs <= kRowsSeqs && !states;
+    if (rows && (st = check_launch(gdnt::scan_rows_groups(batch->n_seqs, C), gdnt::kRowsThreads)) != GDN_OK) return st;
     if (!rows && (ws_bytes < scan_ws(batch->n_rows, C).total || !workspace || !aligned(workspace, 256)))
         return GDN_ERR_ARG;
     gdnt::ScanArgs A = scan_args(dims, params, batch, state_in, workspace, err);
@@ -189,7 +200,7 @@ GDN_EXPORT int32_t gdnt_scan_backward(const gdnt_scan_dims* dims, const gdnt_sca
     if ((st = check_dims(dims)) != GDN_OK) return st;
     if (!params || !params->a_log || !params->dt_bias || !d_a_log || !d_dt_bias) return GDN_ERR_ARG;
     if ((st = check_batch(batch)) != GDN_OK) return st;
-    if ((st = check_size(batch->n_rows, dims->channels)) != GDN_OK) return st;
+    if ((st = check_scan_size(batch->n_rows, dims->channels)) != GDN_OK) return st;
     gdn_batch bt = *batch;
     if (bt.n_seqs == 0) bt.n_rows = 0;  // no row belongs to a sequence
     const int64_t C = dims->channels;
@@ -229,7 +240,7 @@ GDN_EXPORT int32_t gdnt_conv_backward(const gdn_dims* dims, const void* conv_w, 
     if (!conv_w || !d_conv_w || !dtype_ok(dy_dtype) || (activation != 0 && activation != 1)) return GDN_ERR_ARG;
     const int64_t C = 2 * (int64_t)dims->h_k * dims->d_k + (int64_t)dims->h_v * dims->d_v;
     const int32_t dt = dims->act_dtype;
-    if ((st = check_size(batch->n_rows, C)) != GDN_OK) return st;
+    if ((st = check_conv_size(batch->n_rows, C)) != GDN_OK) return st;
     gdn_batch bt = *batch;
     if (bt.n_seqs == 0) bt.n_rows = 0;
     if (conv.base && bt.n_seqs > 0 &&

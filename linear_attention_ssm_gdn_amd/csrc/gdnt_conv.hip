@@ -260,9 +260,11 @@ template <typename T, typename YT, bool VEC> static hipError_t conv_t(const Conv
     const int nc = (int)((a.C + kConvCols - 1) / kConvCols);
     const int own = conv_rows(a.n_rows, a.C);
     const int64_t nt = conv_tiles(a.n_rows, a.C), grid = nt * nc;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    if (grid > 0)
+    if (grid > 0) {
         hipLaunchKernelGGL((k_conv_backward<T, YT, VEC>), dim3((unsigned)grid), dim3(kConvThreads), 0, s, a, nc, own);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
     return launch_sum_tiles(a.part, nt, a.C, 4, a.d_conv_w, nullptr, s);
 }
 

@@ -69,6 +69,18 @@ struct ConvBwdArgs {
 inline int64_t n_tiles(int64_t n_rows) { return (n_rows + kTileRows - 1) / kTileRows; }
 __host__ __device__ inline int64_t padded_channels(int64_t C) { return (C + kTileCols - 1) / kTileCols * kTileCols; }
 
+// Workgroups of the scan kernels, eight waves each; those of the forward pass
+// (128 rows by 128 channels) and of the backward pass (256 by 64), the more of them.
+constexpr int kScanThreads = 512;
+inline int64_t scan_groups(int64_t n_rows, int64_t C) {
+    const int64_t fwd = ((n_rows + 127) / 128) * ((C + 127) / 128);
+    const int64_t bwd = n_tiles(n_rows) * (padded_channels(C) / kTileCols);
+    return fwd > bwd ? fwd : bwd;
+}
+// Of the one-launch form: 256 threads, four channels each, to a sequence.
+constexpr int kRowsThreads = 256;
+inline int64_t scan_rows_groups(int64_t n_seqs, int64_t C) { return n_seqs * ((C + 4 * kRowsThreads - 1) / (4 * kRowsThreads)); }
+
 // k_conv_backward: four strips to a workgroup, 256 channels wide.
 constexpr int kConvWaves = 4;
 constexpr int kConvCols = 256;
@@ -89,6 +101,9 @@ inline int conv_rows(int64_t n_rows, int64_t C) {
 inline int64_t conv_tiles(int64_t n_rows, int64_t C) {
     const int64_t rows = kConvWaves * conv_rows(n_rows, C);
     return (n_rows + rows - 1) / rows;
+}
+inline int64_t conv_groups(int64_t n_rows, int64_t C) {
+    return conv_tiles(n_rows, C) * ((C + kConvCols - 1) / kConvCols);
 }
 // The most tiles that a batch of up to n_rows rows has: a batch just too small
 // for longer strips has more of them than one just large enough.

@@ -26,6 +26,7 @@ namespace gdnt {
 
 constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * 64;
+static_assert(kThreads == kScanThreads, "launch size");
 constexpr int kFwdRows = FR * kWaves;        // 128
 constexpr int kFwdCols = 128;
 static_assert(kTileRows % kFwdRows == 0, "tile shape");
@@ -212,14 +213,14 @@ __global__ __launch_bounds__(kThreads, 4) void k_scan_forward(const ScanArgs A, 
 // of one row by 4096 channels take 4.2 us, a launch's own time: 4 MB are 0.8
 // us of memory.
 template <typename T, bool VEC>
-__global__ __launch_bounds__(256) void k_scan_rows(const ScanArgs A, int n_x) {
+__global__ __launch_bounds__(kRowsThreads) void k_scan_rows(const ScanArgs A, int n_x) {
     const int seq = (int)(blockIdx.x / n_x);
-    const int64_t c0 = ((int64_t)(blockIdx.x % n_x) * 256 + threadIdx.x) * 4;
+    const int64_t c0 = ((int64_t)(blockIdx.x % n_x) * kRowsThreads + threadIdx.x) * 4;
     const bool tell = blockIdx.x % n_x == 0 && threadIdx.x == 0;
     const int page = A.page_idx[seq], r0 = A.cu[seq], r1 = A.cu[seq + 1];
     // all bounds up to this sequence's, as the row map does
     bool bad = false;
-    for (int s = threadIdx.x; s <= seq; s += 256) bad |= !bounds_ok(A.n_rows, A.cu[s], A.cu[s + 1]);
+    for (int s = threadIdx.x; s <= seq; s += kRowsThreads) bad |= !bounds_ok(A.n_rows, A.cu[s], A.cu[s + 1]);
     bad = __syncthreads_or(bad) != 0;
     if (page < 0) return;
     if (page >= A.page_limit) {
@@ -283,10 +284,9 @@ MapArgs scan_map_args(const ScanArgs& a) {
 }
 
 template <typename T, bool VEC> static hipError_t rows_t(const ScanArgs& a, hipStream_t s) {
-    const int64_t n_x = (a.C + 1023) / 1024, grid = n_x * a.n_seqs;
+    const int64_t n_x = scan_rows_groups(1, a.C), grid = scan_rows_groups(a.n_seqs, a.C);
     if (grid == 0) return hipSuccess;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((k_scan_rows<T, VEC>), dim3((unsigned)grid), dim3(256), 0, s, a, (int)n_x);
+    hipLaunchKernelGGL((k_scan_rows<T, VEC>), dim3((unsigned)grid), dim3(kRowsThreads), 0, s, a, (int)n_x);
     return hipGetLastError();
 }
 
@@ -299,7 +299,6 @@ template <typename T, bool PAIR> static hipError_t forward_t(const ScanArgs& a, 
     const int nc = (int)((a.C + kFwdCols - 1) / kFwdCols);
     const int64_t nt = (a.n_rows + kFwdRows - 1) / kFwdRows, grid = nt * nc;
     if (grid == 0) return hipSuccess;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
     if (a.q)
         hipLaunchKernelGGL((k_scan_forward<T, PAIR, true>), dim3((unsigned)grid), dim3(kThreads), 0, s, a, nc, nt);
     else

@@ -30,6 +30,7 @@ namespace gdnt {
 constexpr int kWaves = 8;
 constexpr int kThreads = kWaves * 64;
 static_assert(kWaves * 2 * FR == kTileRows && 32 * 2 == kTileCols, "tile shape");
+static_assert(kThreads == kScanThreads, "launch size");
 
 // The largest scale whose 127-fold is finite: that of a block around the
 // largest fp32 number is one step above it.
@@ -569,7 +570,6 @@ constexpr int64_t kGroups = 256;
 template <typename T, bool PAIR, bool CKPT> static hipError_t backward_t(const ScanArgs& a, hipStream_t s) {
     const int nc = (int)(padded_channels(a.C) / kTileCols);
     const int64_t nt = n_tiles(a.n_rows), grid = nt * nc;
-    if (grid > 0x7fffffff) return hipErrorInvalidValue;
     if (grid > 0) {
         if (sizeof(T) == 2 && PAIR && a.vec8)
             hipLaunchKernelGGL((k_scan_backward<T, PAIR, CKPT, sizeof(T) == 2 && PAIR>),
@@ -577,6 +577,8 @@ template <typename T, bool PAIR, bool CKPT> static hipError_t backward_t(const S
         else
             hipLaunchKernelGGL((k_scan_backward<T, PAIR, CKPT, false>), dim3((unsigned)grid), dim3(kThreads), 0, s, a,
                                nc, nt);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
     }
     return launch_sum_tiles(a.part, nt, a.C, 2, a.d_a_log, a.d_dt_bias, s);
 }

@@ -33,7 +33,7 @@ HEADS = [(1, 1, 32, 32), (1, 1, 32, 608), (16, 32, 128, 128), (2048, 4096, 128, 
 def test_the_conv_workspace_never_shrinks_with_rows(L, heads):
     C = 2 * heads[0] * heads[2] + heads[1] * heads[3]
     strips = -(-2048 // -(-C // 256))  # of a column, for 2048 in all
-    rows = {0, 1, 2, 255, 256, 257, 70000, 1 << 20}
+    rows = {0, 1, 2, 255, 256, 257, 70000, 1 << 18}
     for own in (13, 25, 57):  # where the strips' length may change
         rows |= {max(0, (strips + k) * own + j) for k in (-2, -1, 0, 1) for j in range(-2, 3)}
     sizes = [conv_bytes(L, heads, r) for r in sorted(rows)]
@@ -48,6 +48,29 @@ def test_the_scan_workspace_never_shrinks_with_rows(L):
             assert L.load().gdnt_scan_workspace_bytes(ctypes.byref(d), 3, rows, ctypes.byref(ws)) == 0
             assert ws.value >= last
             last = ws.value
+
+
+def test_batches_beyond_one_launch_are_refused(L):
+    """HIP launches fewer than 2^32 threads: 2^23 workgroups of 512 are too many.  Refused on the host, by the queries
+    and the call, before anything is launched."""
+    ws = ctypes.c_size_t()
+    ask = lambda C, rows: L.load().gdnt_scan_workspace_bytes(ctypes.byref(L.GdntScanDims(C, BF16, F32)), 1, rows,
+                                                             ctypes.byref(ws))
+    for C, per_row in ((1, 1), (128, 1), (129, 2), (4096, 32)):
+        rows = (1 << 23) // per_row * 128  # 2^23 blocks of 128 rows by 128 channels
+        assert ask(C, rows - 256) == 0, C
+        assert ask(C, rows) == 1, C
+        d = L.GdntScanDims(C, BF16, F32)
+        assert L.load().gdnt_scan_saved_bytes(ctypes.byref(d), rows, ctypes.byref(ws), None) == 1
+    d, p = L.GdntScanDims(64, BF16, F32), L.GdntScanParams(FAKE, FAKE)
+    b, s = L.GdnBatch(FAKE, FAKE, None, 2, 0, (1 << 30) + 1), L.GdnStatePool(FAKE, 64, 4)
+    assert L.load().gdnt_scan_forward(ctypes.byref(d), ctypes.byref(p), FAKE, 64, FAKE, FAKE, 64, ctypes.byref(b), s, s,
+                                      FAKE, 64, None, None, FAKE, 1 << 62, None, None) == 1
+    # the one-launch form: 2^24 workgroups of 256
+    C = 1 << 24
+    d, b, s = L.GdntScanDims(C, BF16, F32), L.GdnBatch(FAKE, FAKE, None, 1024, 1, 1024), L.GdnStatePool(FAKE, C, 1024)
+    assert L.load().gdnt_scan_forward(ctypes.byref(d), ctypes.byref(p), FAKE, C, FAKE, FAKE, C, ctypes.byref(b), s, s,
+                                      FAKE, C, None, None, None, 0, None, None) == 1
 
 
 @pytest.mark.gpu
