@@ -49,15 +49,17 @@ template <typename T> __device__ __forceinline__ Raw2<T> zero2() {
 // channel it was 1146).  Else there is only one channel.  The lane with an odd
 // count's last channel loads a pair all the same, with what is behind it (the
 // descriptor's end, or what fills the row); last_alone then loads that channel
-// alone, in the one column that has it.
-template <typename T, bool PAIR> struct WaveRows {
+// alone, in the one column that has it.  ODD false: the count is even, no lane
+// has one channel alone.
+template <typename T, bool PAIR, bool ODD = true> struct WaveRows {
+    static_assert(PAIR || ODD, "one channel is an odd count");
     __amdgpu_buffer_rsrc_t rs;
     uint32_t row, at;  // bytes
     bool odd;          // uniform: a lane here has one channel
     __device__ __forceinline__ WaveRows(const void* base, int64_t stride, int64_t n_rows, int64_t first, int32_t C,
                                         int64_t col, int64_t lane_at)
         : row((uint32_t)stride * (uint32_t)sizeof(T)), at((uint32_t)lane_at * (uint32_t)sizeof(T)),
-          odd((C & 1) && C - col < 128) {
+          odd(ODD && (C & 1) && C - col < 128) {
         // where rows are walked tile after tile, keeps the rows' offsets from being held in registers
         asm volatile("" : "+s"(row));
         int64_t bytes = ((n_rows - 1 - first) * stride + C - col) * (int64_t)sizeof(T);
@@ -80,7 +82,7 @@ template <typename T, bool PAIR> struct WaveRows {
     }
     // rows: those of the lane that belong to a sequence, as bits
     __device__ __forceinline__ void last_alone(Raw2<T> (&v)[FR], uint32_t rows, int nc) const {
-        if (!PAIR || !odd || nc != 1) return;
+        if (!PAIR || !ODD || !odd || nc != 1) return;
 #pragma unroll
         for (int r = 0; r < FR; ++r)
             if (rows >> r & 1u) v[r] = load_one(r);
@@ -91,12 +93,12 @@ template <typename T, bool PAIR> struct WaveRows {
         if constexpr (sizeof(T) == 2) {
             const uint32_t v = gdn::f32x2_to_bf16x2(a, b);
             if (PAIR && nc == 2) __builtin_amdgcn_raw_buffer_store_b32(v, rs, at, r * row, 0);
-            if (odd && nc == 1) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)v, rs, at, r * row, 0);
+            if (ODD && odd && nc == 1) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)v, rs, at, r * row, 0);
         } else {
             const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
             typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
             if (PAIR && nc == 2) __builtin_amdgcn_raw_buffer_store_b64((u32x2){x, y}, rs, at, r * row, 0);
-            if (odd && nc == 1) __builtin_amdgcn_raw_buffer_store_b32(x, rs, at, r * row, 0);
+            if (ODD && odd && nc == 1) __builtin_amdgcn_raw_buffer_store_b32(x, rs, at, r * row, 0);
         }
     }
 };

@@ -119,6 +119,7 @@ __device__ __forceinline__ const __attribute__((address_space(4))) ScanArgs* rar
 // channels, 577 with 4094, which go without (fp32 rows would not fit in LDS).
 template <typename T, bool PAIR, bool CKPT, bool PIPE>
 __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A, int n_cols, int64_t n_tiles) {
+    using Rows = WaveRows<T, PAIR, !PIPE>;
     __shared__ float2 s_a[kWaves][32], s_u[kWaves][32], s_ra[kWaves][32], s_ru[kWaves][32], s_h[32];
     __shared__ float2 s_s1[kWaves][32], s_s2[kWaves][32];
     __shared__ uint32_t s_ticket;
@@ -234,10 +235,10 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
         auto seq_of = [&](int r) { return __shfl(m32, half * FR + r) >> 2; };  // all lanes together
 
         auto rows = [&](const void* base, int64_t stride) {
-            return WaveRows<T, PAIR>(base, stride, A.n_rows, r0, A.C, cb, half * FR * stride + hl * 2);
+            return Rows(base, stride, A.n_rows, r0, A.C, cb, half * FR * stride + hl * 2);
         };
         const bool whole = in == 0xffffffffu;
-        const WaveRows<T, PAIR> D = rows(A.dh, A.dh_stride);
+        const Rows D = rows(A.dh, A.dh_stride);
         Raw2<T> rd[FR], rx[FR], ra[FR], rb[FR];
         Ckpt2 qx, qa, qb;
         if (PIPE && whole) {
@@ -283,7 +284,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
                 getq(2, qb);
                 getq(0, qx);
             }
-            const WaveRows<T, PAIR> X = rows(A.x, A.x_stride), Ag = rows(A.a, A.ab_stride), Bg = rows(A.b, A.ab_stride);
+            const Rows X = rows(A.x, A.x_stride), Ag = rows(A.a, A.ab_stride), Bg = rows(A.b, A.ab_stride);
             auto row = [&](int r) {
                 if constexpr (!CKPT) {
                     ra[r] = Ag.load(r);
@@ -488,7 +489,7 @@ __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A,
             else again(qx.w[r & 7]);
         }
         // third walk: the gradients, from the last row to the first
-        const WaveRows<T, PAIR> DX = rows(A.dx, A.dx_stride), DA = rows(A.da, A.dab_stride), DB = rows(A.db, A.dab_stride);
+        const Rows DX = rows(A.dx, A.dx_stride), DA = rows(A.da, A.dab_stride), DB = rows(A.db, A.dab_stride);
         const float kg[2] = {kk[0] / kLog2e, kk[1] / kLog2e};
         float s1[2] = {}, s2[2] = {};  // sums of dg y and of dg sigmoid(z)
 #pragma unroll
