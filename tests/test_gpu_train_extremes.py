@@ -8,6 +8,7 @@ import torch
 
 import oracle.train as ora
 from gpu_util import DEV, gdn, host
+from test_gpu_conv_backward import Conv
 from test_gpu_scan import decode
 from train_util import DT, Case, check_forward, check_grads
 
@@ -143,3 +144,126 @@ def test_infinite_gates_are_their_limits(act):
         inf.t[name][r, ch] = float("inf") * sign
     for p, q in zip(results(far, False), results(inf, False)):
         assert same(p, q)
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ["x", "a", "b", "dh"])
+def test_a_nan_in_8_bits_stays_in_its_blocks(name, act):
+    """16 rows by 4 channels of NaNs (dh is not stored: itself alone); all other channels keep their bits, and in these
+    NaNs stand where the formulas at the stored values have them."""
+    C = 72
+    c, clean = (Case(NAN_LENS, C, act, "f32", seed=66) for _ in range(2))
+    put(c, name, NAN_ROWS, (6, 33), nan_of(DT[act], 1))
+    touched = [6, 33] if name == "dh" else [4, 5, 6, 7, 32, 33, 34, 35]
+    rest = [k for k in range(C) if k not in touched]
+    for got, want in zip(results(c, True), results(clean, True)):
+        assert same(got[..., rest], want[..., rest])
+    saved = c.saved(ckpt=True)
+    c.forward(saved)
+    v, _, _ = decode(c, saved)
+    out = c.backward(saved, from_ckpt=True)
+    with np.errstate(invalid="ignore"):
+        before = ora.scan(c.f64("x"), c.f64("a"), c.f64("b"), c.a_log, c.dt_bias, c.spans, c.seq_h0())[2]
+        rb = ora.rebuilt(v[0], v[1], v[2], c.a_log, c.dt_bias, c.spans, before)
+        ref = ora.scan_backward(v[0], v[1], v[2], c.a_log, c.dt_bias, c.spans, rb, c.f64("dh"), c.d_state, c.init)
+    for k, r in ref.items():
+        assert np.array_equal(np.isnan(host(getattr(out, k))), np.isnan(r)), k
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ["x", "a", "b", "a_log", "dt_bias", "state", "dh", "d_state"])
+def test_an_infinity_stays_in_its_sequence_and_channel(name, act):
+    """Every other channel, and every other sequence of the channel, keeps its bits, forward and backward."""
+    C, channels = 72, (6, 33, 70)
+    for value in (float("inf"), float("-inf")):
+        c, clean = (Case(NAN_LENS, C, act, "f32", seed=67) for _ in range(2))
+        put(c, name, NAN_ROWS, channels, value)
+        rest = [k for k in range(C) if k not in channels]
+        got, want = results(c, False), results(clean, False)
+        for p, q in zip(got, want):
+            assert same(p[..., rest], q[..., rest])
+        if name in ("a_log", "dt_bias"):
+            continue
+        other = [r for r in range(c.rows) if not 200 <= r < 600]
+        for k in (0, 3, 4, 5):  # h, dx, da, db
+            assert same(got[k][other], want[k][other])
+        page = int(c.pages[0]), int(c.pages[2])
+        assert same(got[1][list(page)], want[1][list(page)]) and same(got[-1][[0, 2]], want[-1][[0, 2]])
+
+
+def test_an_infinite_gradient_is_the_formulas():
+    """dh infinite at one row: what it reaches is infinite with the formulas' signs, or NaN where they have Inf - Inf
+    and 0 Inf."""
+    c = Case([300, 20], 64, "f32", "f32", seed=68)
+    c.t["dh"][150, 7], c.t["dh"][310, 8] = float("inf"), float("-inf")
+    saved = c.saved()
+    c.forward(saved)
+    out = c.backward(saved)
+    with np.errstate(invalid="ignore", over="ignore"):
+        args = (c.f64("x"), c.f64("a"), c.f64("b"), c.a_log, c.dt_bias, c.spans)
+        ref = ora.scan_backward(*args, ora.scan(*args, c.seq_h0())[2], c.f64("dh"), c.d_state, c.init)
+    for k, r in ref.items():
+        got = host(getattr(out, k))
+        assert np.array_equal(np.isnan(got), np.isnan(r)) and np.array_equal(got[np.isinf(r)], r[np.isinf(r)]), k
+        assert np.isfinite(got[np.isfinite(r)]).all(), k
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ["x", "a", "b", "a_log", "dt_bias", "state"])
+def test_a_nan_in_the_one_launch_form(name, act):
+    """At most 8 rows a sequence, one launch: rows, sequences and channels as above."""
+    g = gdn()
+    c, clean = (Case([1, 8, 0, 3, 7], 72, act, "f32", seed=69) for _ in range(2))
+    put(c, name, (4,), (6, 33, 71), nan_of(DT[act] if name in ("x", "a", "b") else torch.float32, -1))
+    rest = [k for k in range(72) if k not in (6, 33, 71)]
+    few = lambda c: c.forward(batch=g.Batch(c.batch.cu_seqlens, c.batch.page_idx, None, 8, c.rows))
+    (h, _, so), (h2, _, so2) = few(c), few(clean)
+    assert same(h[:, rest], h2[:, rest]) and same(so.buf[:, rest], so2.buf[:, rest])
+    check_forward(c, h, so, ora)
+
+
+# ------------------------------------------------------------------------ conv
+
+
+CONV_LENS = [70, 1, 200, 2, 60]  # the third from row 71 to 270
+
+
+@pytest.mark.parametrize("act,ydt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
+@pytest.mark.parametrize("name", ["x", "dy", "w", "window", "d_window"])
+def test_conv_nan_stays_in_its_sequence_and_channel(name, act, ydt):
+    """NaN at a sequence's first, middle and last rows: NaNs where the formulas have them, all else in its bounds, the
+    other channels bit for bit; infinities change no other channel and no other sequence."""
+    C = 96
+    for value in (float("nan"), float("inf"), float("-inf")):
+        c, clean = (Conv(CONV_LENS, act=act, ydt=ydt, seed=70) for _ in range(2))
+        channels = (6, 33, 95)
+        for ch, row in zip(channels, (71, 130, 270)):
+            if name == "w":
+                c.w[ch, 1] = value
+            elif name == "window":
+                c.win[int(c.pages[2]), 1, ch] = value
+            elif name == "d_window":
+                c.d_window[2, 1, ch] = value
+            else:
+                getattr(c, name)[row, ch] = value
+        out, ref = c.run(), clean.run()
+        rest = [k for k in range(C) if k not in channels]
+        assert same(out.dx[:, rest], ref.dx[:, rest]) and same(out.d_conv_w[rest], ref.d_conv_w[rest])
+        assert same(out.d_window0[..., rest], ref.d_window0[..., rest])
+        if name != "w":
+            other = [r for r in range(c.rows) if not 71 <= r <= 270]
+            assert same(out.dx[other], ref.dx[other])
+            assert same(out.d_window0[[0, 1, 3, 4]], ref.d_window0[[0, 1, 3, 4]])
+        if value != value:
+            c.check(out)
+
+
+def test_conv_backward_far_out():
+    """z at the ends of the range: silu' is 0 or 1 there, and nothing becomes NaN."""
+    c = Conv([40, 300], act="f32", ydt="f32", seed=72)
+    c.x[10:14, :8] = 1e30
+    c.x[60:64, 8:16] = -1e30
+    c.x[200, 16:24] = 90.0
+    c.x[210, 24:32] = -90.0
+    out = c.run()
+    assert all(bool(torch.isfinite(t).all()) for t in out)
