@@ -110,9 +110,9 @@ def gdnt_conv_workspace_bytes(dims: Dims, n_seqs: int, n_rows: int) -> int:
 
 
 def _on(dev: torch.device, **tensors) -> None:
-    where = dev.index
+    where = -1 if dev.index is None else dev.index  # the host's tensors give -1
     for name, t in tensors.items():
-        if t is not None and (t.get_device() != where if where is not None else t.device != dev):
+        if t is not None and t.get_device() != where:
             raise ValueError(f"{name} is on {t.device}, not on {dev}")
 
 
@@ -140,10 +140,9 @@ def _err(err: Optional[torch.Tensor]) -> Optional[int]:
     return _p(err)
 
 
-def _no_history(fn: str, *tensors: Optional[torch.Tensor]) -> None:
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors):
-        raise ValueError(f"{fn} records nothing for autograd, but one of its tensors requires a gradient: call it "
-                         "under torch.no_grad() or with detached tensors, and the backward pass by hand")
+def _no_history(fn: str) -> None:
+    raise ValueError(f"{fn} records nothing for autograd, but one of its tensors requires a gradient: call it "
+                     "under torch.no_grad() or with detached tensors, and the backward pass by hand")
 
 
 def _check_batch(batch: Batch, dev: torch.device) -> None:
@@ -208,19 +207,22 @@ def gdnt_scan_forward(dims: ScanDims, params: ScanParams, x: torch.Tensor, a: to
     are); the final states go to state_out (default: state_in, in place).
     `saved` receives what gdnt_scan_backward needs, x, a and b in 8 bits among
     it where it has a ckpt."""
-    dev, n, C = x.device, batch.n_rows, dims.channels
+    dev, n, C, dt = x.device, batch.n_rows, dims.channels, dims.act_torch
     state_out = state_in if state_out is None else state_out
-    _no_history("gdnt_scan_forward", x, a, b, params.a_log, params.dt_bias, state_in.buf, state_out.buf, h)
+    if torch.is_grad_enabled() and (x.requires_grad or a.requires_grad or b.requires_grad or
+                                    params.a_log.requires_grad or params.dt_bias.requires_grad or
+                                    state_in.buf.requires_grad):
+        _no_history("gdnt_scan_forward")
     if h is None:
-        h = torch.empty((n, C), dtype=dims.act_torch, device=dev)
+        h = torch.empty((n, C), dtype=dt, device=dev)
     _on(dev, a=a, b=b, h=h, state_in=state_in.buf, state_out=state_out.buf, a_log=params.a_log,
         dt_bias=params.dt_bias, err=err)
     _check_params(params, dims)
     _check_batch(batch, dev)
     _check_state_pool("state_in", state_in, dims)
     _check_state_pool("state_out", state_out, dims)
-    xs, hs = (_rows2(k, t, n, C, dims.act_torch) for k, t in (("x", x), ("h", h)))
-    as_, bs = (_rows2(k, t, n, C, dims.act_torch) for k, t in (("a", a), ("b", b)))
+    xs, hs = _rows2("x", x, n, C, dt), _rows2("h", h, n, C, dt)
+    as_, bs = _rows2("a", a, n, C, dt), _rows2("b", b, n, C, dt)
     if as_ != bs:
         raise ValueError("a and b must share their row stride")
     if saved is not None:
@@ -244,15 +246,16 @@ def gdnt_scan_backward(dims: ScanDims, params: ScanParams, batch: Batch, state_i
     before the forward call; d_state [n_seqs][channels] fp32: the gradient of
     the final states.  Rows of no sequence and of padding are left as they
     are in every output: give zeroed ones where something reads them."""
-    dev, n, C, s = dh.device, batch.n_rows, dims.channels, batch.n_seqs
-    _no_history("gdnt_scan_backward", dh, d_state)
+    dev, n, C, s, dt = dh.device, batch.n_rows, dims.channels, batch.n_seqs, dims.act_torch
+    if torch.is_grad_enabled() and (dh.requires_grad or (d_state is not None and d_state.requires_grad)):
+        _no_history("gdnt_scan_backward")
     given = [t is not None for t in (x, a, b)]
     if any(given) and not all(given):
         raise ValueError("x, a and b go together")
     if not any(given) and saved.ckpt is None:
         raise ValueError("a backward pass needs x, a and b, or a checkpoint")
     if out is None:
-        out = ScanGrads(*(torch.empty((n, C), dtype=dims.act_torch, device=dev) for _ in range(3)),
+        out = ScanGrads(*(torch.empty((n, C), dtype=dt, device=dev) for _ in range(3)),
                         *(torch.empty(C, dtype=torch.float32, device=dev) for _ in range(2)),
                         torch.empty((s, C), dtype=torch.float32, device=dev))
     _on(dev, x=x, a=a, b=b, d_state=d_state, state_in=state_in.buf, a_log=params.a_log, dt_bias=params.dt_bias,
@@ -263,9 +266,9 @@ def gdnt_scan_backward(dims: ScanDims, params: ScanParams, batch: Batch, state_i
     _check_saved(saved, dims, n, dev)
     xs = as_ = bs = 0
     if all(given):
-        xs, as_, bs = (_rows2(k, t, n, C, dims.act_torch) for k, t in (("x", x), ("a", a), ("b", b)))
-    hs, dxs, das, dbs = (_rows2(k, t, n, C, dims.act_torch)
-                         for k, t in (("dh", dh), ("dx", out.dx), ("da", out.da), ("db", out.db)))
+        xs, as_, bs = _rows2("x", x, n, C, dt), _rows2("a", a, n, C, dt), _rows2("b", b, n, C, dt)
+    hs, dxs = _rows2("dh", dh, n, C, dt), _rows2("dx", out.dx, n, C, dt)
+    das, dbs = _rows2("da", out.da, n, C, dt), _rows2("db", out.db, n, C, dt)
     if as_ != bs or das != dbs:
         raise ValueError("a and b, and da and db, must share their row stride")
     _flat("d_state", d_state, (s, C), torch.float32)
@@ -292,7 +295,8 @@ def gdnt_conv_backward(dims: Dims, conv_w: torch.Tensor, x: torch.Tensor, dy: to
     of the rolled windows.  Rows of no sequence and of padding are left as
     they are in dx: give a zeroed one where something reads them."""
     dev, n, C, s, k = x.device, batch.n_rows, dims.c_conv, batch.n_seqs, dims.conv_w - 1
-    _no_history("gdnt_conv_backward", dy, d_window)
+    if torch.is_grad_enabled() and (dy.requires_grad or (d_window is not None and d_window.requires_grad)):
+        _no_history("gdnt_conv_backward")
     if dy.dtype not in _NAMES:
         raise ValueError(f"dy must be fp32 or bf16, not {dy.dtype}")
     if out is None:
