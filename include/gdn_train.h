@@ -21,10 +21,11 @@
  *   sequence (before the first, behind the last) and rows of padding
  *   sequences (page_idx < 0) are neither read nor written.
  * - A sequence is skipped, as a padding one is, and a bit is set, when its
- *   page index is beyond a pool it uses (GDN_DEVERR_PAGE), when its bounds
- *   are negative, decreasing, beyond n_rows or before the end of an earlier
- *   valid sequence, or when it is longer than a max_seqlen > 0
- *   (GDN_DEVERR_BATCH).
+ *   page index is beyond a pool it uses (GDN_DEVERR_PAGE; a backward call knows
+ *   state_in alone, so where state_out has fewer pages give it that number in
+ *   state_in.n_pages), when its bounds are negative, decreasing, beyond n_rows
+ *   or before the end of an earlier valid sequence, or when it is longer than a
+ *   max_seqlen > 0 (GDN_DEVERR_BATCH).
  * - Sequences of length 0 are no-ops, whose page stays as it is; a backward
  *   pass hands the gradient of their final state or window through to the
  *   initial one, whatever has_init says.
@@ -40,9 +41,9 @@
  *   both state_in and state_out.
  * - workspace: 256-byte aligned device memory of at least the queried size,
  *   ignored on entry, scratch on return.  The size queried for a number of
- *   rows serves every call with the same dims and no more rows.  Calls that share one workspace
- *   must be ordered (same stream, or events); graphs captured over one
- *   workspace likewise.
+ *   rows serves every call with the same dims and no more rows.  Calls that
+ *   share one workspace must be ordered (same stream, or events); graphs
+ *   captured over one workspace likewise.
  * - An infinite a or b stands for its limit (e^g and beta are 0 or 1, with no
  *   gradient through them).
  * - All arithmetic is fp32 (sums over rows of a parameter's gradient: fp32
@@ -130,7 +131,9 @@ int32_t gdnt_scan_forward(const gdnt_scan_dims* dims, const gdnt_scan_params* pa
  * the gradient of h, d_state [n_seqs][channels] fp32 (or NULL: zero) that of
  * the final states before their rounding.  With lambda_t = dh_t +
  * e^{g_{t+1}} lambda_{t+1} (+ d_state at the last row):
- *   dx_t = beta_t lambda_t,  db_t = lambda_t x_t beta_t (1 - beta_t),
+ *   dx_t = beta_t lambda_t,  db_t = lambda_t x_t beta_t (1 - beta_t)
+ *   (1 - beta_t from beta_t in fp32: within 2^-23 of 1, so that db of a b far
+ *   above 0 is small without being exact to its own digits),
  *   dg_t = lambda_t e^{g_t} h_{t-1},  da_t = -exp(A_log) dg_t sigmoid(z_t),
  *   d_dt_bias = sum_t da_t,  d_a_log = sum_t dg_t g_t,
  *   d_state0 = e^{g_1} lambda_1,

@@ -1,4 +1,6 @@
-// gdnt_chain.hpp -- how a state travels from tile to tile inside one launch.
+// gdnt_chain.hpp -- how a state travels from tile to tile inside one launch:
+// the published single-pass scan with decoupled look-back (Merrill and Garland,
+// 2016), for runs h -> a h + u.
 //
 // Tiles are handed out by a ticket in the order of the recurrence, so a tile
 // only ever waits for tiles that already run: every wait ends.  A tile first

@@ -45,7 +45,7 @@ template <typename T> __device__ __forceinline__ Raw2<T> zero2() {
 // (32 bits: row strides end at 2^24 elements); it ends with the tensor.
 // PAIR: a lane's two channels move together, wherever the row starts, for bf16
 // at odd offsets as dwords across dword boundaries (forward and backward over
-// 16692 rows take 590 us with 4095 bf16 channels, 576 with 4094; channel by
+// 16692 rows take 596 us with 4095 bf16 channels, 571 with 4094; channel by
 // channel it was 1146).  Else there is only one channel.  The lane with an odd
 // count's last channel loads a pair all the same, with what is behind it (the
 // descriptor's end, or what fills the row); last_alone then loads that channel

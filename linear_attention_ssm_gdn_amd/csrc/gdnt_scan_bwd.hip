@@ -17,11 +17,13 @@
 // stays there, draws tile after tile, and loads the next tile's rows into LDS
 // (128 KB in bf16) while it computes.
 //
-// 32768 x 4096 in bf16 takes 491 us for 1.88 GB (3.8 TB/s, 75% of a large
-// copy's rate) at 73 vector instructions an element (56% of the issue slots);
-// from the checkpoint 502 us for 1.50 GB.  What is left is neither: a
-// tile's eight waves meet three times, and wait for mu from the tile behind
-// (10 to 20 of some 50 thousand cycles).
+// 32768 x 4096 in bf16 takes 460 us for 1.88 GB (4.1 TB/s, 81% of a large
+// copy's rate) at 72 vector instructions an element (58% of the issue slots);
+// from the checkpoint 470 us for 1.50 GB, 82 instructions (64%).  What is left
+// is neither: a tile's eight waves meet three times, and wait for mu from the
+// tile behind (10 to 20 of some 50 thousand cycles).  fp32 rows take all 256
+// registers and nine more, which are spilled (40 bytes a lane); 13212 x 2050
+// take 228 us.
 #include "gdnt_chain.hpp"
 #include "gdnt_rows.hpp"
 
@@ -115,8 +117,8 @@ __device__ __forceinline__ const __attribute__((address_space(4))) ScanArgs* rar
 
 // PIPE: x, a, b (or the checkpoint) and dh of the next tile load into LDS
 // while this one is computed.  For bf16 rows on 16 bytes and channels a
-// multiple of 8: forward and backward over 16692 rows take 414 us with 4096
-// channels, 577 with 4094, which go without (fp32 rows would not fit in LDS).
+// multiple of 8: forward and backward over 16692 rows take 401 us with 4096
+// channels, 571 with 4094, which go without (fp32 rows would not fit in LDS).
 template <typename T, bool PAIR, bool CKPT, bool PIPE>
 __global__ __launch_bounds__(kThreads, 2) void k_scan_backward(const ScanArgs A, int n_cols, int64_t n_tiles) {
     using Rows = WaveRows<T, PAIR, !PIPE>;
