@@ -116,9 +116,10 @@ int32_t gdnt_conv_workspace_bytes(const gdn_dims* dims, int32_t n_seqs, int64_t 
  * fl(m / 127), q = v * up rounded once to the nearest integer, ties to even;
  * the stored value is q * scale (finite also where m is the largest number:
  * a scale whose 127-fold is not finite counts as the next one below it).  A
- * block with m < 2^-100 is stored as zeros, one with an Inf or NaN as NaNs.  Layout, with nb = ceil(n_rows/16)
- * and n4 = ceil(channels/64)*16: int8 q[nb][3][n4][16][4] (tensor x, a, b;
- * row and channel within the block innermost), then fp32 scale[nb][3][n4].
+ * block with m < 2^-100 is stored as zeros, one with an Inf or NaN as NaNs.
+ * Layout, with nb = ceil(n_rows/16) and n4 = ceil(channels/64)*16: int8
+ * q[nb][3][n4][16][4] (tensor x, a, b; row and channel within the block
+ * innermost), then fp32 scale[nb][3][n4].
  * Batches of at most 4096 sequences with 0 < max_seqlen <= 8 that keep
  * nothing are computed by one launch, others by two. */
 int32_t gdnt_scan_forward(const gdnt_scan_dims* dims, const gdnt_scan_params* params,

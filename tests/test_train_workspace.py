@@ -94,3 +94,31 @@ def test_a_smaller_batch_in_a_larger_ones_workspace(rows):
     assert all(torch.equal(p, q) for p, q in zip(got, want))
     assert bool((whole[size:] == 0xA5).all())
     assert np.isfinite(got.d_conv_w.cpu().numpy()).all()
+
+
+@pytest.mark.gpu
+def test_pools_of_different_sizes():
+    """A page that one of the two pools lacks is skipped and flagged; a backward call told the smaller number skips
+    the same sequence, whose gradients are then nobody's."""
+    import oracle.train as ora
+    import torch
+    from gpu_util import DEV, gdn
+    from train_util import Case, check_grads
+    g = gdn()
+    c = Case([40, 300, 9], 64, "f32", "f32", seed=73)
+    few = int(c.pages.max())  # one page too few for one sequence
+    gone = int(np.argmax(c.pages))
+    pool, err = g.StatePool(c.h0.to(DEV)), torch.zeros(1, dtype=torch.int32, device=DEV)
+    small, saved = g.StatePool(torch.full((few, 64), float("nan"), device=DEV)), c.saved()
+    h = c.empty_rows()
+    g.gdnt_scan_forward(c.dims, c.params, c.t["x"], c.t["a"], c.t["b"], c.batch, pool, small, h=h, saved=saved, err=err)
+    assert int(err.item()) == g.GDN_DEVERR_PAGE
+    span = c.spans[gone]
+    assert bool(torch.isnan(h[span[0]:span[1]]).all())
+    err.zero_()
+    out = g.gdnt_scan_backward(c.dims, c.params, c.batch, g.StatePool(pool.buf[:few]), saved, c.t["dh"], x=c.t["x"],
+                               a=c.t["a"], b=c.t["b"], d_state=torch.from_numpy(c.d_state).to(DEV), out=c.grads_out(),
+                               err=err)
+    assert int(err.item()) == g.GDN_DEVERR_PAGE
+    c.spans[gone] = None
+    check_grads(c, out, ora)
