@@ -1,4 +1,4 @@
-"""ctypes mirror of include/gdn.h and include/gdn_train.h and the loader of libgdn.so.
+"""ctypes mirror of include/gdn.h, include/gdn_train.h and include/gdn_linear.h and the loader of libgdn.so.
 
 The library is loaded after torch so that it binds to the HIP runtime torch
 already holds (both answer to the soname libamdhip64.so.7).  There is no
@@ -24,13 +24,19 @@ GDN_MIXED_AUTO, GDN_MIXED_ONE_LAUNCH, GDN_MIXED_TWO_LAUNCHES = 0, 1, 2
 GDN_NOALLOC_SYNC_WORDS = 65536
 GDNT_SCAN_BLOCK, GDNT_CKPT_ROWS, GDNT_CKPT_CHANNELS = 256, 16, 4
 GDNT_DEVERR_TIMEOUT = 32
+GDNL_CACHE_COLS = 64
+GDNL_NORM_RMS, GDNL_NORM_L2 = 0, 1
+GDNL_PAIRS_HALVES, GDNL_PAIRS_NEIGHBOURS = 0, 1
 
 SYMBOLS = ("gdn_abi_version", "gdn_status_str", "gdn_spec_page_layout", "gdn_chunked_workspace_bytes",
            "gdn_conv_update", "gdn_recurrent_seq", "gdn_recurrent_seq_noalloc", "gdn_chunked_prefill", "gdn_prefill_path", "gdn_prefill",
            "gdn_spec_verify", "gdn_spec_verify_cached", "gdn_prefix_restore", "gdn_mixed_step",
            "gdn_mixed_launches", "gdn_mixed_step_launches",
            "gdnt_scan_workspace_bytes", "gdnt_scan_saved_bytes", "gdnt_conv_workspace_bytes",
-           "gdnt_scan_forward", "gdnt_scan_backward", "gdnt_conv_backward")
+           "gdnt_scan_forward", "gdnt_scan_backward", "gdnt_conv_backward",
+           "gdnl_attend_workspace_bytes", "gdnl_attend_forward", "gdnl_attend_backward",
+           "gdnl_rotate_workspace_bytes", "gdnl_rotate_forward", "gdnl_rotate_backward",
+           "gdnl_cache_bytes", "gdnl_cache_store", "gdnl_cache_load")
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -89,6 +95,20 @@ class GdntScanDims(ctypes.Structure):
 
 class GdntScanParams(ctypes.Structure):
     _fields_ = [("a_log", _vp), ("dt_bias", _vp)]
+
+
+class GdnlDims(ctypes.Structure):
+    _fields_ = [("h_k", _i32), ("h_v", _i32), ("d_k", _i32), ("d_v", _i32), ("act_dtype", _i32),
+                ("state_dtype", _i32), ("scale", ctypes.c_float)]
+
+
+class GdnlRotateDims(ctypes.Structure):
+    _fields_ = [("h_q", _i32), ("h_k", _i32), ("d", _i32), ("rot", _i32), ("act_dtype", _i32), ("norm", _i32),
+                ("pairs", _i32), ("eps", ctypes.c_float)]
+
+
+class GdnlCache(ctypes.Structure):
+    _fields_ = [("q", _vp), ("scale", _vp), ("n_entries", _i32)]
 
 
 _lib = None
@@ -175,5 +195,28 @@ def load() -> ctypes.CDLL:
     L.gdnt_conv_backward.argtypes = [ctypes.POINTER(GdnDims), _vp, _vp, _i64, _vp, _i32, _i64,
                                      ctypes.POINTER(GdnBatch), GdnConvPool, _i32, _vp, _vp, _i64, _vp, _vp,
                                      _vp, sz, _vp, _vp]
+    dims, rot = ctypes.POINTER(GdnlDims), ctypes.POINTER(GdnlRotateDims)
+    L.gdnl_attend_workspace_bytes.restype = _i32
+    L.gdnl_attend_workspace_bytes.argtypes = [dims, _i32, _i64, _i32, szp]
+    L.gdnl_attend_forward.restype = _i32
+    L.gdnl_attend_forward.argtypes = [dims, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, ctypes.POINTER(GdnBatch),
+                                      GdnStatePool, GdnStatePool, _vp, _i64, _vp, sz, _vp, _vp]
+    L.gdnl_attend_backward.restype = _i32
+    L.gdnl_attend_backward.argtypes = [dims, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, ctypes.POINTER(GdnBatch),
+                                       GdnStatePool, _vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _vp,
+                                       _vp, sz, _vp, _vp]
+    L.gdnl_rotate_workspace_bytes.restype = _i32
+    L.gdnl_rotate_workspace_bytes.argtypes = [rot, _i64, szp]
+    L.gdnl_rotate_forward.restype = _i32
+    L.gdnl_rotate_forward.argtypes = [rot, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp]
+    L.gdnl_rotate_backward.restype = _i32
+    L.gdnl_rotate_backward.argtypes = [rot, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _i64,
+                                       _vp, _i64, _vp, _i64, _vp, _vp, _vp, sz, _vp]
+    L.gdnl_cache_bytes.restype = _i32
+    L.gdnl_cache_bytes.argtypes = [dims, _i32, szp, szp]
+    L.gdnl_cache_store.restype = _i32
+    L.gdnl_cache_store.argtypes = [dims, _i32, _vp, _vp, GdnStatePool, ctypes.POINTER(GdnlCache), _vp, _vp]
+    L.gdnl_cache_load.restype = _i32
+    L.gdnl_cache_load.argtypes = [dims, _i32, _vp, _vp, ctypes.POINTER(GdnlCache), GdnStatePool, _vp, _vp]
     _lib = L
     return L

@@ -1,0 +1,152 @@
+// gdnl_kernels.h -- argument blocks and launchers of the operators of
+// include/gdn_linear.h (the C ABI in gdnl_api.cpp validates arguments and
+// calls these).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace gdnl {
+
+constexpr int kChunk = 64;       // rows that meet each other by matrix products
+constexpr int kThreads = 256;    // of every kernel here
+constexpr int kMaxDim = 128;     // head dims of the attend kernels
+
+// A run of one sequence's rows that a workgroup walks: packed rows
+// [row, row + rows), rows 0 for a slot that no segment has.
+struct Segment {
+    int32_t seq, row, rows, page;
+    bool first, last;            // of its sequence
+};
+struct SegWord { int32_t seq, row, rows, page; };  // page: page * 4 + 2 * last + first
+// Where a sequence's segments stand: slots [slot, slot + n), n 0 for none.
+struct SeqSlots { int32_t slot, n; };
+
+// Segments of `len` rows (a multiple of 64) of every valid sequence: segment i
+// of sequence s has slot s + cu[s] / len + i.  Valid sequences do not overlap,
+// so their slots do not either, and all are below n_seqs + ceil(n_rows / len).
+struct SegmentArgs {
+    const int32_t* cu; const int32_t* page_idx; int32_t n_seqs;
+    int64_t n_rows, n_slots;
+    int32_t len, max_len, page_limit;
+    SegWord* segs; SeqSlots* seqs;
+    // a backward pass hands the gradient of empty sequences through and clears
+    // that of skipped ones: `pass_width` values a sequence, NULL src: zeros
+    const float* pass_src; float* pass_dst; int64_t pass_width;
+    float* zero; int64_t n_zero;   // floats to clear
+    int32_t* err;
+};
+hipError_t launch_segments(const SegmentArgs& a, hipStream_t s);
+
+struct Rows {                    // packed rows of heads
+    const void* p; int64_t stride;
+    int32_t per;                 // value heads to a head of these rows
+    int32_t vec;                 // rows and heads on 16 bytes
+};
+
+// Where a segment's state comes from or goes to.
+enum StateAt { kNoState = 0, kByPage, kBySeq, kBySlot };
+struct States {
+    void* p; int32_t at, bf16;
+    int64_t unit, head;          // elements from page (sequence, slot) to the next, from head to head
+    int32_t rs, cs;              // from row to row and column to column of the matrix the kernel holds
+};
+
+// One pass of linear attention over segments, forward or backward in time.
+// For output row x and source row y of a chunk, y <= x forward, y >= x backward:
+//   out_x = f_p sum_y e^{|G_x - G_y|}' (q_x . k_y) v_y + f_i e^{..} q_x^T S,
+//   S <- e^{G_C} S + f_u sum_y e^{..} k_y v_y^T,
+// forward with e^{G_x - G_y}, e^{G_x}, e^{G_C - G_y}, backward with e^{G_y -
+// G_x}, e^{G_C - G_x}, e^{G_y}; G the inclusive sum of g within the chunk.
+struct AttendArgs {
+    const SegWord* segs; int64_t n_slots;
+    Rows q, k, v, x;
+    const float* g; int64_t g_stride;
+    const uint8_t* has_init;
+    int32_t dk, dv, heads;       // widths of q, k and of v, out; value heads
+    int32_t back;
+    float f_p, f_i, f_u;
+    States in, out;              // out: at the end of the sequence (local sums: of the segment)
+    int32_t zero_uninit;         // out is zero where has_init is 0
+    void* o; int64_t o_stride; int32_t o_f32;
+    float* dot;                  // [heads][n_rows]: see kDot, kDotRows
+    int64_t n_rows;
+    double* total;               // [slot][heads]: the segment's sum of g, local sums only
+};
+enum AttendMode {
+    kAttend = 0,
+    kDot,        // also dot_x = x_x . (f_i part of out_x), over the columns
+    kDotRows,    // the same, plus row sums less column sums of M_xy = (f_p e^{..} q_x.k_y)(x_x.v_y), y != x
+    kLocal       // the state's sum over the segment alone, from zero
+};
+hipError_t launch_attend_bf16(const AttendArgs& a, int mode, hipStream_t s);
+hipError_t launch_attend_f32(const AttendArgs& a, int mode, hipStream_t s);
+
+// S in front of (back: behind) every segment in the place of its local sum.
+struct ScanArgs {
+    const SeqSlots* seqs; const int32_t* page_idx; const uint8_t* has_init;
+    int32_t n_seqs, heads, size, back;   // size: dk * dv
+    States in;
+    float* local; const double* total;
+};
+hipError_t launch_state_scan(const ScanArgs& a, hipStream_t s);
+
+// dg_t = X + sum_{i >= t} (rows_i - cols_i) within a segment, X = <state, its
+// gradient> at the segment's end.
+struct GateArgs {
+    const SegWord* segs; int64_t n_slots, n_rows;
+    int32_t heads, size;
+    const float* g; int64_t g_stride;
+    const float* rows; const float* cols;          // [heads][n_rows]
+    const float* before; const float* after;       // [slot][heads][size], NULL: one segment to a sequence
+    const float* last; const float* d_state;       // [seq][heads][size]; d_state NULL: X is 0 at a sequence's end
+    float* dg;                                     // [n_rows][heads], or with g_stride 0:
+    double* part;                                  // [slot][heads]
+};
+hipError_t launch_gate(const GateArgs& a, hipStream_t s);
+hipError_t launch_gate_sum(const double* part, int64_t n_slots, int32_t heads, float* dg, hipStream_t s);
+
+// out[row][h][c] = sum over a group's value heads of part[row][h * per + j][c], in order.
+struct GroupArgs {
+    const SegWord* segs; int64_t n_slots;
+    int32_t heads, per, d, bf16;
+    const float* part; void* out; int64_t stride;
+};
+hipError_t launch_group_sum(const GroupArgs& a, hipStream_t s);
+
+// Sequences of a few rows, one workgroup to a sequence and value head.
+struct TokenArgs {
+    const int32_t* cu; const int32_t* page_idx; const uint8_t* has_init;
+    int32_t n_seqs, max_len, page_limit; int64_t n_rows;
+    const void* q; const void* k; const void* v; const float* g; void* o;
+    int64_t q_stride, k_stride, v_stride, g_stride, o_stride;
+    const void* st_in; int64_t st_in_stride; void* st_out; int64_t st_out_stride;
+    int32_t heads, per, dk, dv, act_bf16, state_bf16, vec;
+    float scale;
+    int32_t* err;
+};
+hipError_t launch_tokens(const TokenArgs& a, hipStream_t s);
+
+struct RotateArgs {
+    const void* x[2]; const void* dy[2]; void* y[2];   // q, k; y: the output, or dx
+    int64_t x_stride[2], dy_stride[2], y_stride[2];
+    const float* w[2];
+    const int32_t* pos; const float* inv_freq;
+    int64_t n_rows;
+    int32_t heads[2], d, rot, neighbours, bf16, vec;
+    float over, eps;             // the sum of squares is divided by `over`
+    float* part; float* dw[2];   // backward: [groups][2][d]
+};
+int64_t rotate_groups(int64_t n_rows);
+hipError_t launch_rotate(const RotateArgs& a, bool back, hipStream_t s);
+
+struct CacheArgs {
+    int32_t n; const int32_t* page; const int32_t* entry;
+    void* st; int64_t st_stride; int32_t n_pages, bf16, vec;
+    int8_t* q; float* scale; int32_t n_entries;
+    int64_t rows; int32_t dv;    // rows of an entry (heads * d_k) and their width
+    int32_t* err;
+};
+hipError_t launch_cache(const CacheArgs& a, bool store, hipStream_t s);
+
+}  // namespace gdnl

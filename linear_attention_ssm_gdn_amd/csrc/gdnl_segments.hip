@@ -1,0 +1,244 @@
+// gdnl_segments.hip -- which rows a workgroup of the chunked kernels walks,
+// the states between segments, the gates' gradient and the sum over the value
+// heads of a key head.
+#include "gdn_device.hpp"
+#include "gdnl_kernels.h"
+#include "gdnt_device.hpp"
+
+namespace gdnl {
+
+using gdnt::bounds_ok;
+using gdnt::raise;
+using gdnt::valid_slow;
+
+// One thread to a slot finds its segment by bisection of cu_seqlens; every
+// workgroup first looks all of cu_seqlens over, and takes the slow check of a
+// sequence's validity where a bound is bad.  About a launch's time.
+__global__ __launch_bounds__(kThreads) void k_segments(const SegmentArgs A) {
+    const int tid = threadIdx.x;
+    const int64_t gid = (int64_t)blockIdx.x * kThreads + tid, stride = (int64_t)gridDim.x * kThreads;
+    bool bad = false;
+    for (int s = tid; s < A.n_seqs; s += kThreads) bad |= !bounds_ok(A.n_rows, A.cu[s], A.cu[s + 1]);
+    bad = __syncthreads_or(bad) != 0;
+    auto live = [&](int s) {
+        const int page = A.page_idx[s];
+        return page >= 0 && page < A.page_limit && !(bad && !valid_slow(A.cu, A.n_rows, s)) &&
+               (A.max_len == 0 || A.cu[s + 1] - A.cu[s] <= A.max_len);
+    };
+    for (int64_t slot = gid; slot < A.n_slots; slot += stride) {
+        SegWord w{0, 0, 0, 0};
+        // the last s with s + cu[s] / len <= slot; with a bad bound somewhere any valid s whose slots hold it
+        int lo = 0, hi = A.n_seqs;
+        if (!bad) {
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if ((int64_t)mid + A.cu[mid] / A.len <= slot) lo = mid + 1;
+                else hi = mid;
+            }
+            hi = lo;
+            lo = hi - 1;
+        }
+        for (int s = lo < 0 ? 0 : lo; s < hi; ++s) {
+            const int c0 = A.cu[s], c1 = A.cu[s + 1];
+            if (bad && !bounds_ok(A.n_rows, c0, c1)) continue;
+            const int64_t at = slot - ((int64_t)s + c0 / A.len);
+            if (at < 0 || at * A.len >= c1 - c0 || !live(s)) continue;
+            const int row = c0 + (int)at * A.len, rows = c1 - row < A.len ? c1 - row : A.len;
+            w = SegWord{s, row, rows, A.page_idx[s] * 4 + (row + rows == c1 ? 2 : 0) + (at == 0 ? 1 : 0)};
+            break;
+        }
+        A.segs[slot] = w;
+    }
+    for (int64_t s = gid; s < A.n_seqs; s += stride) {
+        const bool ok = live((int)s);
+        const int len = ok ? A.cu[s + 1] - A.cu[s] : 0;
+        A.seqs[s] = SeqSlots{ok ? (int)s + A.cu[s] / A.len : 0, ok ? (int)(((int64_t)len + A.len - 1) / A.len) : 0};
+    }
+    for (int64_t j = gid; j < A.n_zero; j += stride) A.zero[j] = 0.0f;
+    if (blockIdx.x == 0) {
+        for (int s = tid; s < A.n_seqs; s += kThreads) {
+            const int page = A.page_idx[s];
+            if (page < 0) continue;
+            if (page >= A.page_limit) raise(A.err, GDN_DEVERR_PAGE);
+            else if (bad && !valid_slow(A.cu, A.n_rows, s)) raise(A.err, GDN_DEVERR_BATCH);
+            else if (A.max_len > 0 && A.cu[s + 1] - A.cu[s] > A.max_len) raise(A.err, GDN_DEVERR_BATCH);
+        }
+    }
+    if (A.pass_dst) {  // gradients of sequences that no kernel behind this one writes
+        for (int s = blockIdx.x; s < A.n_seqs; s += gridDim.x) {
+            const bool ok = live(s);
+            if (ok && A.cu[s] != A.cu[s + 1]) continue;
+            const int64_t at = (int64_t)s * A.pass_width;
+            for (int64_t j = tid; j < A.pass_width; j += kThreads)
+                A.pass_dst[at + j] = ok && A.pass_src ? A.pass_src[at + j] : 0.0f;
+        }
+    }
+}
+
+hipError_t launch_segments(const SegmentArgs& a, hipStream_t s) {
+    int64_t n = a.n_slots > a.n_seqs ? a.n_slots : a.n_seqs;
+    int64_t grid = (n + kThreads - 1) / kThreads;
+    if (a.pass_dst && grid < a.n_seqs) grid = a.n_seqs;
+    grid = grid < 1 ? 1 : grid > 1024 ? 1024 : grid;
+    hipLaunchKernelGGL(k_segments, dim3((unsigned)grid), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+// Four values of a state to a thread, a segment after the other.
+constexpr int kScanMine = 4;
+__global__ __launch_bounds__(kThreads) void k_state_scan(const ScanArgs A, int blocks) {
+    for (int64_t b = blockIdx.x; b < (int64_t)A.n_seqs * A.heads * blocks; b += gridDim.x) {
+        const int part = (int)(b % blocks), head = (int)(b / blocks % A.heads), seq = (int)(b / blocks / A.heads);
+        const SeqSlots at = A.seqs[seq];
+        if (at.n <= 0) continue;
+        const bool zero = A.in.at == kNoState || (A.in.at == kByPage && A.has_init && A.has_init[seq] == 0);
+        const int64_t base = zero ? 0 : (A.in.at == kByPage ? (int64_t)A.page_idx[seq] : (int64_t)seq) * A.in.unit + head * A.in.head;
+        float cur[kScanMine];
+#pragma unroll
+        for (int j = 0; j < kScanMine; ++j) {
+            const int e = (part * kScanMine + j) * kThreads + threadIdx.x;
+            cur[j] = zero || e >= A.size ? 0.0f
+                     : A.in.bf16         ? gdn::to_f32(static_cast<const gdn::bf16_t*>(A.in.p)[base + e])
+                                         : static_cast<const float*>(A.in.p)[base + e];
+        }
+        for (int k = 0; k < at.n; ++k) {
+            const int64_t slot = at.slot + (A.back ? at.n - 1 - k : k);
+            float* const p = A.local + (slot * A.heads + head) * A.size;
+            const bool more = k + 1 < at.n;  // the last one's local sum was not made
+            const float decay = more ? (float)exp2(A.total[slot * A.heads + head]) : 0.0f;
+#pragma unroll
+            for (int j = 0; j < kScanMine; ++j) {
+                const int e = (part * kScanMine + j) * kThreads + threadIdx.x;
+                if (e < A.size) {
+                    const float own = more ? p[e] : 0.0f;
+                    p[e] = cur[j];
+                    cur[j] = fmaf(decay, cur[j], own);
+                }
+            }
+        }
+    }
+}
+hipError_t launch_state_scan(const ScanArgs& a, hipStream_t s) {
+    const int blocks = (a.size + kScanMine * kThreads - 1) / (kScanMine * kThreads);
+    int64_t grid = (int64_t)a.n_seqs * a.heads * blocks;
+    if (grid > (1 << 20)) grid = 1 << 20;
+    hipLaunchKernelGGL(k_state_scan, dim3((unsigned)grid), dim3(kThreads), 0, s, a, blocks);
+    return hipGetLastError();
+}
+
+__device__ __forceinline__ double block_sum(double v, double* s_part) {
+#pragma unroll
+    for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, 64);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) s_part[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return (s_part[0] + s_part[1]) + (s_part[2] + s_part[3]);
+}
+
+// A workgroup to a segment and head: <state, its gradient> at the segment's
+// end, then the suffix sums, 256 rows at a time from the last, in 64 bits.
+__global__ __launch_bounds__(kThreads) void k_gate(const GateArgs A) {
+    __shared__ double s_part[4];
+    __shared__ double s_wave[4];
+    const int64_t slot = blockIdx.x / A.heads;
+    const int head = (int)(blockIdx.x % A.heads), tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int4 w = *reinterpret_cast<const int4*>(A.segs + slot);
+    const int row0 = w.y, rows = w.z;
+    const bool is_last = (w.w & 2) != 0;
+    if (rows <= 0) {
+        if (A.part && tid == 0) A.part[blockIdx.x] = 0.0;
+        return;
+    }
+    const float* p = nullptr;
+    const float* e = nullptr;
+    if (is_last && A.d_state) {
+        p = A.last + ((int64_t)w.x * A.heads + head) * A.size;
+        e = A.d_state + ((int64_t)w.x * A.heads + head) * A.size;
+    } else if (!is_last) {
+        p = A.before + ((slot + 1) * A.heads + head) * A.size;
+        e = A.after + (slot * A.heads + head) * A.size;
+    }
+    double x = 0.0;
+    if (p)
+        for (int j = tid; j < A.size; j += kThreads) x += (double)p[j] * (double)e[j];
+    double carry = block_sum(x, s_part), sum = 0.0;
+    for (int t0 = (rows - 1) / kThreads * kThreads; t0 >= 0; t0 -= kThreads) {
+        // thread 0 takes the tile's last row
+        const int t = t0 + kThreads - 1 - tid;
+        double v = 0.0;
+        if (t < rows) {
+            const int64_t at = (int64_t)head * A.n_rows + row0 + t;
+            v = (double)A.rows[at] - (double)A.cols[at];
+        }
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const double up = __shfl_up(v, d, 64);
+            if (lane >= d) v += up;
+        }
+        __syncthreads();
+        if (lane == 63) s_wave[wave] = v;
+        __syncthreads();
+        double front = carry;
+        for (int k = 0; k < 4; ++k) {
+            if (k < wave) front += s_wave[k];
+            carry += s_wave[k];
+        }
+        if (t < rows) {
+            // a decay of 0 lets no gradient through
+            const float gv = A.g[((int64_t)row0 + t) * A.g_stride + head];
+            const double dg = gv < -128.0f ? 0.0 : front + v;
+            if (A.part) sum += dg;
+            else A.dg[((int64_t)row0 + t) * A.heads + head] = (float)dg;
+        }
+    }
+    if (A.part) {
+        sum = block_sum(sum, s_part);
+        if (tid == 0) A.part[blockIdx.x] = sum;
+    }
+}
+hipError_t launch_gate(const GateArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL(k_gate, dim3((unsigned)(a.n_slots * a.heads)), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+}
+
+__global__ __launch_bounds__(kThreads) void k_gate_sum(const double* part, int64_t n_slots, int32_t heads, float* dg) {
+    __shared__ double s_part[4];
+    double v = 0.0;
+    for (int64_t j = threadIdx.x; j < n_slots; j += kThreads) v += part[j * heads + blockIdx.x];
+    v = block_sum(v, s_part);
+    if (threadIdx.x == 0) dg[blockIdx.x] = (float)v;
+}
+hipError_t launch_gate_sum(const double* part, int64_t n_slots, int32_t heads, float* dg, hipStream_t s) {
+    hipLaunchKernelGGL(k_gate_sum, dim3((unsigned)heads), dim3(kThreads), 0, s, part, n_slots, heads, dg);
+    return hipGetLastError();
+}
+
+// A workgroup to 16 rows of a segment.
+constexpr int kGroupRows = 16;
+__global__ __launch_bounds__(kThreads) void k_group_sum(const GroupArgs A, int blocks) {
+    const int64_t slot = blockIdx.x / blocks;
+    const int4 w = *reinterpret_cast<const int4*>(A.segs + slot);
+    const int width = A.heads / A.per * A.d;
+    for (int t0 = (int)(blockIdx.x % blocks) * kGroupRows; t0 < w.z; t0 += blocks * kGroupRows) {
+        const int n = min(kGroupRows, w.z - t0);
+        for (int j = threadIdx.x; j < n * width; j += kThreads) {
+            const int t = j / width, c = j - t * width, h = c / A.d, d = c - h * A.d;
+            const int64_t row = (int64_t)w.y + t0 + t;
+            const float* p = A.part + (row * A.heads + (int64_t)h * A.per) * A.d + d;
+            float v = 0.0f;
+            for (int q = 0; q < A.per; ++q) v += p[(int64_t)q * A.d];
+            const int64_t at = row * A.stride + c;
+            if (A.bf16) static_cast<gdn::bf16_t*>(A.out)[at] = gdn::f32_to_bf16(v);
+            else static_cast<float*>(A.out)[at] = v;
+        }
+    }
+}
+hipError_t launch_group_sum(const GroupArgs& a, hipStream_t s) {
+    // enough workgroups for the card whatever the segments' length
+    int64_t blocks = (8192 + a.n_slots - 1) / a.n_slots;
+    blocks = blocks > 128 ? 128 : blocks;
+    hipLaunchKernelGGL(k_group_sum, dim3((unsigned)(a.n_slots * blocks)), dim3(kThreads), 0, s, a, (int)blocks);
+    return hipGetLastError();
+}
+
+}  // namespace gdnl
