@@ -26,7 +26,7 @@
  *   pass hands the gradient of their final state through to the initial one,
  *   whatever has_init says.
  * - A row holds its heads one behind the other.  Any row stride from the row's
- *   width up and any element-aligned pointer is accepted.  Rows on 16 bytes
+ *   width to 2^24 and any element-aligned pointer is accepted.  Rows on 16 bytes
  *   whose heads are a multiple of 16 bytes wide are faster.
  * - Inputs and outputs of one call must not overlap, but a state pool may be
  *   both state_in and state_out.

@@ -20,7 +20,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 SOURCES = ["gdn_api.cpp", "gdn_seq.hip", "gdn_conv.hip", "gdn_verify.hip", "gdn_chunked.hip", "gdn_mixed.hip",
            "gdn_noalloc.hip", "gdnt_api.cpp", "gdnt_map.hip", "gdnt_scan.hip",
            "gdnt_scan_bwd.hip", "gdnt_conv.hip", "gdnl_api.cpp", "gdnl_segments.hip", "gdnl_attend_bf16.hip",
-           "gdnl_attend_f32.hip", "gdnl_tokens.hip", "gdnl_rotate.hip", "gdnl_cache.hip"]
+           "gdnl_attend_bf16_back.hip", "gdnl_attend_f32.hip", "gdnl_attend_f32_back.hip", "gdnl_tokens.hip", "gdnl_rotate.hip", "gdnl_cache.hip"]
 FLAGS = [
     "--offload-arch=gfx950", "-mcode-object-version=5", "-O3", "-std=c++17", "-fPIC",
     "-fvisibility=hidden", "-ffp-contract=off", "-Wall", "-Wno-unused-function",

@@ -29,7 +29,8 @@ int32_t from_hip(hipError_t e) { return e == hipSuccess ? GDN_OK : GDN_ERR_LAUNC
 size_t round_up(size_t v) { return (v + 255) / 256 * 256; }
 
 bool rows_ok(const void* p, int64_t stride, int64_t width, int32_t dt) {
-    return p && stride >= width && stride <= (1 << 30) && aligned(p, (size_t)elem_size(dt));
+    // a chunk's rows are addressed by 32-bit byte offsets
+    return p && stride >= width && stride <= (1 << 24) && aligned(p, (size_t)elem_size(dt));
 }
 // `bytes`: what rows and heads have to be multiples of.
 bool rows_on(const void* p, int64_t stride, int64_t d, int32_t dt, int64_t bytes) {
@@ -78,7 +79,7 @@ int64_t most_slots(int64_t n_seqs, int64_t n_rows, int64_t heads) {
 }
 
 struct Ws {
-    size_t segs, seqs, total, before, after, rows, cols, last, gate, part, all;
+    size_t segs, seqs, total, gates, before, after, rows, cols, last, gate, part, all;
 };
 Ws layout(const gdnl_dims* d, int64_t slots, int64_t n_seqs, int64_t n_rows, bool backward) {
     Ws w{};
@@ -92,6 +93,7 @@ Ws layout(const gdnl_dims* d, int64_t slots, int64_t n_seqs, int64_t n_rows, boo
     w.segs = take((size_t)slots * sizeof(gdnl::SegWord));
     w.seqs = take((size_t)n_seqs * sizeof(gdnl::SeqSlots));
     w.total = take((size_t)slots * H * sizeof(double));
+    w.gates = take(H * (size_t)n_rows * sizeof(float4));
     w.before = take((size_t)slots * H * size * sizeof(float));
     if (backward) {
         w.after = take((size_t)slots * H * size * sizeof(float));
@@ -105,9 +107,6 @@ Ws layout(const gdnl_dims* d, int64_t slots, int64_t n_seqs, int64_t n_rows, boo
     return w;
 }
 
-gdnl::Rows rows_of(const void* p, int64_t stride, int64_t d, int32_t per, int32_t dt) {
-    return gdnl::Rows{p, stride, per, rows_on(p, stride, d, dt, 16) ? 1 : 0};
-}
 gdnl::States pages_of(const gdnl_dims* d, const gdn_state_pool& s) {
     return gdnl::States{s.base, gdnl::kByPage, d->state_dtype == GDN_BF16 ? 1 : 0, s.page_stride,
                         (int64_t)d->d_k * d->d_v, d->d_v, 1};
@@ -134,10 +133,6 @@ Plan plan_of(const gdnl_dims* d, const gdn_batch* b) {
     if (!p.split) p.len = kSegWhole;
     p.slots = slots_of(b->n_seqs, b->n_rows, p.len);
     return p;
-}
-
-hipError_t run(const gdnl::AttendArgs& a, int mode, int32_t dt, hipStream_t s) {
-    return dt == GDN_BF16 ? gdnl::launch_attend_bf16(a, mode, s) : gdnl::launch_attend_f32(a, mode, s);
 }
 
 }  // namespace
@@ -168,7 +163,7 @@ GDN_EXPORT int32_t gdnl_attend_forward(const gdnl_dims* dims, const void* q, int
     const int64_t wk = (int64_t)dims->h_k * dims->d_k, wv = (int64_t)H * dims->d_v;
     if (batch->n_rows > 0 && (!rows_ok(q, q_stride, wk, dt) || !rows_ok(k, k_stride, wk, dt) ||
                               !rows_ok(v, v_stride, wv, dt) || !rows_ok(o, o_stride, wv, dt) || !g || !aligned(g, 4) ||
-                              (g_stride != 0 && (g_stride < H || g_stride > (1 << 30)))))
+                              (g_stride != 0 && (g_stride < H || g_stride > (1 << 24)))))
         return GDN_ERR_ARG;
     const hipStream_t s = (hipStream_t)stream;
     const int32_t limit = state_in.n_pages < state_out.n_pages ? state_in.n_pages : state_out.n_pages;
@@ -206,16 +201,20 @@ GDN_EXPORT int32_t gdnl_attend_forward(const gdnl_dims* dims, const void* q, int
 
     gdnl::AttendArgs A{};
     A.segs = G.segs; A.n_slots = p.slots; A.n_rows = batch->n_rows;
-    A.q = rows_of(q, q_stride, dims->d_k, per, dt);
-    A.k = rows_of(k, k_stride, dims->d_k, per, dt);
-    A.v = rows_of(v, v_stride, dims->d_v, 1, dt);
-    A.g = g; A.g_stride = g_stride; A.has_init = batch->has_init;
+    A.q = {q, q_stride, per};
+    A.k = {k, k_stride, per};
+    A.v = {v, v_stride, 1};
+    A.vec = rows_on(q, q_stride, dims->d_k, dt, 16) && rows_on(k, k_stride, dims->d_k, dt, 16) &&
+            rows_on(v, v_stride, dims->d_v, dt, 16) && rows_on(o, o_stride, dims->d_v, dt, 16);
+    A.has_init = batch->has_init;
     A.dk = dims->d_k; A.dv = dims->d_v; A.heads = H;
     A.f_p = A.f_i = dims->scale; A.f_u = 1.0f;
-    A.total = total;
+    A.gates = reinterpret_cast<const float4*>(ws + w.gates);
+    gdnl::DecayArgs D{G.segs, p.slots, batch->n_rows, H, g, g_stride, reinterpret_cast<float4*>(ws + w.gates), total};
+    if ((e = gdnl::launch_decays(D, s)) != hipSuccess) return from_hip(e);
     if (p.split) {
         A.out = dense(dims, before, gdnl::kBySlot);
-        if ((e = run(A, gdnl::kLocal, dt, s)) != hipSuccess) return from_hip(e);
+        if ((e = gdnl::launch_attend(A, gdnl::kLocal, false, dt == GDN_BF16, s)) != hipSuccess) return from_hip(e);
         gdnl::ScanArgs C{G.seqs, batch->page_idx, batch->has_init, batch->n_seqs, H, dims->d_k * dims->d_v, 0,
                          pages_of(dims, state_in), before, total};
         if ((e = gdnl::launch_state_scan(C, s)) != hipSuccess) return from_hip(e);
@@ -224,7 +223,7 @@ GDN_EXPORT int32_t gdnl_attend_forward(const gdnl_dims* dims, const void* q, int
     A.out = pages_of(dims, state_out);
     A.o = o; A.o_stride = o_stride;
     A.o_f32 = dt == GDN_F32;
-    return from_hip(run(A, gdnl::kAttend, dt, s));
+    return from_hip(gdnl::launch_attend(A, gdnl::kAttend, false, dt == GDN_BF16, s));
 }
 
 GDN_EXPORT int32_t gdnl_attend_backward(const gdnl_dims* dims, const void* q, int64_t q_stride, const void* k,
@@ -240,7 +239,7 @@ GDN_EXPORT int32_t gdnl_attend_backward(const gdnl_dims* dims, const void* q, in
     const int32_t dt = dims->act_dtype, H = dims->h_v, per = H / dims->h_k;
     const hipStream_t s = (hipStream_t)stream;
     if (!aligned(dg, 4) || !aligned(d_state, 4) || !aligned(d_state0, 4)) return GDN_ERR_ARG;
-    if (g_stride != 0 && (g_stride < H || g_stride > (1 << 30))) return GDN_ERR_ARG;
+    if (g_stride != 0 && (g_stride < H || g_stride > (1 << 24))) return GDN_ERR_ARG;
     const bool one_decay = g_stride == 0;
     if (batch->n_seqs == 0) return dg && one_decay ? from_hip(gdnl::launch_gate_sum(nullptr, 0, H, dg, s)) : GDN_OK;
     if ((st = check_pool(dims, state_in)) != GDN_OK) return st;
@@ -274,24 +273,29 @@ GDN_EXPORT int32_t gdnl_attend_backward(const gdnl_dims* dims, const void* q, in
     float* const part = reinterpret_cast<float*>(ws + w.part);
     double* const total = reinterpret_cast<double*>(ws + w.total);
 
-    const gdnl::Rows rq = rows_of(q, q_stride, dims->d_k, per, dt), rk = rows_of(k, k_stride, dims->d_k, per, dt);
-    const gdnl::Rows rv = rows_of(v, v_stride, dims->d_v, 1, dt), ro = rows_of(d_o, do_stride, dims->d_v, 1, dt);
+    const gdnl::Rows rq{q, q_stride, per}, rk{k, k_stride, per}, rv{v, v_stride, 1}, ro{d_o, do_stride, 1};
     gdnl::AttendArgs A{};
+    A.vec = rows_on(q, q_stride, dims->d_k, dt, 16) && rows_on(k, k_stride, dims->d_k, dt, 16) &&
+            rows_on(v, v_stride, dims->d_v, dt, 16) && rows_on(d_o, do_stride, dims->d_v, dt, 16) &&
+            rows_on(dq, dq_stride, dims->d_k, dt, 16) && rows_on(dk, dk_stride, dims->d_k, dt, 16) &&
+            rows_on(dv, dv_stride, dims->d_v, dt, 16);
     A.segs = G.segs; A.n_slots = p.slots; A.n_rows = batch->n_rows;
-    A.g = g; A.g_stride = g_stride; A.has_init = batch->has_init; A.heads = H;
-    A.total = total;
+    A.has_init = batch->has_init; A.heads = H;
+    A.gates = reinterpret_cast<const float4*>(ws + w.gates);
+    gdnl::DecayArgs D{G.segs, p.slots, batch->n_rows, H, g, g_stride, reinterpret_cast<float4*>(ws + w.gates), total};
+    if ((e = gdnl::launch_decays(D, s)) != hipSuccess) return from_hip(e);
     const gdnl::States ends = dense(dims, d_state, gdnl::kBySeq);
     if (p.split) {
         // S in front of every segment, then its gradient behind every segment
         A.k = rk; A.v = rv; A.dk = dims->d_k; A.dv = dims->d_v; A.f_u = 1.0f;
         A.out = dense(dims, before, gdnl::kBySlot);
-        if ((e = run(A, gdnl::kLocal, dt, s)) != hipSuccess) return from_hip(e);
+        if ((e = gdnl::launch_attend(A, gdnl::kLocal, false, dt == GDN_BF16, s)) != hipSuccess) return from_hip(e);
         gdnl::ScanArgs C{G.seqs, batch->page_idx, batch->has_init, batch->n_seqs, H, size, 0, pages_of(dims, state_in),
                          before, total};
         if ((e = gdnl::launch_state_scan(C, s)) != hipSuccess) return from_hip(e);
-        A.k = rq; A.v = ro; A.f_u = dims->scale; A.back = 1;
+        A.k = rq; A.v = ro; A.f_u = dims->scale;
         A.out = dense(dims, after, gdnl::kBySlot);
-        if ((e = run(A, gdnl::kLocal, dt, s)) != hipSuccess) return from_hip(e);
+        if ((e = gdnl::launch_attend(A, gdnl::kLocal, true, dt == GDN_BF16, s)) != hipSuccess) return from_hip(e);
         C.in = ends; C.back = 1; C.local = after;
         if ((e = gdnl::launch_state_scan(C, s)) != hipSuccess) return from_hip(e);
     }
@@ -307,22 +311,22 @@ GDN_EXPORT int32_t gdnl_attend_backward(const gdnl_dims* dims, const void* q, in
     };
     // dq: linear attention of d_o over the rows of v and k
     A.q = ro; A.k = rv; A.v = rk; A.x = rq;
-    A.dk = dims->d_v; A.dv = dims->d_k; A.back = 0;
+    A.dk = dims->d_v; A.dv = dims->d_k;
     A.f_p = A.f_i = dims->scale; A.f_u = 1.0f;
     A.in = turned(p.split ? dense(dims, before, gdnl::kBySlot) : pages_of(dims, state_in));
     A.out = turned(dense(dims, dg && d_state ? last : nullptr, gdnl::kBySeq));
     A.dot = rows;
     to_keys(dq, dq_stride);
-    if ((e = run(A, dg ? gdnl::kDotRows : gdnl::kAttend, dt, s)) != hipSuccess) return from_hip(e);
+    if ((e = gdnl::launch_attend(A, dg ? gdnl::kDotRows : gdnl::kAttend, false, dt == GDN_BF16, s)) != hipSuccess) return from_hip(e);
     if ((e = group(dq, dq_stride)) != hipSuccess) return from_hip(e);
     // dk: of v over d_o and q, backward in time
     A.q = rv; A.k = ro; A.v = rq; A.x = rk;
-    A.back = 1; A.f_i = 1.0f; A.f_u = dims->scale;
+    A.f_i = 1.0f; A.f_u = dims->scale;
     A.in = turned(p.split ? dense(dims, after, gdnl::kBySlot) : ends);
     A.out = gdnl::States{};
     A.dot = cols;
     to_keys(dk, dk_stride);
-    if ((e = run(A, dg ? gdnl::kDot : gdnl::kAttend, dt, s)) != hipSuccess) return from_hip(e);
+    if ((e = gdnl::launch_attend(A, dg ? gdnl::kDot : gdnl::kAttend, true, dt == GDN_BF16, s)) != hipSuccess) return from_hip(e);
     if ((e = group(dk, dk_stride)) != hipSuccess) return from_hip(e);
     // dv: of k over q and d_o, backward in time, and the initial state's gradient
     A.q = rk; A.k = rq; A.v = ro;
@@ -331,7 +335,7 @@ GDN_EXPORT int32_t gdnl_attend_backward(const gdnl_dims* dims, const void* q, in
     A.out = dense(dims, d_state0, gdnl::kBySeq);
     A.zero_uninit = 1;
     A.o = dv; A.o_stride = dv_stride; A.o_f32 = dt == GDN_F32;
-    if ((e = run(A, gdnl::kAttend, dt, s)) != hipSuccess) return from_hip(e);
+    if ((e = gdnl::launch_attend(A, gdnl::kAttend, true, dt == GDN_BF16, s)) != hipSuccess) return from_hip(e);
     if (!dg) return GDN_OK;
     gdnl::GateArgs T{G.segs, p.slots, batch->n_rows, H, size, g, g_stride, rows, cols, before, after, last, d_state, dg,
                      one_decay ? reinterpret_cast<double*>(ws + w.gate) : nullptr};

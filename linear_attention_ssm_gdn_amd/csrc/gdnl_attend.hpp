@@ -1,9 +1,9 @@
 // gdnl_attend.hpp -- linear attention over chunks of 64 rows on matrix cores,
 // forward or backward in time (AttendArgs), for one act type.
 //
-// A workgroup of four waves walks a segment's chunks for one value head; a
-// wave owns 16 NT columns of the head's state S, all DK rows of them, in the
-// accumulators, so S never leaves the registers.  Matrix products reduce over
+// A workgroup walks a segment's chunks for one value head; each of its four or
+// eight waves owns 16 NT columns of the head's state S, all DK rows of them, in
+// the accumulators, so S never leaves the registers.  Matrix products reduce over
 // 32 positions at a time, eight to a lane, and which positions a lane holds is
 // free as long as both operands agree.  The choice here, 4g..4g+3 of two tiles
 // of 16 (g = lane / 16), is how a product leaves its rows in the accumulators:
@@ -14,10 +14,9 @@
 // transposing loads (fp32: value by value), one reading of v serving P v and
 // the update.
 //
-// Decays.  G is summed within a chunk in 64 bits and kept as two floats, so
-// e^{G_x - G_y} is good to the difference's own digits; it is set, not
-// multiplied, to zero where y lies ahead of x.  g ends at -128, where e^g is 0:
-// differences of the rows behind it stay finite.
+// Decays.  G is summed within a chunk in 64 bits and kept as two floats
+// (k_decays, once for all passes), so e^{G_x - G_y} is good to the difference's
+// own digits; it is set, not multiplied, to zero where y lies ahead of x.
 //
 // Roundings with bf16 rows.  The products of q, k and v themselves are exact.
 // What is not a bf16 number is split into terms of eight bits: P into two (2^-16
@@ -41,10 +40,18 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 
-constexpr int kWaves = kThreads / 64;
 constexpr int kTri = 10;  // tiles of 16 x 16 on or below the diagonal of 64 x 64
 
 __device__ __forceinline__ int tri(int lo, int hi) { return hi * (hi + 1) / 2 + lo; }
+// P in LDS: for an output tile x, the source tiles 2 ys and 2 ys + 1 side by
+// side, as one operand of a product takes them; six such pairs have a tile on
+// the right side of the diagonal.  In two of them the other half is zeros.
+constexpr int kPairs = 6;
+template <bool BACK> __host__ __device__ constexpr bool is_pair(int x, int ys) { return BACK ? 2 * ys + 1 >= x : 2 * ys <= x; }
+template <bool BACK> __host__ __device__ constexpr int pair(int x, int ys) {
+    // forward (0,0) (1,0) (2,0) (2,1) (3,0) (3,1), backward (0,0) (0,1) (1,0) (1,1) (2,1) (3,1)
+    return BACK ? (x < 2 ? 2 * x + ys : x + 2) : (x < 2 ? x : 2 * x - 2 + ys);
+}
 
 __device__ __forceinline__ float exp2_hw(float v) { return __builtin_amdgcn_exp2f(v); }
 
@@ -113,54 +120,91 @@ __device__ __forceinline__ void values(const Frag<float>& t, float (&f)[8]) {
 }
 
 // 64 rows of W values, row-major in pieces of 16 bytes whose place within the
-// row is exclusive-ored by the row: both readings below spread over all banks.
+// row is exclusive-ored by the row: all the readings below spread over all
+// banks, and what the row contributes is the same for rows 16 apart, so that a
+// lane needs few addresses, the rest being constants of the instructions.
 template <typename T, int W> struct Tile {
     static constexpr int kPieces = W * (int)sizeof(T) / 16;           // of a row
-    static constexpr int kMine = kChunk * kPieces / kThreads;        // of a thread
     static constexpr int kElems = 16 / (int)sizeof(T);
-    static constexpr int kBytes = kChunk * W * (int)sizeof(T);
+    static constexpr int kRow = W * (int)sizeof(T);
+    static constexpr int kBytes = kChunk * kRow;
     static __device__ __forceinline__ int place(int row, int piece) {
-        const int x = sizeof(T) == 4 ? (row & 15) : W == 128 ? (row & 7) << 1 : ((row >> 1) & 3) << 1;
-        return row * (W * (int)sizeof(T)) + ((piece ^ x) << 4);
+        // bf16: sixteen rows, a piece each, and eight rows, two pieces each, are both read at once
+        const int r = W == 128 ? row : row >> 1;
+        const int x = sizeof(T) == 4 ? (row & 15) : W == 128 ? (r & 7) << 1 | (r >> 3 & 1) : (r & 3) << 1 | (r >> 2 & 1);
+        return row * kRow + ((piece ^ x) << 4);
     }
-    // positions 4g..4g+3 of the 16s at 32 ks and 32 ks + 16, of row `row`
-    static __device__ __forceinline__ Frag<T> row_frag(const char* t, int row, int ks, int g) {
+    // Positions 4g..4g+3 of the 16s at 32 ks and 32 ks + 16, of row 16 b + i.
+    // `base`: row_base(); what ks adds to a lane's piece is exclusive-ored too.
+    static __device__ __forceinline__ int row_base(int g, int i) {
+        return sizeof(T) == 2 ? place(i, g >> 1) + (g & 1) * 8 : place(i, g);
+    }
+    static __device__ __forceinline__ Frag<T> by_row(const char* t, int base, int b, int ks) {
         Frag<T> f;
         if constexpr (sizeof(T) == 2) {
-            const u32x2 a = *reinterpret_cast<const u32x2*>(t + place(row, 4 * ks + (g >> 1)) + (g & 1) * 8);
-            const u32x2 b = *reinterpret_cast<const u32x2*>(t + place(row, 4 * ks + 2 + (g >> 1)) + (g & 1) * 8);
-            f.v = u32x4{a.x, a.y, b.x, b.y};
+            const char* const p = t + b * 16 * kRow;
+            const u32x2 a = *reinterpret_cast<const u32x2*>(p + (base ^ (4 * ks) << 4));
+            const u32x2 c = *reinterpret_cast<const u32x2*>(p + (base ^ (4 * ks + 2) << 4));
+            f.v = u32x4{a.x, a.y, c.x, c.y};
         } else {
-            const f32x4 a = *reinterpret_cast<const f32x4*>(t + place(row, 8 * ks + g));
-            const f32x4 b = *reinterpret_cast<const f32x4*>(t + place(row, 8 * ks + 4 + g));
+            const char* const p = t + b * 16 * kRow + (ks >> 1) * 256;
+            const f32x4 a = *reinterpret_cast<const f32x4*>(p + (base ^ (8 * (ks & 1)) << 4));
+            const f32x4 c = *reinterpret_cast<const f32x4*>(p + (base ^ (8 * (ks & 1) + 4) << 4));
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 f.v[e] = a[e];
-                f.v[4 + e] = b[e];
+                f.v[4 + e] = c[e];
             }
         }
         return f;
     }
-    // rows 4g..4g+3 of the 16s at 32 ys and 32 ys + 16, of column c0 + i
-    static __device__ __forceinline__ Frag<T> col_frag(const char* t, int ys, int c0, int g, int i) {
+    // Rows 4g..4g+3 of the 16s at 32 ys and 32 ys + 16, of column 16 m + i.
+    // bf16: lanes 4j..4j+3 of a group of 16 name row 4g + j, 16 columns of it;
+    // the transposing load gives each lane a column.
+    static __device__ __forceinline__ int col_base(int g, int i) {
+        return sizeof(T) == 2 ? place(4 * g + (i >> 2), (i & 3) >> 1) + (i & 1) * 8
+                              : 4 * g * kRow + (((i >> 2) ^ (4 * g)) << 4) + (i & 3) * 4;
+    }
+    static __device__ __forceinline__ Frag<T> by_col(const char* t, int base, int ys, int m) {
         Frag<T> f;
         if constexpr (sizeof(T) == 2) {
-            // lanes 4j..4j+3 of a group of 16 name row 4g + j, 16 columns of it; each lane receives a column
             typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-            const int row = 32 * ys + 4 * g + (i >> 2), piece = (c0 >> 3) + ((i & 3) >> 1), in = (i & 1) * 8;
-            const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + place(row, piece) + in));
-            const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(t + place(row + 16, piece) + in));
+            const char* const p = t + ys * 32 * kRow + (base ^ (2 * m) << 4);
+            const s16x4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)p);
+            const s16x4 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 16 * kRow));
             const u32x2 a2 = __builtin_bit_cast(u32x2, a), b2 = __builtin_bit_cast(u32x2, b);
             f.v = u32x4{a2.x, a2.y, b2.x, b2.y};
         } else {
-            const int c = c0 + i;
+            const char* const p = t + ys * 32 * kRow + (m >> 2) * 256;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int row = 32 * ys + 16 * (e >> 2) + 4 * g + (e & 3);
-                f.v[e] = *reinterpret_cast<const float*>(t + place(row, c >> 2) + (c & 3) * 4);
-            }
+            for (int e = 0; e < 8; ++e)
+                f.v[e] = *reinterpret_cast<const float*>(p + ((e >> 2) * 16 + (e & 3)) * kRow + (base ^ (4 * (m & 3) + (e & 3)) << 4));
         }
         return f;
+    }
+    // The same reading from a tile that is read by rows alone (put_by_row): a
+    // lane's eight bf16 positions stand together.
+    static __device__ __forceinline__ int whole_base(int g, int i) {
+        return sizeof(T) == 2 ? i * kRow + ((g ^ (i & (kPieces - 1))) << 4) : row_base(g, i);
+    }
+    static __device__ __forceinline__ Frag<T> whole(const char* t, int base, int b, int ks) {
+        if constexpr (sizeof(T) == 2) {
+            Frag<T> f;
+            f.v = *reinterpret_cast<const u32x4*>(t + b * 16 * kRow + (base ^ (4 * ks) << 4));
+            return f;
+        } else {
+            return by_row(t, base, b, ks);
+        }
+    }
+    static __device__ __forceinline__ void put_by_row(char* t, int row, int piece, u32x4 v) {
+        if constexpr (sizeof(T) == 2) {
+            // columns 8 piece..: quads 2 (piece & 1) and the next of the first or second 16 of 32
+            const int to = row * kRow + (((piece >> 2) * 4 + (piece & 1) * 2) ^ (row & (kPieces - 1))) * 16 + (piece >> 1 & 1) * 8;
+            *reinterpret_cast<u32x2*>(t + to) = u32x2{v.x, v.y};
+            *reinterpret_cast<u32x2*>(t + (to ^ 16)) = u32x2{v.z, v.w};
+        } else {
+            *reinterpret_cast<u32x4*>(t + place(row, piece)) = v;
+        }
     }
     static __device__ __forceinline__ T* at(char* t, int row, int c) {
         return reinterpret_cast<T*>(t + place(row, c / kElems)) + c % kElems;
@@ -173,8 +217,7 @@ template <> __device__ __forceinline__ bool not_finite<float>(float v) {
     return (__float_as_uint(v) & 0x7f800000u) == 0x7f800000u;
 }
 // Some value of the piece is not finite.
-template <typename T> __device__ __forceinline__ bool piece_not_finite(uint4 p) {
-    const uint32_t w[4] = {p.x, p.y, p.z, p.w};
+template <typename T> __device__ __forceinline__ bool piece_not_finite(u32x4 w) {
     uint32_t any = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -184,46 +227,64 @@ template <typename T> __device__ __forceinline__ bool piece_not_finite(uint4 p) 
     return any != 0;
 }
 
+// A buffer descriptor of the first n rows of a chunk (none for n <= 0): a read
+// beyond is 0, a write beyond is dropped, without a branch.  Rows begin within
+// 32 bits of the first (row strides end at 2^24 elements); kNowhere is beyond
+// every descriptor.
+constexpr uint32_t kNowhere = 0xffffff00u;
+template <typename T> __device__ __forceinline__ __amdgpu_buffer_rsrc_t rows_buffer(const void* p, int64_t stride, int64_t row0, int64_t at, int n, int d) {
+    const uint32_t bytes = n > 0 ? ((uint32_t)(n - 1) * (uint32_t)stride + (uint32_t)d) * (uint32_t)sizeof(T) : 0u;
+    return __builtin_amdgcn_make_buffer_rsrc(static_cast<T*>(const_cast<void*>(p)) + row0 * stride + at, 0, bytes, 0x00020000);
+}
+
 // A thread's pieces of 64 rows of a head, on their way to LDS.  Rows from n on
 // and columns from d on are zeros.
-template <typename T, int W> struct Fetch {
+template <typename T, int W, int THREADS, bool VEC> struct Fetch {
     using L = Tile<T, W>;
-    uint4 r[L::kMine];
+    static constexpr int kMine = kChunk * L::kPieces / THREADS, kStep = THREADS / L::kPieces;  // kStep rows between two
+    u32x4 r[kMine];
     __device__ __forceinline__ void load(const Rows& R, int head, int d, int64_t row0, int n, int tid) {
-        const T* base = static_cast<const T*>(R.p) + row0 * R.stride + (int64_t)(head / R.per) * d;
+        const __amdgpu_buffer_rsrc_t rs = rows_buffer<T>(R.p, R.stride, row0, (int64_t)(head / R.per) * d, n, d);
+        const int row = tid / L::kPieces, c = tid % L::kPieces * L::kElems;
+        const bool some = VEC ? c < d : true;
+        uint32_t off = some ? ((uint32_t)row * (uint32_t)R.stride + (uint32_t)c) * (uint32_t)sizeof(T) : kNowhere;
+        const uint32_t step = some ? kStep * (uint32_t)R.stride * (uint32_t)sizeof(T) : 0u;
 #pragma unroll
-        for (int i = 0; i < L::kMine; ++i) {
-            const int idx = tid + i * kThreads, row = idx / L::kPieces, c = idx % L::kPieces * L::kElems;
-            r[i] = make_uint4(0, 0, 0, 0);
-            if (row < n && c < d) {
-                const T* p = base + row * R.stride + c;
-                if (R.vec) {
-                    r[i] = *reinterpret_cast<const uint4*>(p);
-                } else {
-                    uint32_t w[4] = {0, 0, 0, 0};
+        for (int i = 0; i < kMine; ++i) {
+            if constexpr (VEC) {
+                r[i] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0));
+            } else {
+                uint32_t w[4] = {0, 0, 0, 0};
 #pragma unroll
-                    for (int e = 0; e < L::kElems; ++e) {
-                        if (c + e < d) {
-                            if constexpr (sizeof(T) == 2) w[e >> 1] |= (uint32_t)p[e] << (16 * (e & 1));
-                            else w[e] = __float_as_uint(p[e]);
-                        }
-                    }
-                    r[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                for (int e = 0; e < L::kElems; ++e) {
+                    const bool in = c + e < d;
+                    const uint32_t at = in ? off + e * (uint32_t)sizeof(T) : kNowhere;
+                    if constexpr (sizeof(T) == 2) w[e >> 1] |= (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, at, 0, 0) << (16 * (e & 1));
+                    else w[e] = __builtin_amdgcn_raw_buffer_load_b32(rs, at, 0, 0);
                 }
+                r[i] = u32x4{w[0], w[1], w[2], w[3]};
             }
+            off += step;
         }
     }
     __device__ __forceinline__ void put(char* t, int tid) const {
 #pragma unroll
-        for (int i = 0; i < L::kMine; ++i) {
-            const int idx = tid + i * kThreads;
-            *reinterpret_cast<uint4*>(t + L::place(idx / L::kPieces, idx % L::kPieces)) = r[i];
+        for (int i = 0; i < kMine; ++i) {
+            const int idx = tid + i * THREADS;
+            *reinterpret_cast<u32x4*>(t + L::place(idx / L::kPieces, idx % L::kPieces)) = r[i];
+        }
+    }
+    __device__ __forceinline__ void put_by_row(char* t, int tid) const {
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            const int idx = tid + i * THREADS;
+            L::put_by_row(t, idx / L::kPieces, idx % L::kPieces, r[i]);
         }
     }
     __device__ __forceinline__ bool bad() const {
         bool b = false;
 #pragma unroll
-        for (int i = 0; i < L::kMine; ++i) b |= piece_not_finite<T>(r[i]);
+        for (int i = 0; i < kMine; ++i) b |= piece_not_finite<T>(r[i]);
         return b;
     }
 };
@@ -246,44 +307,107 @@ __device__ __forceinline__ int64_t xcd_item(int64_t b, int64_t n) {
 }
 inline int64_t xcd_grid(int64_t n) { return (n + 7) / 8 * 8; }
 
-template <typename T, int DK, int NT, int MODE> struct Layout {
-    static constexpr int DV = 64 * NT;
+// What the decays of a chunk come to, in LDS.
+struct Gates {
+    float hi[64], lo[64];   // G, the inclusive sum of g in powers of two, as two floats
+    float row[64];          // factor of an output row's state part
+    float src[64];          // weight of a source row in the state's update
+    float all, pad[3];      // e^{G_C}
+};
+
+// Four values of an output row, the first at byte `at` of rs; VEC: all four
+// exist, on whole vectors.
+template <typename O, bool VEC> __device__ __forceinline__ void put4(__amdgpu_buffer_rsrc_t rs, uint32_t at, const f32x4& v, int nc) {
+    if constexpr (VEC) {
+        if constexpr (sizeof(O) == 4) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rs, at, 0, 0);
+        else __builtin_amdgcn_raw_buffer_store_b64(u32x2{gdn::f32x2_to_bf16x2(v[0], v[1]), gdn::f32x2_to_bf16x2(v[2], v[3])}, rs, at, 0, 0);
+    } else {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const uint32_t to = r < nc ? at + r * (uint32_t)sizeof(O) : kNowhere;
+            if constexpr (sizeof(O) == 4) __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v[r]), rs, to, 0, 0);
+            else __builtin_amdgcn_raw_buffer_store_b16(gdn::f32_to_bf16(v[r]), rs, to, 0, 0);
+        }
+    }
+}
+template <typename O> __device__ __forceinline__ void put_nan(__amdgpu_buffer_rsrc_t rs, uint32_t at) {
+    if constexpr (sizeof(O) == 4) __builtin_amdgcn_raw_buffer_store_b32(0x7fc00000u, rs, at, 0, 0);
+    else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)0x7fc0u, rs, at, 0, 0);
+}
+// A wave's share of a chunk's output: 64 rows by 16 NT columns.
+template <typename O, bool VEC, int NT>
+__device__ __forceinline__ void put_rows(const AttendArgs& A, const f32x4 (&o)[4 * NT], int64_t row0, int head, int n, int col0, int g, int i) {
+    const __amdgpu_buffer_rsrc_t rs = rows_buffer<O>(A.o, A.o_stride, row0, (int64_t)head * A.dv, n, A.dv);
+    const uint32_t row = (uint32_t)A.o_stride * (uint32_t)sizeof(O);
+#pragma unroll
+    for (int nn = 0; nn < NT; ++nn) {
+        const int c4 = col0 + 16 * nn + 4 * g;
+        const uint32_t at = (uint32_t)i * row + (uint32_t)c4 * (uint32_t)sizeof(O);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) put4<O, VEC>(rs, c4 < A.dv ? at + 16 * b * row : kNowhere, o[b * NT + nn], A.dv - c4);
+    }
+}
+
+template <typename T, int DK, int W, int NT, int MODE> struct Layout {
+    static constexpr int DV = 16 * W * NT;
     static constexpr int kTermsP = sizeof(T) == 2 ? 2 : 1;
     static constexpr int kTermsV = sizeof(T) == 2 ? 3 : 1;
     static constexpr int kTermsS = sizeof(T) == 4 ? 1 : MODE == kAttend ? 2 : 3;
-    static constexpr int kPTile = 64 * 4 * (int)sizeof(T);
+    static constexpr int kPPair = 64 * 8 * (int)sizeof(T);  // of one term
     static constexpr bool kX = MODE == kDot || MODE == kDotRows;
     static constexpr int oK = 0;
     static constexpr int oV = oK + Tile<T, DK>::kBytes;
     static constexpr int oQ = oV + Tile<T, DV>::kBytes;
     static constexpr int oX = oQ + (MODE == kLocal ? 0 : Tile<T, DK>::kBytes);
     static constexpr int oP = oX + (kX ? Tile<T, DV>::kBytes : 0);
-    static constexpr int oG = oP + (MODE == kLocal ? 0 : kTri * kTermsP * kPTile);  // G (two floats), row factors, weights, e^{G_C}
-    static constexpr int oBad = oG + 4 * 64 * 4 + 16;                               // first row of a column that is not finite
-    static constexpr int oDot = oBad + DV * 4;
-    static constexpr int oSum = oDot + (kX ? kWaves * 64 * 4 : 0);
+    static constexpr int oG = oP + (MODE == kLocal ? 0 : kPairs * kTermsP * kPPair);
+    static constexpr int oBad = oG + (int)sizeof(Gates);       // first row of a column that is not finite
+    static constexpr int oDot = oBad + DV * 8 + 16;
+    static constexpr int oSum = oDot + (kX ? W * 64 * 4 : 0);
     static constexpr int kBytes = oSum + (MODE == kDotRows ? kTri * 32 * 4 : 0);
+    // Waves on a SIMD that the registers are cut for: what LDS has room for, four at most.
+    static constexpr int kRoom = 160 * 1024 / kBytes * W / 4;
+    static constexpr int kWavesPerSimd = kRoom < 1 ? 1 : kRoom > 4 ? 4 : kRoom;
 };
 
-template <typename T, int DK, int NT, int MODE>
-__global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void k_attend(const AttendArgs A) {
-    using Y = Layout<T, DK, NT, MODE>;
+// The state's rows 16 m + 4 g + r of one column, `at` from each other by rs;
+// those that do not exist are zeros.
+template <typename S, int M> __device__ __forceinline__ void load_state(f32x4 (&s)[M], const S* p, int rs, int dk, int g) {
+    S raw[M][4];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) raw[m][r] = p[(int64_t)min(16 * m + 4 * g + r, dk - 1) * rs];
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) s[m][r] = 16 * m + 4 * g + r < dk ? gdn::to_f32(raw[m][r]) : 0.0f;
+}
+template <typename S, int M> __device__ __forceinline__ void store_state(const f32x4 (&s)[M], S* p, int rs, int dk, int g, bool zero) {
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            if (16 * m + 4 * g + r < dk) p[(int64_t)(16 * m + 4 * g + r) * rs] = gdn::from_f32<S>(zero ? 0.0f : s[m][r]);
+}
+
+// W waves, 16 NT columns each.
+template <typename T, int DK, int W, int NT, int MODE, bool back, bool VEC>
+__global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE>::kWavesPerSimd)) void k_attend(const AttendArgs A) {
+    using Y = Layout<T, DK, W, NT, MODE>;
     using TK = Tile<T, DK>;
     using TV = Tile<T, Y::DV>;
-    constexpr int M = DK / 16, KS = DK / 32;
+    constexpr int M = DK / 16, KS = DK / 32, TH = 64 * W;
     __shared__ __attribute__((aligned(16))) char lds[Y::kBytes];
     char* const tk = lds + Y::oK;
     char* const tv = lds + Y::oV;
     char* const tq = lds + Y::oQ;
     char* const tx = lds + Y::oX;
     char* const tp = lds + Y::oP;
-    float* const g_hi = reinterpret_cast<float*>(lds + Y::oG);
-    float* const g_lo = g_hi + 64;
-    float* const g_row = g_hi + 128;   // factor of an output row's state part
-    float* const g_src = g_hi + 192;   // weight of a source row in the update
-    float* const g_all = g_hi + 256;   // e^{G_C}; then: some value of v is not finite
-    int* const s_bad = reinterpret_cast<int*>(g_hi + 257);
+    Gates& G = *reinterpret_cast<Gates*>(lds + Y::oG);
     int* const bad_row = reinterpret_cast<int*>(lds + Y::oBad);
+    float* const poison = reinterpret_cast<float*>(bad_row + Y::DV);  // of a column's state, 0 or NaN
+    int* const s_bad = bad_row + 2 * Y::DV;                       // some value of v is not finite
     float* const s_dot = reinterpret_cast<float*>(lds + Y::oDot);
     float* const s_sum = reinterpret_cast<float*>(lds + Y::oSum);
 
@@ -293,138 +417,134 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void k_attend(con
     const int head = (int)(item - slot * A.heads);
     const Segment seg = segment_of(A.segs, slot);
     if (seg.rows <= 0) return;
-    if (MODE == kLocal && (A.back ? seg.first : seg.last)) return;  // nothing follows
+    if (MODE == kLocal && (back ? seg.first : seg.last)) return;  // nothing follows
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int g = lane >> 4, i = lane & 15;
+    const int lane0 = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int col0 = wave * 16 * NT;
-    const bool back = A.back != 0;
-
-    f32x4 S[M][NT];
-    {
-        const bool zero = MODE == kLocal || A.in.at == kNoState ||
-                          (A.in.at == kByPage && A.has_init && A.has_init[seg.seq] == 0);
-        const int64_t base = zero ? 0 : state_base(A.in, seg, slot, head);
-#pragma unroll
-        for (int m = 0; m < M; ++m)
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * m + 4 * g + r, col = col0 + 16 * n + i;
-                    float v = 0.0f;
-                    if (!zero && row < A.dk && col < A.dv) {
-                        const int64_t at = base + (int64_t)row * A.in.rs + (int64_t)col * A.in.cs;
-                        v = A.in.bf16 ? gdn::to_f32(static_cast<const bf16_t*>(A.in.p)[at])
-                                      : static_cast<const float*>(A.in.p)[at];
-                    }
-                    S[m][n][r] = v;
-                }
-    }
-
     const int n_chunks = (seg.rows + kChunk - 1) / kChunk;
-    Fetch<T, DK> fq, fk;
-    Fetch<T, Y::DV> fv, fx;
-    float fg = 0.0f;
-    auto fetch = [&](int c) {
+
+    Fetch<T, DK, TH, VEC> fq, fk;
+    Fetch<T, Y::DV, TH, VEC> fv, fx;
+    float4 fg = make_float4(0, 0, 0, 0);
+    auto fetch = [&](int c, int tid, int lane) {  // nothing where the segment has no chunk c
         const int64_t row0 = (int64_t)seg.row + (int64_t)c * kChunk;
-        const int n = min(kChunk, seg.rows - c * kChunk);
+        const int n = c < 0 ? 0 : min(kChunk, seg.rows - c * kChunk);
         fk.load(A.k, head, A.dk, row0, n, tid);
         fv.load(A.v, head, A.dv, row0, n, tid);
         if constexpr (MODE != kLocal) fq.load(A.q, head, A.dk, row0, n, tid);
         if constexpr (Y::kX) fx.load(A.x, head, A.dv, row0, n, tid);
-        fg = lane < n ? A.g[(row0 + lane) * A.g_stride + head] : 0.0f;
+        if (wave == 0 && n > 0) fg = A.gates[(int64_t)head * A.n_rows + row0 + min(lane, n - 1)];
     };
-    if (tid == 0) *s_bad = 0;
-    for (int c = tid; c < Y::DV; c += kThreads) bad_row[c] = kChunk;
-    fetch(back ? n_chunks - 1 : 0);
-    double total = 0.0;
+    if constexpr (MODE != kLocal)  // zeros, of which those that no tile overwrites stay
+        for (int c = threadIdx.x; c < kPairs * Y::kTermsP * Y::kPPair / 16; c += TH)
+            *reinterpret_cast<u32x4*>(tp + c * 16) = u32x4{0, 0, 0, 0};
+    if (threadIdx.x == 0) *s_bad = 0;
+    for (int c = threadIdx.x; c < Y::DV; c += TH) poison[c] = 0.0f;
+    fetch(back ? n_chunks - 1 : 0, threadIdx.x, lane0);
+    f32x4 S[NT][M];
+    {
+        const int g = lane0 >> 4, i = lane0 & 15;
+        const bool zero = MODE == kLocal || A.in.at == kNoState ||
+                          (A.in.at == kByPage && A.has_init && A.has_init[seg.seq] == 0);
+        const int64_t base = zero ? 0 : state_base(A.in, seg, slot, head);
+#pragma unroll
+        for (int nn = 0; nn < NT; ++nn) {
+            const int col = col0 + 16 * nn + i;
+#pragma unroll
+            for (int m = 0; m < M; ++m) S[nn][m] = f32x4{0, 0, 0, 0};
+            if (!zero && col < A.dv) {
+                const int64_t at = base + (int64_t)col * A.in.cs;
+                if (A.in.bf16) load_state(S[nn], static_cast<const bf16_t*>(A.in.p) + at, A.in.rs, A.dk, g);
+                else load_state(S[nn], static_cast<const float*>(A.in.p) + at, A.in.rs, A.dk, g);
+            }
+        }
+    }
     lds_barrier();
 
     for (int step = 0; step < n_chunks; ++step) {
         const int c = back ? n_chunks - 1 - step : step;
         const int64_t row0 = (int64_t)seg.row + (int64_t)c * kChunk;
         const int n = min(kChunk, seg.rows - c * kChunk);
+        // what follows from a lane's number is worked out again for each chunk: kept, it would fill the registers
+        int lane = lane0;
+        asm volatile("" : "+v"(lane));
+        const int tid = wave * 64 + lane, g = lane >> 4, i = lane & 15;
         fk.put(tk, tid);
         fv.put(tv, tid);
-        if constexpr (MODE != kLocal) fq.put(tq, tid);
+        if constexpr (MODE != kLocal) fq.put_by_row(tq, tid);
         if constexpr (Y::kX) fx.put(tx, tid);
-        if (fv.bad()) *s_bad = 1;
-        if (wave == 0) {
-            const float gv = fg < -128.0f ? -128.0f : fg;  // a NaN stays
-            double G = (double)gv * 1.4426950408889634;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const double up = __shfl_up(G, d, 64);
-                if (lane >= d) G += up;
-            }
-            const double GC = __shfl(G, 63, 64);
-            total += GC;
-            const float hi = (float)G, lo = (float)(G - (double)hi);
-            const float into = (float)G, rest = (float)(GC - G);
-            const float e_into = exp2_hw(into) * (1.0f + 0.6931472f * (float)(G - (double)into));
-            const float e_rest = exp2_hw(rest) * (1.0f + 0.6931472f * (float)((GC - G) - (double)rest));
-            g_hi[lane] = hi;
-            g_lo[lane] = lo;
-            g_row[lane] = A.f_i * (back ? e_rest : e_into);
-            g_src[lane] = A.f_u * (back ? e_into : e_rest);
-            if (lane == 63) *g_all = e_into;
+        if (MODE != kLocal && !back && fv.bad()) *s_bad = 1;
+        if (wave == 0) {  // rows behind the end count as the last one, whose weight is 1 and whose values are zeros
+            G.hi[lane] = fg.x;
+            G.lo[lane] = fg.y;
+            G.row[lane] = A.f_i * (back ? fg.w : fg.z);
+            G.src[lane] = A.f_u * (back ? fg.z : fg.w);
+            if (lane == 63) G.all = fg.z;
         }
         lds_barrier();
-        const bool bad = !back && *s_bad != 0;  // rare
+        // Where v is not finite (rare) zeros take its place, 0 times it being NaN:
+        // outputs from its row on are overwritten, and the state's column is told.
+        const bool bad = MODE != kLocal && !back && *s_bad != 0;
         if (bad) {
-            for (int c2 = tid; c2 < Y::DV; c2 += kThreads) {
+            for (int c2 = tid; c2 < Y::DV; c2 += TH) {
                 int first = kChunk;
-                for (int r = 0; r < kChunk; ++r) {
-                    T* p = TV::at(tv, r, c2);
+                for (int r = kChunk - 1; r >= 0; --r) {
+                    T* const p = TV::at(tv, r, c2);
                     if (not_finite<T>(*p)) {
                         *p = 0;
-                        first = min(first, r);
+                        first = r;
                     }
                 }
                 bad_row[c2] = first;
+                poison[c2] = first < kChunk ? __uint_as_float(0x7fc00000u) : 0.0f;
             }
             lds_barrier();
         }
-        if (step + 1 < n_chunks) fetch(back ? c - 1 : c + 1);
 
         f32x4 O[4 * NT];
         if constexpr (MODE != kLocal) {
-            // P: tile (y, x) of k q^T, decayed, as two terms
-            for (int t = wave; t < kTri; t += kWaves) {
+            const int kr = TK::row_base(g, i), qr = TK::whole_base(g, i), xr = TV::row_base(g, i);
+            // P: tile (y, x) of k q^T, decayed, in terms; the products of a wave's first tile are under way while
+            // it multiplies q and S
+            struct Of { int ty, tx; };
+            auto tile_of = [](int t) {
                 const int hi = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, lo = t - hi * (hi + 1) / 2;
-                const int ty = back ? hi : lo, tx_ = back ? lo : hi;
-                if (16 * hi >= n) continue;
-                f32x4 p[1] = {f32x4{0, 0, 0, 0}};
+                return back ? Of{hi, lo} : Of{lo, hi};
+            };
+            auto products = [&](int t, f32x4 (&p)[2], f32x4 (&pm)[2]) {
+                const Of o = tile_of(t);
+                p[0] = p[1] = pm[0] = pm[1] = f32x4{0, 0, 0, 0};
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-                    p[0] = mma(TK::row_frag(tk, 16 * ty + i, ks, g), TK::row_frag(tq, 16 * tx_ + i, ks, g), p[0]);
-                f32x4 pm[1] = {f32x4{0, 0, 0, 0}};
+                for (int ks = 0; ks < KS; ++ks) p[ks & 1] = mma(TK::by_row(tk, kr, o.ty, ks), TK::whole(tq, qr, o.tx, ks), p[ks & 1]);
                 if constexpr (MODE == kDotRows) {
 #pragma unroll
                     for (int ks = 0; ks < Y::DV / 32; ++ks)
-                        pm[0] = mma(TV::row_frag(tv, 16 * ty + i, ks, g), TV::row_frag(tx, 16 * tx_ + i, ks, g), pm[0]);
-                    settle(pm);
+                        pm[ks & 1] = mma(TV::by_row(tv, xr, o.ty, ks), TV::by_row(tx, xr, o.tx, ks), pm[ks & 1]);
                 }
+            };
+            auto decayed = [&](int t, f32x4 (&p)[2], f32x4 (&pm)[2]) {
+                const Of o = tile_of(t);
                 settle(p);
-                const int x = 16 * tx_ + i, y0 = 16 * ty + 4 * g;
-                const float xh = g_hi[x], xl = g_lo[x];
-                const f32x4 yh = *reinterpret_cast<const f32x4*>(g_hi + y0);
-                const f32x4 yl = *reinterpret_cast<const f32x4*>(g_lo + y0);
+                if constexpr (MODE == kDotRows) settle(pm);
+                const int x = 16 * o.tx + i, y0 = 16 * o.ty + 4 * g;
+                const float xh = G.hi[x], xl = G.lo[x];
+                const f32x4 yh = *reinterpret_cast<const f32x4*>(G.hi + y0);
+                const f32x4 yl = *reinterpret_cast<const f32x4*>(G.lo + y0);
                 float v[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float d = back ? (yh[r] - xh) + (yl[r] - xl) : (xh - yh[r]) + (xl - yl[r]);
                     const bool in = back ? y0 + r >= x : y0 + r <= x;
-                    v[r] = in ? A.f_p * exp2_hw(d) * p[0][r] : 0.0f;
+                    v[r] = in ? A.f_p * exp2_hw(d) * (p[0][r] + p[1][r]) : 0.0f;
                 }
-                char* const at = tp + t * (Y::kTermsP * Y::kPTile) + lane * (4 * (int)sizeof(T));
+                char* const at = tp + pair<back>(o.tx, o.ty >> 1) * (Y::kTermsP * Y::kPPair) + lane * (8 * (int)sizeof(T)) +
+                                 (o.ty & 1) * (4 * (int)sizeof(T));
                 if constexpr (sizeof(T) == 2) {
                     uint32_t a[2], b[2];
                     split2<2>(v[0], v[1], a);
                     split2<2>(v[2], v[3], b);
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) *reinterpret_cast<u32x2*>(at + j * Y::kPTile) = u32x2{a[j], b[j]};
+                    for (int j = 0; j < 2; ++j) *reinterpret_cast<u32x2*>(at + j * Y::kPPair) = u32x2{a[j], b[j]};
                 } else {
                     *reinterpret_cast<f32x4*>(at) = f32x4{v[0], v[1], v[2], v[3]};
                 }
@@ -433,230 +553,206 @@ __global__ __launch_bounds__(kThreads, sizeof(T) == 2 ? 2 : 1) void k_attend(con
                     float row = 0.0f;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float m = y0 + r == x ? 0.0f : v[r] * pm[0][r];
+                        const float m = y0 + r == x ? 0.0f : v[r] * (pm[0][r] + pm[1][r]);
                         row += m;
-                        const float col = reduce16(m);
-                        if (i == 0) s_sum[t * 32 + 16 + 4 * g + r] = col;
+                        const float cs = reduce16(m);
+                        if (i == 0) s_sum[t * 32 + 16 + 4 * g + r] = cs;
                     }
                     row += __shfl_xor(row, 16, 64);
                     row += __shfl_xor(row, 32, 64);
                     if (g == 0) s_sum[t * 32 + i] = row;
                 }
-            }
-            // the state's part
+            };
+            f32x4 p[2], pm[2];
+            products(wave, p, pm);
+            // the state's part, transposed: a lane holds four columns of row 16 b + i
 #pragma unroll
             for (int j = 0; j < 4 * NT; ++j) O[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                Frag<T> sf[NT][Y::kTermsS];
+                Frag<T> sf[NT][Y::kTermsS], qf[4];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) qf[b] = TK::whole(tq, qr, b, ks);
 #pragma unroll
                 for (int nn = 0; nn < NT; ++nn) {
                     float f[8];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        f[r] = S[2 * ks][nn][r];
-                        f[4 + r] = S[2 * ks + 1][nn][r];
+                        f[r] = S[nn][2 * ks][r];
+                        f[4 + r] = S[nn][2 * ks + 1][r];
                     }
                     split<Y::kTermsS>(f, sf[nn]);
                 }
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const Frag<T> qf = TK::row_frag(tq, 16 * b + i, ks, g);
+                for (int ts = 0; ts < Y::kTermsS; ++ts)
 #pragma unroll
-                    for (int nn = 0; nn < NT; ++nn)
+                    for (int b = 0; b < 4; ++b)
 #pragma unroll
-                        for (int ts = 0; ts < Y::kTermsS; ++ts) O[b * NT + nn] = mma(qf, sf[nn][ts], O[b * NT + nn]);
-                }
+                        for (int nn = 0; nn < NT; ++nn) O[b * NT + nn] = mma(sf[nn][ts], qf[b], O[b * NT + nn]);
+            }
+            decayed(wave, p, pm);
+            for (int t = wave + W; t < kTri; t += W) {
+                products(t, p, pm);
+                decayed(t, p, pm);
             }
             settle(O);
 #pragma unroll
             for (int b = 0; b < 4; ++b) {
-                const f32x4 f = *reinterpret_cast<const f32x4*>(g_row + 16 * b + 4 * g);
+                const float f = G.row[16 * b + i];
 #pragma unroll
                 for (int nn = 0; nn < NT; ++nn) O[b * NT + nn] *= f;
                 if constexpr (Y::kX) {
+                    float d = 0.0f;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        float d = 0.0f;
+                    for (int nn = 0; nn < NT; ++nn) {
+                        const T* const p = TV::at(tx, 16 * b + i, col0 + 16 * nn + 4 * g);
 #pragma unroll
-                        for (int nn = 0; nn < NT; ++nn)
-                            d = fmaf(O[b * NT + nn][r], gdn::to_f32(*TV::at(tx, 16 * b + 4 * g + r, col0 + 16 * nn + i)), d);
-                        d = reduce16(d);
-                        if (i == 0) s_dot[wave * 64 + 16 * b + 4 * g + r] = d;
+                        for (int r = 0; r < 4; ++r) d = fmaf(O[b * NT + nn][r], gdn::to_f32(p[r]), d);
                     }
+                    d += __shfl_xor(d, 16, 64);
+                    d += __shfl_xor(d, 32, 64);
+                    if (g == 0) s_dot[wave * 64 + 16 * b + i] = d;
                 }
             }
             lds_barrier();  // P is whole
             if constexpr (Y::kX) {
                 if (tid < n) {
-                    float d = (s_dot[tid] + s_dot[64 + tid]) + (s_dot[128 + tid] + s_dot[192 + tid]);
+                    float d = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < W; ++w) d += s_dot[w * 64 + tid];
                     if constexpr (MODE == kDotRows) {
                         const int b = tid >> 4, k = tid & 15;
-                        float row = 0.0f, col = 0.0f;
+                        float row = 0.0f, cs = 0.0f;
                         for (int o = 0; o < 4; ++o) {  // the other tile's index
-                            if (16 * max(o, b) >= n) break;
                             if (back ? o >= b : o <= b) row += s_sum[tri(min(o, b), max(o, b)) * 32 + k];
-                            if (back ? o <= b : o >= b) col += s_sum[tri(min(o, b), max(o, b)) * 32 + 16 + k];
+                            if (back ? o <= b : o >= b) cs += s_sum[tri(min(o, b), max(o, b)) * 32 + 16 + k];
                         }
-                        d += row - col;
+                        d += row - cs;
                     }
                     A.dot[(int64_t)head * A.n_rows + row0 + tid] = d;
                 }
             }
         }
-
-        // P v, and the state's update from the same v
-        const float all = *g_all;
+        const int vc = TV::col_base(g, i);
+        if constexpr (MODE != kLocal) {  // P v, and the chunk's output is whole
 #pragma unroll
-        for (int m = 0; m < M; ++m)
+            for (int ys = 0; ys < 2; ++ys) {
+                Frag<T> vf[NT];
 #pragma unroll
-            for (int nn = 0; nn < NT; ++nn) S[m][nn] *= all;
+                for (int nn = 0; nn < NT; ++nn) vf[nn] = TV::by_col(tv, vc, ys, wave * NT + nn);
+#pragma unroll
+                for (int j = 0; j < Y::kTermsP; ++j)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                        if (!is_pair<back>(b, ys)) continue;
+                        const char* const p = tp + (pair<back>(b, ys) * Y::kTermsP + j) * Y::kPPair + lane * (8 * (int)sizeof(T));
+                        Frag<T> pf;
+                        if constexpr (sizeof(T) == 2) {
+                            pf.v = *reinterpret_cast<const u32x4*>(p);
+                        } else {
+                            const f32x4 a = *reinterpret_cast<const f32x4*>(p), c2 = *reinterpret_cast<const f32x4*>(p + 16);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                pf.v[e] = a[e];
+                                pf.v[4 + e] = c2[e];
+                            }
+                        }
+#pragma unroll
+                        for (int nn = 0; nn < NT; ++nn) O[b * NT + nn] = mma(vf[nn], pf, O[b * NT + nn]);
+                    }
+            }
+            settle(O);
+            if (sizeof(T) == 4 || A.o_f32) put_rows<float, VEC, NT>(A, O, row0, head, n, col0, g, i);
+            else put_rows<T, VEC, NT>(A, O, row0, head, n, col0, g, i);
+            if (bad) {
+                const __amdgpu_buffer_rsrc_t rs = rows_buffer<T>(A.o, A.o_stride, row0, (int64_t)head * A.dv, n, A.dv);
+                for (int nn = 0; nn < NT; ++nn)
+                    for (int r = 0; r < 4; ++r) {
+                        const int c2 = col0 + 16 * nn + 4 * g + r;  // the same lanes wrote these places before
+                        for (int x = i; x < kChunk; x += 16) {
+                            const uint32_t at = ((uint32_t)x * (uint32_t)A.o_stride + (uint32_t)c2) * (uint32_t)sizeof(T);
+                            put_nan<T>(rs, c2 < A.dv && x >= bad_row[c2] ? at : kNowhere);
+                        }
+                    }
+            }
+        }
+        // The next chunk's rows are asked for where the registers that held the output are free.
+        fetch(back ? c - 1 : c + 1, tid, lane);
+        const float all = G.all;
+        const int kc = TK::col_base(g, i);
+#pragma unroll
+        for (int nn = 0; nn < NT; ++nn)
+#pragma unroll
+            for (int m = 0; m < M; ++m) S[nn][m] *= all;
 #pragma unroll
         for (int ys = 0; ys < 2; ++ys) {
-            if (32 * ys >= n) break;
-            Frag<T> vf[NT], vw[NT][Y::kTermsV];
-            const f32x4 w0 = *reinterpret_cast<const f32x4*>(g_src + 32 * ys + 4 * g);
-            const f32x4 w1 = *reinterpret_cast<const f32x4*>(g_src + 32 * ys + 16 + 4 * g);
+            Frag<T> vw[NT][Y::kTermsV];
+            const f32x4 w0 = *reinterpret_cast<const f32x4*>(G.src + 32 * ys + 4 * g);
+            const f32x4 w1 = *reinterpret_cast<const f32x4*>(G.src + 32 * ys + 16 + 4 * g);
 #pragma unroll
             for (int nn = 0; nn < NT; ++nn) {
-                vf[nn] = TV::col_frag(tv, ys, col0 + 16 * nn, g, i);
                 float f[8];
-                values(vf[nn], f);
+                values(TV::by_col(tv, vc, ys, wave * NT + nn), f);
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     f[r] *= w0[r];
                     f[4 + r] *= w1[r];
                 }
+                if constexpr (MODE != kLocal && !back) f[0] += poison[col0 + 16 * nn + i];
                 split<Y::kTermsV>(f, vw[nn]);
             }
-            if constexpr (MODE != kLocal) {
 #pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    const bool lower = back ? 2 * ys >= b : 2 * ys <= b, upper = back ? 2 * ys + 1 >= b : 2 * ys + 1 <= b;
-                    const bool is_lower = lower && 16 * max(2 * ys, b) < n, is_upper = upper && 16 * max(2 * ys + 1, b) < n;
-                    if (!is_lower && !is_upper) continue;
-                    const int t0 = tri(min(2 * ys, b), max(2 * ys, b)), t1 = tri(min(2 * ys + 1, b), max(2 * ys + 1, b));
+            for (int m = 0; m < M; m += 4) {  // four sums in turn: none waits for itself
+                Frag<T> kf[4];
 #pragma unroll
-                    for (int j = 0; j < Y::kTermsP; ++j) {
-                        Frag<T> pf;
-                        const char* const p0 = tp + (t0 * Y::kTermsP + j) * Y::kPTile + lane * (4 * (int)sizeof(T));
-                        const char* const p1 = tp + (t1 * Y::kTermsP + j) * Y::kPTile + lane * (4 * (int)sizeof(T));
-                        if constexpr (sizeof(T) == 2) {
-                            const u32x2 a = is_lower ? *reinterpret_cast<const u32x2*>(p0) : u32x2{0, 0};
-                            const u32x2 bb = is_upper ? *reinterpret_cast<const u32x2*>(p1) : u32x2{0, 0};
-                            pf.v = u32x4{a.x, a.y, bb.x, bb.y};
-                        } else {
-                            const f32x4 z = {0, 0, 0, 0};
-                            const f32x4 a = is_lower ? *reinterpret_cast<const f32x4*>(p0) : z;
-                            const f32x4 bb = is_upper ? *reinterpret_cast<const f32x4*>(p1) : z;
+                for (int j = 0; j < 4; ++j) kf[j] = TK::by_col(tk, kc, ys, m + j);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                pf.v[e] = a[e];
-                                pf.v[4 + e] = bb[e];
-                            }
-                        }
+                for (int tt = 0; tt < Y::kTermsV; ++tt)
 #pragma unroll
-                        for (int nn = 0; nn < NT; ++nn) O[b * NT + nn] = mma(pf, vf[nn], O[b * NT + nn]);
-                    }
-                }
-            }
+                    for (int j = 0; j < 4; ++j)
 #pragma unroll
-            for (int m = 0; m < M; ++m) {
-                const Frag<T> kf = TK::col_frag(tk, ys, 16 * m, g, i);
-#pragma unroll
-                for (int nn = 0; nn < NT; ++nn)
-#pragma unroll
-                    for (int tt = 0; tt < Y::kTermsV; ++tt) S[m][nn] = mma(kf, vw[nn][tt], S[m][nn]);
+                        for (int nn = 0; nn < NT; ++nn) S[nn][m + j] = mma(kf[j], vw[nn][tt], S[nn][m + j]);
             }
         }
-        if constexpr (MODE != kLocal) {
-            settle(O);
-            if (bad) {
-#pragma unroll
-                for (int b = 0; b < 4; ++b)
-#pragma unroll
-                    for (int nn = 0; nn < NT; ++nn) {
-                        const int first = bad_row[col0 + 16 * nn + i];
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            const int x = 16 * b + 4 * g + r;
-                            if (x >= first) O[b * NT + nn][r] = __uint_as_float(0x7fc00000u);
-                        }
-                    }
-            }
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-#pragma unroll
-                for (int nn = 0; nn < NT; ++nn) {
-                    const int col = col0 + 16 * nn + i;
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int x = 16 * b + 4 * g + r;
-                        if (x < n && col < A.dv) {
-                            const int64_t at = (row0 + x) * A.o_stride + (int64_t)head * A.dv + col;
-                            if (A.o_f32) static_cast<float*>(A.o)[at] = O[b * NT + nn][r];
-                            else static_cast<T*>(A.o)[at] = gdn::from_f32<T>(O[b * NT + nn][r]);
-                        }
-                    }
-                }
-        }
-        if (bad) {  // the column is not a number from here on
-#pragma unroll
-            for (int nn = 0; nn < NT; ++nn)
-                if (bad_row[col0 + 16 * nn + i] != kChunk) {
-#pragma unroll
-                    for (int m = 0; m < M; ++m)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) S[m][nn][r] = __uint_as_float(0x7fc00000u);
-                }
+        if (bad) {
             lds_barrier();
             if (tid == 0) *s_bad = 0;
-            for (int c2 = tid; c2 < Y::DV; c2 += kThreads) bad_row[c2] = kChunk;
+            for (int c2 = tid; c2 < Y::DV; c2 += TH) poison[c2] = 0.0f;
         }
         lds_barrier();  // the tiles are free
     }
 
-    const bool write = A.out.at != kNoState && (MODE == kLocal || (back ? seg.first : seg.last));
-    if (write) {
-#pragma unroll
-        for (int m = 0; m < M; ++m) settle(S[m]);
+    if (A.out.at != kNoState && (MODE == kLocal || (back ? seg.first : seg.last))) {
         const bool zero = A.zero_uninit && A.has_init && A.has_init[seg.seq] == 0;
         const int64_t base = state_base(A.out, seg, slot, head);
+        const int g = lane0 >> 4, i = lane0 & 15;
 #pragma unroll
-        for (int m = 0; m < M; ++m)
-#pragma unroll
-            for (int nn = 0; nn < NT; ++nn)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 16 * m + 4 * g + r, col = col0 + 16 * nn + i;
-                    if (row < A.dk && col < A.dv) {
-                        const int64_t at = base + (int64_t)row * A.out.rs + (int64_t)col * A.out.cs;
-                        const float v = zero ? 0.0f : S[m][nn][r];
-                        if (A.out.bf16) static_cast<bf16_t*>(A.out.p)[at] = gdn::f32_to_bf16(v);
-                        else static_cast<float*>(A.out.p)[at] = v;
-                    }
-                }
+        for (int nn = 0; nn < NT; ++nn) {
+            const int col = col0 + 16 * nn + i;
+            settle(S[nn]);
+            if (col < A.dv) {
+                const int64_t at = base + (int64_t)col * A.out.cs;
+                if (A.out.bf16) store_state(S[nn], static_cast<bf16_t*>(A.out.p) + at, A.out.rs, A.dk, g, zero);
+                else store_state(S[nn], static_cast<float*>(A.out.p) + at, A.out.rs, A.dk, g, zero);
+            }
+        }
     }
-    if (MODE == kLocal && tid == 0) A.total[slot * A.heads + head] = total;
 }
 
-template <typename T, int DK, int NT, int MODE> hipError_t run_attend(const AttendArgs& a, hipStream_t s) {
-    static_assert(Layout<T, DK, NT, MODE>::kBytes <= 160 * 1024, "LDS");
+template <typename T, int DK, int W, int NT, int MODE, bool BACK, bool VEC> hipError_t run_attend(const AttendArgs& a, hipStream_t s) {
+    static_assert(Layout<T, DK, W, NT, MODE>::kBytes <= 160 * 1024, "LDS");
     const int64_t grid = xcd_grid(a.n_slots * a.heads);
-    hipLaunchKernelGGL((k_attend<T, DK, NT, MODE>), dim3((unsigned)grid), dim3(kThreads), 0, s, a);
+    hipLaunchKernelGGL((k_attend<T, DK, W, NT, MODE, BACK, VEC>), dim3((unsigned)grid), dim3(64 * W), 0, s, a);
     return hipGetLastError();
 }
-template <typename T, int MODE> hipError_t pick_attend(const AttendArgs& a, hipStream_t s) {
-    if (a.dk <= 64) return a.dv <= 64 ? run_attend<T, 64, 1, MODE>(a, s) : run_attend<T, 64, 2, MODE>(a, s);
-    return a.dv <= 64 ? run_attend<T, 128, 1, MODE>(a, s) : run_attend<T, 128, 2, MODE>(a, s);
+template <typename T, int MODE, bool BACK, bool VEC> hipError_t pick_attend(const AttendArgs& a, hipStream_t s) {
+    constexpr int W = 8, NT = 1;  // for 128 columns
+    if (a.dk <= 64)
+        return a.dv <= 64 ? run_attend<T, 64, 4, 1, MODE, BACK, VEC>(a, s) : run_attend<T, 64, W, NT, MODE, BACK, VEC>(a, s);
+    return a.dv <= 64 ? run_attend<T, 128, 4, 1, MODE, BACK, VEC>(a, s) : run_attend<T, 128, W, NT, MODE, BACK, VEC>(a, s);
 }
-template <typename T> hipError_t launch_attend(const AttendArgs& a, int mode, hipStream_t s) {
-    switch (mode) {
-        case kAttend: return pick_attend<T, kAttend>(a, s);
-        case kDot: return pick_attend<T, kDot>(a, s);
-        case kDotRows: return pick_attend<T, kDotRows>(a, s);
-        default: return pick_attend<T, kLocal>(a, s);
-    }
+template <typename T, int MODE, bool BACK> hipError_t launch_attend(const AttendArgs& a, hipStream_t s) {
+    return a.vec ? pick_attend<T, MODE, BACK, true>(a, s) : pick_attend<T, MODE, BACK, false>(a, s);
 }
 
 }  // namespace gdnl

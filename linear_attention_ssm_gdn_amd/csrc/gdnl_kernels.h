@@ -41,7 +41,6 @@ hipError_t launch_segments(const SegmentArgs& a, hipStream_t s);
 struct Rows {                    // packed rows of heads
     const void* p; int64_t stride;
     int32_t per;                 // value heads to a head of these rows
-    int32_t vec;                 // rows and heads on 16 bytes
 };
 
 // Where a segment's state comes from or goes to.
@@ -52,6 +51,18 @@ struct States {
     int32_t rs, cs;              // from row to row and column to column of the matrix the kernel holds
 };
 
+// For every row and head, G the inclusive sum of g log2(e) within the row's
+// chunk of its segment: {G, what G's float leaves of it, e^G, e^{G_C - G}}, and
+// for every segment the sum over its rows.
+struct DecayArgs {
+    const SegWord* segs; int64_t n_slots, n_rows;
+    int32_t heads;
+    const float* g; int64_t g_stride;
+    float4* gates;               // [heads][n_rows]
+    double* total;               // [slot][heads]
+};
+hipError_t launch_decays(const DecayArgs& a, hipStream_t s);
+
 // One pass of linear attention over segments, forward or backward in time.
 // For output row x and source row y of a chunk, y <= x forward, y >= x backward:
 //   out_x = f_p sum_y e^{|G_x - G_y|}' (q_x . k_y) v_y + f_i e^{..} q_x^T S,
@@ -61,17 +72,16 @@ struct States {
 struct AttendArgs {
     const SegWord* segs; int64_t n_slots;
     Rows q, k, v, x;
-    const float* g; int64_t g_stride;
+    const float4* gates;         // of launch_decays
     const uint8_t* has_init;
     int32_t dk, dv, heads;       // widths of q, k and of v, out; value heads
-    int32_t back;
     float f_p, f_i, f_u;
     States in, out;              // out: at the end of the sequence (local sums: of the segment)
     int32_t zero_uninit;         // out is zero where has_init is 0
     void* o; int64_t o_stride; int32_t o_f32;
+    int32_t vec;                 // all rows and heads on 16 bytes, those of o on four values
     float* dot;                  // [heads][n_rows]: see kDot, kDotRows
     int64_t n_rows;
-    double* total;               // [slot][heads]: the segment's sum of g, local sums only
 };
 enum AttendMode {
     kAttend = 0,
@@ -79,8 +89,15 @@ enum AttendMode {
     kDotRows,    // the same, plus row sums less column sums of M_xy = (f_p e^{..} q_x.k_y)(x_x.v_y), y != x
     kLocal       // the state's sum over the segment alone, from zero
 };
+// mode kAttend, kDotRows or kLocal; back: kAttend, kDot or kLocal
 hipError_t launch_attend_bf16(const AttendArgs& a, int mode, hipStream_t s);
 hipError_t launch_attend_f32(const AttendArgs& a, int mode, hipStream_t s);
+hipError_t launch_attend_bf16_back(const AttendArgs& a, int mode, hipStream_t s);
+hipError_t launch_attend_f32_back(const AttendArgs& a, int mode, hipStream_t s);
+inline hipError_t launch_attend(const AttendArgs& a, int mode, bool back, bool bf16, hipStream_t s) {
+    if (back) return bf16 ? launch_attend_bf16_back(a, mode, s) : launch_attend_f32_back(a, mode, s);
+    return bf16 ? launch_attend_bf16(a, mode, s) : launch_attend_f32(a, mode, s);
+}
 
 // S in front of (back: behind) every segment in the place of its local sum.
 struct ScanArgs {

@@ -84,6 +84,43 @@ hipError_t launch_segments(const SegmentArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// A workgroup to a segment and head, a wave to a chunk, a lane to a row.  g ends
+// at -128, where e^g is 0: differences of the sums behind it stay finite.
+__global__ __launch_bounds__(kThreads) void k_decays(const DecayArgs A) {
+    __shared__ double s_sum[kThreads / 64];
+    const int64_t slot = blockIdx.x / A.heads;
+    const int head = (int)(blockIdx.x % A.heads), lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int4 w = *reinterpret_cast<const int4*>(A.segs + slot);
+    if (w.z <= 0) return;
+    double total = 0.0;
+    for (int t0 = wave * kChunk; t0 < w.z; t0 += kThreads) {
+        const int64_t row = (int64_t)w.y + t0 + lane;
+        const bool in = t0 + lane < w.z;
+        const float g = in ? A.g[row * A.g_stride + head] : 0.0f;
+        double G = (double)(g < -128.0f ? -128.0f : g) * 1.4426950408889634;  // a NaN stays
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const double up = __shfl_up(G, d, 64);
+            if (lane >= d) G += up;
+        }
+        const double GC = __shfl(G, 63, 64);
+        total += GC;
+        const float into = (float)G, rest = (float)(GC - G);
+        const float lo = (float)(G - (double)into), rest_lo = (float)((GC - G) - (double)rest);
+        if (in)
+            A.gates[(int64_t)head * A.n_rows + row] =
+                make_float4(into, lo, gdnt::exp2_hw(into) * (1.0f + 0.6931472f * lo),
+                            gdnt::exp2_hw(rest) * (1.0f + 0.6931472f * rest_lo));
+    }
+    if (lane == 0) s_sum[wave] = total;
+    __syncthreads();
+    if (threadIdx.x == 0) A.total[blockIdx.x] = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
+}
+hipError_t launch_decays(const DecayArgs& a, hipStream_t s) {
+    hipLaunchKernelGGL(k_decays, dim3((unsigned)(a.n_slots * a.heads)), dim3(kThreads), 0, s, a);
+    return hipGetLastError();
+}
+
 // Four values of a state to a thread, a segment after the other.
 constexpr int kScanMine = 4;
 __global__ __launch_bounds__(kThreads) void k_state_scan(const ScanArgs A, int blocks) {

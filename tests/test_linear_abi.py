@@ -113,7 +113,7 @@ def _bad(L):
     B, S = L.GdnBatch, L.GdnStatePool
     return [dict(dims=None), dict(q=None), dict(k=None), dict(v=None), dict(g=None), dict(o=None), dict(qs=31), dict(ks=31),
             dict(vs=127), dict(os=127), dict(gs=3), dict(gs=-1), dict(q=FAKE + 1), dict(g=FAKE + 2), dict(o=FAKE + 1),
-            dict(qs=(1 << 30) + 1), dict(batch=None), dict(batch=B(FAKE, FAKE, None, -1, 0, 300)),
+            dict(qs=(1 << 24) + 1), dict(batch=None), dict(batch=B(FAKE, FAKE, None, -1, 0, 300)),
             dict(batch=B(FAKE, FAKE, None, 2, -1, 300)), dict(batch=B(FAKE, FAKE, None, 2, 0, -1)),
             dict(batch=B(None, FAKE, None, 2, 0, 300)), dict(batch=B(FAKE, None, None, 2, 0, 300)),
             dict(batch=B(FAKE, FAKE, None, 2, 0, (1 << 31) - 1)), dict(batch=B(FAKE, FAKE, None, 1 << 28, 0, 300)),
