@@ -330,10 +330,6 @@ template <typename O, bool VEC> __device__ __forceinline__ void put4(__amdgpu_bu
         }
     }
 }
-template <typename O> __device__ __forceinline__ void put_nan(__amdgpu_buffer_rsrc_t rs, uint32_t at) {
-    if constexpr (sizeof(O) == 4) __builtin_amdgcn_raw_buffer_store_b32(0x7fc00000u, rs, at, 0, 0);
-    else __builtin_amdgcn_raw_buffer_store_b16((uint16_t)0x7fc0u, rs, at, 0, 0);
-}
 // A wave's share of a chunk's output: 64 rows by 16 NT columns.
 template <typename O, bool VEC, int NT>
 __device__ __forceinline__ void put_rows(const AttendArgs& A, const f32x4 (&o)[4 * NT], int64_t row0, int head, int n, int col0, int g, int i) {
@@ -345,6 +341,28 @@ __device__ __forceinline__ void put_rows(const AttendArgs& A, const f32x4 (&o)[4
         const uint32_t at = (uint32_t)i * row + (uint32_t)c4 * (uint32_t)sizeof(O);
 #pragma unroll
         for (int b = 0; b < 4; ++b) put4<O, VEC>(rs, c4 < A.dv ? at + 16 * b * row : kNowhere, o[b * NT + nn], A.dv - c4);
+    }
+}
+
+// A chunk's bf16 rows from LDS, by the threads that later put the same pieces.
+template <int W, int THREADS, bool VEC>
+__device__ __forceinline__ void flush_rows(const AttendArgs& A, const char* stage, int64_t row0, int head, int n, int tid) {
+    using L = Tile<bf16_t, W>;
+    constexpr int kMine = kChunk * L::kPieces / THREADS;
+    const __amdgpu_buffer_rsrc_t rs = rows_buffer<bf16_t>(A.o, A.o_stride, row0, (int64_t)head * A.dv, n, A.dv);
+#pragma unroll
+    for (int k = 0; k < kMine; ++k) {
+        const int idx = tid + k * THREADS, row = idx / L::kPieces, c = idx % L::kPieces * L::kElems;
+        const u32x4 v = *reinterpret_cast<const u32x4*>(stage + L::place(row, idx % L::kPieces));
+        const uint32_t at = ((uint32_t)row * (uint32_t)A.o_stride + (uint32_t)c) * 2u;
+        if constexpr (VEC) {
+            __builtin_amdgcn_raw_buffer_store_b128(v, rs, c < A.dv ? at : kNowhere, 0, 0);
+        } else {
+#pragma unroll
+            for (int e = 0; e < L::kElems; ++e)
+                __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(v[e >> 1] >> (16 * (e & 1))), rs,
+                                                      c + e < A.dv ? at + 2u * e : kNowhere, 0, 0);
+        }
     }
 }
 
@@ -361,7 +379,12 @@ template <typename T, int DK, int W, int NT, int MODE> struct Layout {
     static constexpr int oX = oQ + (MODE == kLocal ? 0 : Tile<T, DK>::kBytes);
     static constexpr int oP = oX + (kX ? Tile<T, DV>::kBytes : 0);
     static constexpr int oG = oP + (MODE == kLocal ? 0 : kPairs * kTermsP * kPPair);
-    static constexpr int oBad = oG + (int)sizeof(Gates);       // first row of a column that is not finite
+    // bf16 outputs leave through LDS as whole rows: where x's rows stood, which
+    // the second half of a chunk does not need, else in a place of their own.
+    static constexpr bool kStage = sizeof(T) == 2 && MODE != kLocal;
+    static constexpr int oOwn = oG + (int)sizeof(Gates);
+    static constexpr int oO = kX ? oX : oOwn;
+    static constexpr int oBad = oOwn + (kStage && !kX ? Tile<T, DV>::kBytes : 0);  // first row of a column that is not finite
     static constexpr int oDot = oBad + DV * 8 + 16;
     static constexpr int oSum = oDot + (kX ? W * 64 * 4 : 0);
     static constexpr int kBytes = oSum + (MODE == kDotRows ? kTri * 32 * 4 : 0);
@@ -469,6 +492,11 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE>::kWavesPerSimd)
         int lane = lane0;
         asm volatile("" : "+v"(lane));
         const int tid = wave * 64 + lane, g = lane >> 4, i = lane & 15;
+        if constexpr (Y::kStage) {
+            if (step > 0 && !A.o_f32)
+                flush_rows<Y::DV, TH, VEC>(A, lds + Y::oO, row0 + (back ? kChunk : -kChunk), head,
+                                           back ? min(kChunk, seg.rows - (c + 1) * kChunk) : kChunk, tid);
+        }
         fk.put(tk, tid);
         fv.put(tv, tid);
         if constexpr (MODE != kLocal) fq.put_by_row(tq, tid);
@@ -591,7 +619,8 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE>::kWavesPerSimd)
                         for (int nn = 0; nn < NT; ++nn) O[b * NT + nn] = mma(sf[nn][ts], qf[b], O[b * NT + nn]);
             }
             decayed(wave, p, pm);
-            for (int t = wave + W; t < kTri; t += W) {
+            // the tiles beyond W go to other waves, so to other SIMDs, in every chunk
+            for (int t = W + ((wave - 2 * step) & (W - 1)); t < kTri; t += W) {
                 products(t, p, pm);
                 decayed(t, p, pm);
             }
@@ -662,16 +691,30 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE>::kWavesPerSimd)
                     }
             }
             settle(O);
-            if (sizeof(T) == 4 || A.o_f32) put_rows<float, VEC, NT>(A, O, row0, head, n, col0, g, i);
-            else put_rows<T, VEC, NT>(A, O, row0, head, n, col0, g, i);
-            if (bad) {
+            if (!Y::kStage || A.o_f32) {
+                put_rows<float, VEC, NT>(A, O, row0, head, n, col0, g, i);
+            } else {
+#pragma unroll
+                for (int nn = 0; nn < NT; ++nn)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b)
+                        *reinterpret_cast<u32x2*>(TV::at(lds + Y::oO, 16 * b + i, col0 + 16 * nn + 4 * g)) =
+                            u32x2{gdn::f32x2_to_bf16x2(O[b * NT + nn][0], O[b * NT + nn][1]),
+                                  gdn::f32x2_to_bf16x2(O[b * NT + nn][2], O[b * NT + nn][3])};
+            }
+            if (bad) {  // the same lanes wrote these places before
                 const __amdgpu_buffer_rsrc_t rs = rows_buffer<T>(A.o, A.o_stride, row0, (int64_t)head * A.dv, n, A.dv);
                 for (int nn = 0; nn < NT; ++nn)
                     for (int r = 0; r < 4; ++r) {
-                        const int c2 = col0 + 16 * nn + 4 * g + r;  // the same lanes wrote these places before
+                        const int c2 = col0 + 16 * nn + 4 * g + r;
                         for (int x = i; x < kChunk; x += 16) {
-                            const uint32_t at = ((uint32_t)x * (uint32_t)A.o_stride + (uint32_t)c2) * (uint32_t)sizeof(T);
-                            put_nan<T>(rs, c2 < A.dv && x >= bad_row[c2] ? at : kNowhere);
+                            if (x < bad_row[c2]) continue;
+                            if constexpr (Y::kStage) {
+                                *TV::at(lds + Y::oO, x, c2) = 0x7fc0;
+                            } else {
+                                const uint32_t at = ((uint32_t)x * (uint32_t)A.o_stride + (uint32_t)c2) * (uint32_t)sizeof(T);
+                                __builtin_amdgcn_raw_buffer_store_b32(0x7fc00000u, rs, c2 < A.dv ? at : kNowhere, 0, 0);
+                            }
                         }
                     }
             }
@@ -722,6 +765,12 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE>::kWavesPerSimd)
         lds_barrier();  // the tiles are free
     }
 
+    if constexpr (Y::kStage) {
+        const int c = back ? 0 : n_chunks - 1;
+        if (!A.o_f32)
+            flush_rows<Y::DV, TH, VEC>(A, lds + Y::oO, (int64_t)seg.row + (int64_t)c * kChunk, head,
+                                       min(kChunk, seg.rows - c * kChunk), threadIdx.x);
+    }
     if (A.out.at != kNoState && (MODE == kLocal || (back ? seg.first : seg.last))) {
         const bool zero = A.zero_uninit && A.has_init && A.has_init[seg.seq] == 0;
         const int64_t base = state_base(A.out, seg, slot, head);
