@@ -312,7 +312,6 @@ struct Gates {
     float hi[64], lo[64];   // G, the inclusive sum of g in powers of two, as two floats
     float row[64];          // factor of an output row's state part
     float src[64];          // weight of a source row in the state's update
-    float all, pad[3];      // e^{G_C}
 };
 
 // Four values of an output row, the first at byte `at` of rs; VEC: all four
@@ -366,7 +365,7 @@ __device__ __forceinline__ void flush_rows(const AttendArgs& A, const char* stag
     }
 }
 
-template <typename T, int DK, int W, int NT, int MODE> struct Layout {
+template <typename T, int DK, int W, int NT, int MODE, bool BACK> struct Layout {
     static constexpr int DV = 16 * W * NT;
     static constexpr int kTermsP = sizeof(T) == 2 ? 2 : 1;
     static constexpr int kTermsV = sizeof(T) == 2 ? 3 : 1;
@@ -385,9 +384,10 @@ template <typename T, int DK, int W, int NT, int MODE> struct Layout {
     static constexpr int oOwn = oG + (int)sizeof(Gates);
     static constexpr int oO = kX ? oX : oOwn;
     static constexpr int oBad = oOwn + (kStage && !kX ? Tile<T, DV>::kBytes : 0);  // first row of a column that is not finite
-    static constexpr int oDot = oBad + DV * 8 + 16;
+    static constexpr bool kGuard = MODE == kAttend && !BACK;  // values that are not finite reach no row before theirs
+    static constexpr int oDot = oBad + (kGuard ? DV * 8 + 16 : 0);
     static constexpr int oSum = oDot + (kX ? W * 64 * 4 : 0);
-    static constexpr int kBytes = oSum + (MODE == kDotRows ? kTri * 32 * 4 : 0);
+    static constexpr int kBytes = oSum + (MODE == kDotRows ? 64 * 4 * 4 : 0);
     // Waves on a SIMD that the registers are cut for: what LDS has room for, four at most.
     static constexpr int kRoom = 160 * 1024 / kBytes * W / 4;
     static constexpr int kWavesPerSimd = kRoom < 1 ? 1 : kRoom > 4 ? 4 : kRoom;
@@ -416,8 +416,8 @@ template <typename S, int M> __device__ __forceinline__ void store_state(const f
 
 // W waves, 16 NT columns each.
 template <typename T, int DK, int W, int NT, int MODE, bool back, bool VEC>
-__global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE>::kWavesPerSimd)) void k_attend(const AttendArgs A) {
-    using Y = Layout<T, DK, W, NT, MODE>;
+__global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPerSimd)) void k_attend(const AttendArgs A) {
+    using Y = Layout<T, DK, W, NT, MODE, back>;
     using TK = Tile<T, DK>;
     using TV = Tile<T, Y::DV>;
     constexpr int M = DK / 16, KS = DK / 32, TH = 64 * W;
@@ -449,6 +449,7 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE>::kWavesPerSimd)
     Fetch<T, DK, TH, VEC> fq, fk;
     Fetch<T, Y::DV, TH, VEC> fv, fx;
     float4 fg = make_float4(0, 0, 0, 0);
+    float next_all = 0.0f;  // e^{G_C}
     auto fetch = [&](int c, int tid, int lane) {  // nothing where the segment has no chunk c
         const int64_t row0 = (int64_t)seg.row + (int64_t)c * kChunk;
         const int n = c < 0 ? 0 : min(kChunk, seg.rows - c * kChunk);
@@ -456,13 +457,19 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE>::kWavesPerSimd)
         fv.load(A.v, head, A.dv, row0, n, tid);
         if constexpr (MODE != kLocal) fq.load(A.q, head, A.dk, row0, n, tid);
         if constexpr (Y::kX) fx.load(A.x, head, A.dv, row0, n, tid);
-        if (wave == 0 && n > 0) fg = A.gates[(int64_t)head * A.n_rows + row0 + min(lane, n - 1)];
+        if (n > 0) {
+            const float4* const rows = A.gates + (int64_t)head * A.n_rows + row0;
+            if (wave == 0) fg = rows[min(lane, n - 1)];
+            next_all = rows[n - 1].z;
+        }
     };
     if constexpr (MODE != kLocal)  // zeros, of which those that no tile overwrites stay
         for (int c = threadIdx.x; c < kPairs * Y::kTermsP * Y::kPPair / 16; c += TH)
             *reinterpret_cast<u32x4*>(tp + c * 16) = u32x4{0, 0, 0, 0};
-    if (threadIdx.x == 0) *s_bad = 0;
-    for (int c = threadIdx.x; c < Y::DV; c += TH) poison[c] = 0.0f;
+    if constexpr (Y::kGuard) {
+        if (threadIdx.x == 0) *s_bad = 0;
+        for (int c = threadIdx.x; c < Y::DV; c += TH) poison[c] = 0.0f;
+    }
     fetch(back ? n_chunks - 1 : 0, threadIdx.x, lane0);
     f32x4 S[NT][M];
     {
@@ -497,22 +504,22 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE>::kWavesPerSimd)
                 flush_rows<Y::DV, TH, VEC>(A, lds + Y::oO, row0 + (back ? kChunk : -kChunk), head,
                                            back ? min(kChunk, seg.rows - (c + 1) * kChunk) : kChunk, tid);
         }
+        const float all = next_all;
         fk.put(tk, tid);
         fv.put(tv, tid);
         if constexpr (MODE != kLocal) fq.put_by_row(tq, tid);
         if constexpr (Y::kX) fx.put(tx, tid);
-        if (MODE != kLocal && !back && fv.bad()) *s_bad = 1;
+        if (Y::kGuard && fv.bad()) *s_bad = 1;
         if (wave == 0) {  // rows behind the end count as the last one, whose weight is 1 and whose values are zeros
             G.hi[lane] = fg.x;
             G.lo[lane] = fg.y;
             G.row[lane] = A.f_i * (back ? fg.w : fg.z);
             G.src[lane] = A.f_u * (back ? fg.z : fg.w);
-            if (lane == 63) G.all = fg.z;
         }
         lds_barrier();
         // Where v is not finite (rare) zeros take its place, 0 times it being NaN:
         // outputs from its row on are overwritten, and the state's column is told.
-        const bool bad = MODE != kLocal && !back && *s_bad != 0;
+        const bool bad = Y::kGuard && *s_bad != 0;
         if (bad) {
             for (int c2 = tid; c2 < Y::DV; c2 += TH) {
                 int first = kChunk;
@@ -577,18 +584,20 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE>::kWavesPerSimd)
                     *reinterpret_cast<f32x4*>(at) = f32x4{v[0], v[1], v[2], v[3]};
                 }
                 if constexpr (MODE == kDotRows) {
-                    // M without its diagonal: sums over the tile's columns y for a row x, over its rows x for a column y
+                    // M without its diagonal: for a row x its sum over the tile's columns y, for a column y less its sum
+                    // over the tile's rows x, at s_sum[row][the other tile]
                     float row = 0.0f;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const float m = y0 + r == x ? 0.0f : v[r] * (pm[0][r] + pm[1][r]);
                         row += m;
                         const float cs = reduce16(m);
-                        if (i == 0) s_sum[t * 32 + 16 + 4 * g + r] = cs;
+                        if (i == 0) s_sum[(y0 + r) * 4 + o.tx] = -cs;
                     }
                     row += __shfl_xor(row, 16, 64);
                     row += __shfl_xor(row, 32, 64);
-                    if (g == 0) s_sum[t * 32 + i] = row;
+                    if (o.tx == o.ty) row += s_sum[x * 4 + o.tx];  // written above by this wave
+                    if (g == 0) s_sum[x * 4 + o.ty] = row;
                 }
             };
             f32x4 p[2], pm[2];
@@ -650,13 +659,8 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE>::kWavesPerSimd)
 #pragma unroll
                     for (int w = 0; w < W; ++w) d += s_dot[w * 64 + tid];
                     if constexpr (MODE == kDotRows) {
-                        const int b = tid >> 4, k = tid & 15;
-                        float row = 0.0f, cs = 0.0f;
-                        for (int o = 0; o < 4; ++o) {  // the other tile's index
-                            if (back ? o >= b : o <= b) row += s_sum[tri(min(o, b), max(o, b)) * 32 + k];
-                            if (back ? o <= b : o >= b) cs += s_sum[tri(min(o, b), max(o, b)) * 32 + 16 + k];
-                        }
-                        d += row - cs;
+                        const f32x4 s = *reinterpret_cast<const f32x4*>(s_sum + 4 * tid);
+                        d += (s[0] + s[1]) + (s[2] + s[3]);
                     }
                     A.dot[(int64_t)head * A.n_rows + row0 + tid] = d;
                 }
@@ -721,7 +725,6 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE>::kWavesPerSimd)
         }
         // The next chunk's rows are asked for where the registers that held the output are free.
         fetch(back ? c - 1 : c + 1, tid, lane);
-        const float all = G.all;
         const int kc = TK::col_base(g, i);
 #pragma unroll
         for (int nn = 0; nn < NT; ++nn)
@@ -741,7 +744,7 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE>::kWavesPerSimd)
                     f[r] *= w0[r];
                     f[4 + r] *= w1[r];
                 }
-                if constexpr (MODE != kLocal && !back) f[0] += poison[col0 + 16 * nn + i];
+                if constexpr (Y::kGuard) f[0] += poison[col0 + 16 * nn + i];
                 split<Y::kTermsV>(f, vw[nn]);
             }
 #pragma unroll
@@ -789,7 +792,7 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE>::kWavesPerSimd)
 }
 
 template <typename T, int DK, int W, int NT, int MODE, bool BACK, bool VEC> hipError_t run_attend(const AttendArgs& a, hipStream_t s) {
-    static_assert(Layout<T, DK, W, NT, MODE>::kBytes <= 160 * 1024, "LDS");
+    static_assert(Layout<T, DK, W, NT, MODE, BACK>::kBytes <= 160 * 1024, "LDS");
     const int64_t grid = xcd_grid(a.n_slots * a.heads);
     hipLaunchKernelGGL((k_attend<T, DK, W, NT, MODE, BACK, VEC>), dim3((unsigned)grid), dim3(64 * W), 0, s, a);
     return hipGetLastError();

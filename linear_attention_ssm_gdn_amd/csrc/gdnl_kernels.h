@@ -126,7 +126,8 @@ hipError_t launch_gate_sum(const double* part, int64_t n_slots, int32_t heads, f
 // out[row][h][c] = sum over a group's value heads of part[row][h * per + j][c], in order.
 struct GroupArgs {
     const SegWord* segs; int64_t n_slots;
-    int32_t heads, per, d, bf16;
+    int32_t heads, per, d, bf16, vec;   // vec: rows and heads on four values
+    int64_t most_rows;                  // of a segment
     const float* part; void* out; int64_t stride;
 };
 hipError_t launch_group_sum(const GroupArgs& a, hipStream_t s);

@@ -121,42 +121,41 @@ hipError_t launch_decays(const DecayArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-// Four values of a state to a thread, a segment after the other.
-constexpr int kScanMine = 4;
+// A value of a state to a thread; the local sums of eight segments are asked for
+// together, since they do not depend on what is carried.
+constexpr int kScanAhead = 8;
 __global__ __launch_bounds__(kThreads) void k_state_scan(const ScanArgs A, int blocks) {
     for (int64_t b = blockIdx.x; b < (int64_t)A.n_seqs * A.heads * blocks; b += gridDim.x) {
         const int part = (int)(b % blocks), head = (int)(b / blocks % A.heads), seq = (int)(b / blocks / A.heads);
         const SeqSlots at = A.seqs[seq];
-        if (at.n <= 0) continue;
+        const int e = part * kThreads + threadIdx.x;
+        if (at.n <= 0 || e >= A.size) continue;
         const bool zero = A.in.at == kNoState || (A.in.at == kByPage && A.has_init && A.has_init[seq] == 0);
-        const int64_t base = zero ? 0 : (A.in.at == kByPage ? (int64_t)A.page_idx[seq] : (int64_t)seq) * A.in.unit + head * A.in.head;
-        float cur[kScanMine];
-#pragma unroll
-        for (int j = 0; j < kScanMine; ++j) {
-            const int e = (part * kScanMine + j) * kThreads + threadIdx.x;
-            cur[j] = zero || e >= A.size ? 0.0f
-                     : A.in.bf16         ? gdn::to_f32(static_cast<const gdn::bf16_t*>(A.in.p)[base + e])
-                                         : static_cast<const float*>(A.in.p)[base + e];
+        float cur = 0.0f;
+        if (!zero) {
+            const int64_t from = (A.in.at == kByPage ? (int64_t)A.page_idx[seq] : (int64_t)seq) * A.in.unit + head * A.in.head + e;
+            cur = A.in.bf16 ? gdn::to_f32(static_cast<const gdn::bf16_t*>(A.in.p)[from]) : static_cast<const float*>(A.in.p)[from];
         }
-        for (int k = 0; k < at.n; ++k) {
-            const int64_t slot = at.slot + (A.back ? at.n - 1 - k : k);
-            float* const p = A.local + (slot * A.heads + head) * A.size;
-            const bool more = k + 1 < at.n;  // the last one's local sum was not made
-            const float decay = more ? (float)exp2(A.total[slot * A.heads + head]) : 0.0f;
+        for (int k0 = 0; k0 < at.n; k0 += kScanAhead) {
+            float own[kScanAhead], decay[kScanAhead];
+            const int64_t step = A.back ? -1 : 1, first = at.slot + (A.back ? at.n - 1 - k0 : k0);
 #pragma unroll
-            for (int j = 0; j < kScanMine; ++j) {
-                const int e = (part * kScanMine + j) * kThreads + threadIdx.x;
-                if (e < A.size) {
-                    const float own = more ? p[e] : 0.0f;
-                    p[e] = cur[j];
-                    cur[j] = fmaf(decay, cur[j], own);
-                }
+            for (int j = 0; j < kScanAhead; ++j) {
+                const bool more = k0 + j + 1 < at.n;  // the last one's local sum was not made
+                const int64_t item = (first + step * j) * A.heads + head;
+                own[j] = more ? A.local[item * A.size + e] : 0.0f;
+                decay[j] = more ? (float)exp2(A.total[item]) : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < kScanAhead; ++j) {
+                if (k0 + j < at.n) A.local[((first + step * j) * A.heads + head) * A.size + e] = cur;
+                cur = fmaf(decay[j], cur, own[j]);
             }
         }
     }
 }
 hipError_t launch_state_scan(const ScanArgs& a, hipStream_t s) {
-    const int blocks = (a.size + kScanMine * kThreads - 1) / (kScanMine * kThreads);
+    const int blocks = (a.size + kThreads - 1) / kThreads;
     int64_t grid = (int64_t)a.n_seqs * a.heads * blocks;
     if (grid > (1 << 20)) grid = 1 << 20;
     hipLaunchKernelGGL(k_state_scan, dim3((unsigned)grid), dim3(kThreads), 0, s, a, blocks);
@@ -196,8 +195,10 @@ __global__ __launch_bounds__(kThreads) void k_gate(const GateArgs A) {
         e = A.after + (slot * A.heads + head) * A.size;
     }
     double x = 0.0;
-    if (p)
+    if (p) {
+#pragma unroll 8
         for (int j = tid; j < A.size; j += kThreads) x += (double)p[j] * (double)e[j];
+    }
     double carry = block_sum(x, s_part), sum = 0.0;
     for (int t0 = (rows - 1) / kThreads * kThreads; t0 >= 0; t0 -= kThreads) {
         // thread 0 takes the tile's last row
@@ -250,31 +251,46 @@ hipError_t launch_gate_sum(const double* part, int64_t n_slots, int32_t heads, f
     return hipGetLastError();
 }
 
-// A workgroup to 16 rows of a segment.
-constexpr int kGroupRows = 16;
-__global__ __launch_bounds__(kThreads) void k_group_sum(const GroupArgs A, int blocks) {
+// Four rows of a segment to a workgroup at a time, V values to a thread.
+constexpr int kGroupRows = 4;
+template <int V> __global__ __launch_bounds__(kThreads) void k_group_sum(const GroupArgs A, int blocks) {
     const int64_t slot = blockIdx.x / blocks;
     const int4 w = *reinterpret_cast<const int4*>(A.segs + slot);
-    const int width = A.heads / A.per * A.d;
+    const int per_row = A.heads / A.per * (A.d / V), per_head = A.d / V;
     for (int t0 = (int)(blockIdx.x % blocks) * kGroupRows; t0 < w.z; t0 += blocks * kGroupRows) {
         const int n = min(kGroupRows, w.z - t0);
-        for (int j = threadIdx.x; j < n * width; j += kThreads) {
-            const int t = j / width, c = j - t * width, h = c / A.d, d = c - h * A.d;
+        for (int j = threadIdx.x; j < n * per_row; j += kThreads) {
+            const int t = j / per_row, c = j - t * per_row, h = c / per_head, d = (c - h * per_head) * V;
             const int64_t row = (int64_t)w.y + t0 + t;
             const float* p = A.part + (row * A.heads + (int64_t)h * A.per) * A.d + d;
-            float v = 0.0f;
-            for (int q = 0; q < A.per; ++q) v += p[(int64_t)q * A.d];
-            const int64_t at = row * A.stride + c;
-            if (A.bf16) static_cast<gdn::bf16_t*>(A.out)[at] = gdn::f32_to_bf16(v);
-            else static_cast<float*>(A.out)[at] = v;
+            float v[V] = {};
+            for (int q = 0; q < A.per; ++q) {
+                if constexpr (V == 4) {
+                    const float4 u = *reinterpret_cast<const float4*>(p + (int64_t)q * A.d);
+                    v[0] += u.x; v[1] += u.y; v[2] += u.z; v[3] += u.w;
+                } else {
+                    v[0] += p[(int64_t)q * A.d];
+                }
+            }
+            const int64_t at = row * A.stride + (int64_t)h * A.d + d;
+            if constexpr (V == 4) {
+                if (A.bf16) gdnt::store4<true>(static_cast<gdn::bf16_t*>(A.out) + at, v, 4);
+                else gdnt::store4<true>(static_cast<float*>(A.out) + at, v, 4);
+            } else {
+                if (A.bf16) static_cast<gdn::bf16_t*>(A.out)[at] = gdn::f32_to_bf16(v[0]);
+                else static_cast<float*>(A.out)[at] = v[0];
+            }
         }
     }
 }
 hipError_t launch_group_sum(const GroupArgs& a, hipStream_t s) {
-    // enough workgroups for the card whatever the segments' length
-    int64_t blocks = (8192 + a.n_slots - 1) / a.n_slots;
-    blocks = blocks > 128 ? 128 : blocks;
-    hipLaunchKernelGGL(k_group_sum, dim3((unsigned)(a.n_slots * blocks)), dim3(kThreads), 0, s, a, (int)blocks);
+    // as many workgroups as a segment has rows for, within some 16384
+    int64_t blocks = (a.most_rows + kGroupRows - 1) / kGroupRows;
+    const int64_t most = 16384 / a.n_slots + 1;
+    blocks = blocks > most ? most : blocks < 1 ? 1 : blocks;
+    const dim3 grid((unsigned)(a.n_slots * blocks)), block(kThreads);
+    if (a.vec) hipLaunchKernelGGL(k_group_sum<4>, grid, block, 0, s, a, (int)blocks);
+    else hipLaunchKernelGGL(k_group_sum<1>, grid, block, 0, s, a, (int)blocks);
     return hipGetLastError();
 }
 

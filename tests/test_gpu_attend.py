@@ -63,7 +63,7 @@ def test_backward_without_the_optional_parts(act):
 @pytest.mark.parametrize("decay", ["row", "head"])
 def test_several_segments(act, decay):
     """Long sequences are cut into segments whose states are joined."""
-    c = Case([700, 256, 0, 300, 5], hk=1, hv=2, dk=40, dv=24, act=act, decay=decay, fast=0.1)
+    c = Case([1300, 256, 0, 1100, 5], hk=1, hv=2, dk=40, dv=24, act=act, decay=decay, fast=0.1)
     o, so = c.forward()
     c.check_forward(o, so)
     o, so2 = c.forward(in_place=True)
@@ -73,7 +73,7 @@ def test_several_segments(act, decay):
 
 
 def test_several_segments_with_padding_and_fresh_states():
-    c = Case([300, 290, 600], hk=1, hv=1, dk=16, dv=16, skip=(1,), gap=3, tail=4, has_init=[0, 1, 1], act="bf16", fast=0.05)
+    c = Case([300, 290, 1100], hk=1, hv=1, dk=16, dv=16, skip=(1,), gap=3, tail=4, has_init=[0, 1, 1], act="bf16", fast=0.05)
     o, so = c.forward()
     c.check_forward(o, so)
     c.check_backward(c.backward())
@@ -216,7 +216,7 @@ def test_what_is_not_finite_reaches_its_column_from_its_row_on(act, bad, rows, m
 
 
 def test_on_another_stream_and_twice_at_once():
-    c, d = Case([300, 70], act="bf16", dk=64, dv=64), Case([5, 400], act="bf16", dk=64, dv=64, seed=5)
+    c, d = Case([1300, 70], act="bf16", dk=64, dv=64), Case([5, 1400], act="bf16", dk=64, dv=64, seed=5)
     want = [x.forward()[0] for x in (c, d)], [x.backward() for x in (c, d)]
     streams = [torch.cuda.Stream() for _ in range(2)]
     g = gdn()
@@ -242,7 +242,7 @@ def test_on_another_stream_and_twice_at_once():
 def test_captured_and_replayed(max_len):
     """One capture serves other lengths, pages and values; each replay is the eager result."""
     g = gdn()
-    c = Case([1, 2, 1] if max_len else [300, 2, 90], act="bf16", dk=64, dv=64, max_len=max_len)
+    c = Case([1, 2, 1] if max_len else [1300, 2, 90], act="bf16", dk=64, dv=64, max_len=max_len)
     pool, so = g.StatePool(c.s0.to(DEV).clone()), g.StatePool(torch.zeros_like(c.s0.to(DEV)))
     o, ds = torch.zeros_like(c.t["v"]), torch.from_numpy(c.d_state).to(DEV)
     ws = torch.empty(g.gdnl_attend_workspace_bytes(c.dims, c.n, c.rows, backward=True), dtype=torch.uint8, device=DEV)
@@ -261,7 +261,7 @@ def test_captured_and_replayed(max_len):
         step()
     for k in range(3):
         c.t["v"].normal_()
-        cu = [[0, 1, 3, 4], [0, 2, 3, 4], [0, 0, 1, 3]][k] if max_len else [[0, 300, 302, 392], [0, 10, 300, 301], [0, 0, 390, 392]][k]
+        cu = [[0, 1, 3, 4], [0, 2, 3, 4], [0, 0, 1, 3]][k] if max_len else [[0, 1300, 1302, 1392], [0, 10, 1300, 1301], [0, 0, 1390, 1392]][k]
         c.batch.cu_seqlens.copy_(torch.tensor(cu, dtype=torch.int32))
         for t in (o, so.buf, *grads):
             t.zero_()
@@ -316,7 +316,7 @@ def test_many_sequences_and_an_empty_batch():
 
 
 def test_results_do_not_depend_on_timing():
-    c = Case([900, 70], act="bf16", dk=64, dv=64, decay="head")
+    c = Case([1500, 70], act="bf16", dk=64, dv=64, decay="head")
     o, so = c.forward()
     d = c.backward()
     for _ in range(5):
