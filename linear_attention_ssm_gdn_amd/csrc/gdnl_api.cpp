@@ -16,13 +16,13 @@ namespace {
 // Batches whose longest sequence has at most this many rows go row by row.
 constexpr int32_t kTokensMax = 8;
 // Rows of a segment, at least, and workgroups (segments times value heads)
-// from which on segments grow longer instead of more: twice two to a compute
-// unit (512: 553 against 524 us forward, 2936 against 2726 with the backward
-// pass, over 4 x 8192 rows of 32 heads).
-// Batches whose longest sequence has at most kSegNone rows are not cut: the
-// states between segments cost two more launches and another reading of k and v.
+// from which on segments grow longer instead of more: two to a compute unit
+// (512, 1024, 2048 take 425, 460, 526 us forward and 2165, 2340, 2610 with the
+// backward pass over 4 x 8192 rows of 32 heads).  Batches whose longest sequence
+// has at most kSegNone rows are not cut: the states between segments cost two
+// more launches and another reading of k and v.
 constexpr int32_t kSegMin = 256, kSegNone = 1024;
-constexpr int64_t kSegGroups = 1024;
+constexpr int64_t kSegGroups = 512;
 constexpr int32_t kSegWhole = INT32_MAX;  // every sequence is one segment
 constexpr int64_t kMaxGroups = 1 << 24;  // 256 threads each: HIP launches fewer than 2^32 threads
 
@@ -212,7 +212,7 @@ GDN_EXPORT int32_t gdnl_attend_forward(const gdnl_dims* dims, const void* q, int
     A.vec = rows_on(q, q_stride, dims->d_k, dt, 16) && rows_on(k, k_stride, dims->d_k, dt, 16) &&
             rows_on(v, v_stride, dims->d_v, dt, 16) && rows_on(o, o_stride, dims->d_v, dt, 16);
     A.has_init = batch->has_init;
-    A.dk = dims->d_k; A.dv = dims->d_v; A.heads = H;
+    A.dk = dims->d_k; A.dv = dims->d_v; A.heads = H; A.per = per;
     A.f_p = A.f_i = dims->scale; A.f_u = 1.0f;
     A.gates = reinterpret_cast<const float4*>(ws + w.gates);
     gdnl::DecayArgs D{G.segs, p.slots, batch->n_rows, H, g, g_stride, reinterpret_cast<float4*>(ws + w.gates), total};
@@ -285,7 +285,7 @@ GDN_EXPORT int32_t gdnl_attend_backward(const gdnl_dims* dims, const void* q, in
             rows_on(dq, dq_stride, dims->d_k, dt, 16) && rows_on(dk, dk_stride, dims->d_k, dt, 16) &&
             rows_on(dv, dv_stride, dims->d_v, dt, 16);
     A.segs = G.segs; A.n_slots = p.slots; A.n_rows = batch->n_rows;
-    A.has_init = batch->has_init; A.heads = H;
+    A.has_init = batch->has_init; A.heads = H; A.per = per;
     A.gates = reinterpret_cast<const float4*>(ws + w.gates);
     gdnl::DecayArgs D{G.segs, p.slots, batch->n_rows, H, g, g_stride, reinterpret_cast<float4*>(ws + w.gates), total};
     if ((e = gdnl::launch_decays(D, s)) != hipSuccess) return from_hip(e);

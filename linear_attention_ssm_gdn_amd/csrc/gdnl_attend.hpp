@@ -298,14 +298,14 @@ __device__ __forceinline__ int64_t state_base(const States& s, const Segment& se
     return unit * s.unit + head * s.head;
 }
 
-// Workgroups go round the eight XCDs; each XCD takes a run of consecutive
-// (slot, head) pairs, so the value heads that read the same q and k rows, and
-// a segment's neighbours, share an L2.
-__device__ __forceinline__ int64_t xcd_item(int64_t b, int64_t n) {
-    const int64_t per = (n + 7) / 8;
-    return (b & 7) * per + (b >> 3);
+// Workgroups go round the eight XCDs.  The value heads of a key head, which read
+// the same q and k rows, follow one another on one XCD and share its L2; the
+// slots, some of them empty, are spread over all XCDs evenly.
+__device__ __forceinline__ int64_t xcd_item(int64_t b, int per) {
+    const int64_t j = b >> 3;
+    return ((j / per) * 8 + (b & 7)) * per + j % per;
 }
-inline int64_t xcd_grid(int64_t n) { return (n + 7) / 8 * 8; }
+inline int64_t xcd_grid(int64_t items, int per) { return (items / per + 7) / 8 * 8 * per; }
 
 // What the decays of a chunk come to, in LDS.
 struct Gates {
@@ -434,7 +434,7 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
     float* const s_dot = reinterpret_cast<float*>(lds + Y::oDot);
     float* const s_sum = reinterpret_cast<float*>(lds + Y::oSum);
 
-    const int64_t item = xcd_item(blockIdx.x, A.n_slots * A.heads);
+    const int64_t item = xcd_item(blockIdx.x, A.per);
     if (item >= A.n_slots * A.heads) return;
     const int64_t slot = item / A.heads;
     const int head = (int)(item - slot * A.heads);
@@ -793,7 +793,7 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
 
 template <typename T, int DK, int W, int NT, int MODE, bool BACK, bool VEC> hipError_t run_attend(const AttendArgs& a, hipStream_t s) {
     static_assert(Layout<T, DK, W, NT, MODE, BACK>::kBytes <= 160 * 1024, "LDS");
-    const int64_t grid = xcd_grid(a.n_slots * a.heads);
+    const int64_t grid = xcd_grid(a.n_slots * a.heads, a.per);
     hipLaunchKernelGGL((k_attend<T, DK, W, NT, MODE, BACK, VEC>), dim3((unsigned)grid), dim3(64 * W), 0, s, a);
     return hipGetLastError();
 }

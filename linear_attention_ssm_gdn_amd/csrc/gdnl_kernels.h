@@ -74,7 +74,7 @@ struct AttendArgs {
     Rows q, k, v, x;
     const float4* gates;         // of launch_decays
     const uint8_t* has_init;
-    int32_t dk, dv, heads;       // widths of q, k and of v, out; value heads
+    int32_t dk, dv, heads, per;  // widths of q, k and of v, out; value heads, those to a key head
     float f_p, f_i, f_u;
     States in, out;              // out: at the end of the sequence (local sums: of the segment)
     int32_t zero_uninit;         // out is zero where has_init is 0
