@@ -127,7 +127,7 @@ gdnl::States turned(gdnl::States s) {
 }
 
 struct Plan {
-    int64_t len, slots;
+    int64_t len, slots, segments;  // rows of a segment; segments of the call and, at most, of a sequence
     bool split;  // sequences may have several segments
 };
 Plan plan_of(const gdnl_dims* d, const gdn_batch* b) {
@@ -137,6 +137,7 @@ Plan plan_of(const gdnl_dims* d, const gdn_batch* b) {
     p.split = most > p.len && most > kSegNone;
     if (!p.split) p.len = kSegWhole;
     p.slots = slots_of(b->n_seqs, b->n_rows, p.len);
+    p.segments = (most + p.len - 1) / p.len;
     return p;
 }
 
@@ -222,7 +223,7 @@ GDN_EXPORT int32_t gdnl_attend_forward(const gdnl_dims* dims, const void* q, int
         if ((e = gdnl::launch_attend(A, gdnl::kLocal, false, dt == GDN_BF16, s)) != hipSuccess) return from_hip(e);
         gdnl::ScanArgs C{G.seqs, batch->page_idx, batch->has_init, batch->n_seqs, H, dims->d_k * dims->d_v, 0,
                          pages_of(dims, state_in), before, total};
-        if ((e = gdnl::launch_state_scan(C, s)) != hipSuccess) return from_hip(e);
+        if ((e = gdnl::launch_state_scan(C, p.segments, s)) != hipSuccess) return from_hip(e);
     }
     A.in = p.split ? dense(dims, before, gdnl::kBySlot) : pages_of(dims, state_in);
     A.out = pages_of(dims, state_out);
@@ -297,12 +298,12 @@ GDN_EXPORT int32_t gdnl_attend_backward(const gdnl_dims* dims, const void* q, in
         if ((e = gdnl::launch_attend(A, gdnl::kLocal, false, dt == GDN_BF16, s)) != hipSuccess) return from_hip(e);
         gdnl::ScanArgs C{G.seqs, batch->page_idx, batch->has_init, batch->n_seqs, H, size, 0, pages_of(dims, state_in),
                          before, total};
-        if ((e = gdnl::launch_state_scan(C, s)) != hipSuccess) return from_hip(e);
+        if ((e = gdnl::launch_state_scan(C, p.segments, s)) != hipSuccess) return from_hip(e);
         A.k = rq; A.v = ro; A.f_u = dims->scale;
         A.out = dense(dims, after, gdnl::kBySlot);
         if ((e = gdnl::launch_attend(A, gdnl::kLocal, true, dt == GDN_BF16, s)) != hipSuccess) return from_hip(e);
         C.in = ends; C.back = 1; C.local = after;
-        if ((e = gdnl::launch_state_scan(C, s)) != hipSuccess) return from_hip(e);
+        if ((e = gdnl::launch_state_scan(C, p.segments, s)) != hipSuccess) return from_hip(e);
     }
     const bool grouped = per > 1;
     auto group = [&](void* out, int64_t stride) {

@@ -420,7 +420,9 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
     using Y = Layout<T, DK, W, NT, MODE, back>;
     using TK = Tile<T, DK>;
     using TV = Tile<T, Y::DV>;
-    constexpr int M = DK / 16, KS = DK / 32, TH = 64 * W;
+    // KG sums of the state's update in turn; fewer where a fourth tile's rows are in registers (a spill there waits for
+    // memory: 485 us with four, 400 with two, kDotRows over 32768 rows of 32 heads)
+    constexpr int KG = Y::kX ? 2 : 4, M = DK / 16, KS = DK / 32, TH = 64 * W;
     __shared__ __attribute__((aligned(16))) char lds[Y::kBytes];
     char* const tk = lds + Y::oK;
     char* const tv = lds + Y::oV;
@@ -496,9 +498,10 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
         const int64_t row0 = (int64_t)seg.row + (int64_t)c * kChunk;
         const int n = min(kChunk, seg.rows - c * kChunk);
         // what follows from a lane's number is worked out again for each chunk: kept, it would fill the registers
+        // (not so for the local sums: 110 us against 123 over 32768 rows of 32 heads)
         int lane = lane0;
-        asm volatile("" : "+v"(lane));
-        const int tid = wave * 64 + lane, g = lane >> 4, i = lane & 15;
+        if constexpr (MODE != kLocal) asm volatile("" : "+v"(lane));
+        const int tid = MODE == kLocal ? (int)threadIdx.x : wave * 64 + lane, g = lane >> 4, i = lane & 15;
         if constexpr (Y::kStage) {
             if (step > 0 && !A.o_f32)
                 flush_rows<Y::DV, TH, VEC>(A, lds + Y::oO, row0 + (back ? kChunk : -kChunk), head,
@@ -546,20 +549,21 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
                 const int hi = t >= 6 ? 3 : t >= 3 ? 2 : t >= 1 ? 1 : 0, lo = t - hi * (hi + 1) / 2;
                 return back ? Of{hi, lo} : Of{lo, hi};
             };
-            auto products = [&](int t, f32x4 (&p)[2], f32x4 (&pm)[2]) {
+            auto products = [&](int t, f32x4 (&p)[2]) {
                 const Of o = tile_of(t);
-                p[0] = p[1] = pm[0] = pm[1] = f32x4{0, 0, 0, 0};
+                p[0] = p[1] = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) p[ks & 1] = mma(TK::by_row(tk, kr, o.ty, ks), TK::whole(tq, qr, o.tx, ks), p[ks & 1]);
+            };
+            auto decayed = [&](int t, f32x4 (&p)[2]) {
+                const Of o = tile_of(t);
+                settle(p);
+                f32x4 pm[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
                 if constexpr (MODE == kDotRows) {
 #pragma unroll
                     for (int ks = 0; ks < Y::DV / 32; ++ks)
                         pm[ks & 1] = mma(TV::by_row(tv, xr, o.ty, ks), TV::by_row(tx, xr, o.tx, ks), pm[ks & 1]);
                 }
-            };
-            auto decayed = [&](int t, f32x4 (&p)[2], f32x4 (&pm)[2]) {
-                const Of o = tile_of(t);
-                settle(p);
                 if constexpr (MODE == kDotRows) settle(pm);
                 const int x = 16 * o.tx + i, y0 = 16 * o.ty + 4 * g;
                 const float xh = G.hi[x], xl = G.lo[x];
@@ -600,8 +604,8 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
                     if (g == 0) s_sum[x * 4 + o.ty] = row;
                 }
             };
-            f32x4 p[2], pm[2];
-            products(wave, p, pm);
+            f32x4 p[2];
+            if constexpr (MODE != kDotRows) products(wave, p);  // there, registers are short
             // the state's part, transposed: a lane holds four columns of row 16 b + i
 #pragma unroll
             for (int j = 0; j < 4 * NT; ++j) O[j] = f32x4{0, 0, 0, 0};
@@ -627,11 +631,12 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
 #pragma unroll
                         for (int nn = 0; nn < NT; ++nn) O[b * NT + nn] = mma(sf[nn][ts], qf[b], O[b * NT + nn]);
             }
-            decayed(wave, p, pm);
+            if constexpr (MODE == kDotRows) products(wave, p);
+            decayed(wave, p);
             // the tiles beyond W go to other waves, so to other SIMDs, in every chunk
             for (int t = W + ((wave - 2 * step) & (W - 1)); t < kTri; t += W) {
-                products(t, p, pm);
-                decayed(t, p, pm);
+                products(t, p);
+                decayed(t, p);
             }
             settle(O);
 #pragma unroll
@@ -748,14 +753,14 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
                 split<Y::kTermsV>(f, vw[nn]);
             }
 #pragma unroll
-            for (int m = 0; m < M; m += 4) {  // four sums in turn: none waits for itself
-                Frag<T> kf[4];
+            for (int m = 0; m < M; m += KG) {  // sums in turn: none waits for itself
+                Frag<T> kf[KG];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) kf[j] = TK::by_col(tk, kc, ys, m + j);
+                for (int j = 0; j < KG; ++j) kf[j] = TK::by_col(tk, kc, ys, m + j);
 #pragma unroll
                 for (int tt = 0; tt < Y::kTermsV; ++tt)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                    for (int j = 0; j < KG; ++j)
 #pragma unroll
                         for (int nn = 0; nn < NT; ++nn) S[nn][m + j] = mma(kf[j], vw[nn][tt], S[nn][m + j]);
             }

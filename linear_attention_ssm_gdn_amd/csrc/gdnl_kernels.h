@@ -106,7 +106,7 @@ struct ScanArgs {
     States in;
     float* local; const double* total;
 };
-hipError_t launch_state_scan(const ScanArgs& a, hipStream_t s);
+hipError_t launch_state_scan(const ScanArgs& a, int64_t segments, hipStream_t s);  // of a sequence, at most
 
 // dg_t = X + sum_{i >= t} (rows_i - cols_i) within a segment, X = <state, its
 // gradient> at the segment's end.
