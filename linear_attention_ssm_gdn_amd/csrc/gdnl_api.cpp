@@ -18,11 +18,20 @@ constexpr int32_t kTokensMax = 8;
 // Rows of a segment, at least, and workgroups (segments times value heads)
 // from which on segments grow longer instead of more: two to a compute unit
 // (512, 1024, 2048 take 425, 460, 526 us forward and 2165, 2340, 2610 with the
-// backward pass over 4 x 8192 rows of 32 heads).  Batches whose longest sequence
-// has at most kSegNone rows are not cut: the states between segments cost two
-// more launches and another reading of k and v.
-constexpr int32_t kSegMin = 256, kSegNone = 1024;
+// backward pass over 4 x 8192 rows of 32 heads), and one where segments are short
+// and states wide, whose reading and writing then counts (256 and 512 take 75 and
+// 90 us over 2000 rows of 32 heads of 128 x 128, 96 and 110 us over 4000).
+constexpr int32_t kSegMin = 128, kSegShort = 512;
 constexpr int64_t kSegGroups = 512;
+// Batches whose longest sequence has at most kSegNone rows are not cut, the states
+// between segments costing two more launches and another reading of k and v; where
+// sequences times heads are fewer than kSegFew, batches of at most kSegFewNone
+// (900 rows of 8 heads 87 us uncut and 42 cut, 4 x 1000 rows of 32 heads 104 and 132).
+constexpr int32_t kSegNone = 1024, kSegFewNone = 512;
+constexpr int64_t kSegFew = 128;
+// A backward pass takes no longer ones: the gradients of the decays are sums over
+// the rows to a segment's ends, whose rounding grows with them.
+constexpr int64_t kSegBack = 2048;
 constexpr int32_t kSegWhole = INT32_MAX;  // every sequence is one segment
 constexpr int64_t kMaxGroups = 1 << 24;  // 256 threads each: HIP launches fewer than 2^32 threads
 
@@ -69,21 +78,25 @@ int32_t check_pool(const gdnl_dims* d, const gdn_state_pool& s) {
 
 // Rows of a segment for a batch of n_rows: as few as leave about kSegGroups
 // workgroups.
-int64_t seg_rows(int64_t n_rows, int64_t heads) {
+int64_t seg_rows(int64_t n_rows, const gdnl_dims* d, bool backward) {
+    const int64_t most_short = d->d_k > 64 || d->d_v > 64 ? kSegGroups / 2 : kSegGroups;
     int64_t len = kSegMin;
-    while (len < n_rows && (n_rows + len - 1) / len * heads > kSegGroups) len *= 2;
+    while (len < n_rows && (n_rows + len - 1) / len * d->h_v > (len < kSegShort ? most_short : kSegGroups) &&
+           !(backward && len == kSegBack))
+        len *= 2;
     return len;
 }
 int64_t slots_of(int64_t n_seqs, int64_t n_rows, int64_t len) { return n_seqs + (n_rows + len - 1) / len + 1; }
 // The most slots that a batch of up to n_seqs sequences and n_rows rows has.
-int64_t most_slots(int64_t n_seqs, int64_t n_rows, int64_t heads) {
+int64_t most_slots(int64_t n_seqs, int64_t n_rows, int64_t heads, bool backward) {
     const int64_t by_rows = (n_rows + kSegMin - 1) / kSegMin, by_groups = kSegGroups / heads;
-    const int64_t most = by_rows < by_groups ? by_rows : by_groups;
+    int64_t most = by_rows < by_groups ? by_rows : by_groups;
+    if (backward && most < (n_rows + kSegBack - 1) / kSegBack) most = (n_rows + kSegBack - 1) / kSegBack;
     return n_seqs + (most < 1 ? 1 : most) + 1;
 }
 
 struct Ws {
-    size_t segs, seqs, total, gates, before, after, rows, cols, last, gate, part, all;
+    size_t segs, seqs, total, gates, before, after, rows, cols, last, first, ends, gate, part, all;
 };
 Ws layout(const gdnl_dims* d, int64_t slots, int64_t n_seqs, int64_t n_rows, bool backward) {
     Ws w{};
@@ -104,6 +117,8 @@ Ws layout(const gdnl_dims* d, int64_t slots, int64_t n_seqs, int64_t n_rows, boo
         w.rows = take(H * (size_t)n_rows * sizeof(float));
         w.cols = take(H * (size_t)n_rows * sizeof(float));
         w.last = take((size_t)n_seqs * H * size * sizeof(float));
+        w.first = take((size_t)n_seqs * H * size * sizeof(float));
+        w.ends = take((size_t)(slots + n_seqs) * H * sizeof(double));
         w.gate = take((size_t)slots * H * sizeof(double));
         if (d->h_k != d->h_v) w.part = take((size_t)n_rows * H * (size_t)d->d_k * sizeof(float));
     }
@@ -130,11 +145,12 @@ struct Plan {
     int64_t len, slots, segments;  // rows of a segment; segments of the call and, at most, of a sequence
     bool split;  // sequences may have several segments
 };
-Plan plan_of(const gdnl_dims* d, const gdn_batch* b) {
+Plan plan_of(const gdnl_dims* d, const gdn_batch* b, bool backward) {
     Plan p;
-    p.len = seg_rows(b->n_rows, d->h_v);
+    p.len = seg_rows(b->n_rows, d, backward);
     const int64_t most = b->max_seqlen > 0 && b->max_seqlen < b->n_rows ? b->max_seqlen : b->n_rows;  // rows of a sequence
-    p.split = most > p.len && most > kSegNone;
+    const int64_t whole = (int64_t)b->n_seqs * d->h_v < kSegFew ? kSegFewNone : kSegNone;
+    p.split = most > p.len && most > whole;
     if (!p.split) p.len = kSegWhole;
     p.slots = slots_of(b->n_seqs, b->n_rows, p.len);
     p.segments = (most + p.len - 1) / p.len;
@@ -149,7 +165,7 @@ GDN_EXPORT int32_t gdnl_attend_workspace_bytes(const gdnl_dims* dims, int32_t n_
     if ((st = check_dims(dims)) != GDN_OK) return st;
     if (!out_bytes || n_seqs < 0 || n_seqs > (1 << 28) || (backward != 0 && backward != 1)) return GDN_ERR_ARG;
     if ((st = check_rows(n_rows)) != GDN_OK) return st;
-    const int64_t slots = most_slots(n_seqs, n_rows, dims->h_v);
+    const int64_t slots = most_slots(n_seqs, n_rows, dims->h_v, backward != 0);
     if (slots * dims->h_v > kMaxGroups) return GDN_ERR_ARG;
     *out_bytes = layout(dims, slots, n_seqs, n_rows, backward != 0).all;
     return GDN_OK;
@@ -189,7 +205,7 @@ GDN_EXPORT int32_t gdnl_attend_forward(const gdnl_dims* dims, const void* q, int
                 rows_on(state_out.base, state_out.page_stride, dims->d_v, dims->state_dtype, four);
         return from_hip(gdnl::launch_tokens(A, s));
     }
-    const Plan p = plan_of(dims, batch);
+    const Plan p = plan_of(dims, batch, false);
     if (p.slots * H > kMaxGroups) return GDN_ERR_ARG;
     const Ws w = layout(dims, p.slots, batch->n_seqs, batch->n_rows, false);
     if (!workspace || !aligned(workspace, 256) || ws_bytes < w.all) return GDN_ERR_ARG;
@@ -255,7 +271,7 @@ GDN_EXPORT int32_t gdnl_attend_backward(const gdnl_dims* dims, const void* q, in
          !rows_ok(d_o, do_stride, wv, dt) || !rows_ok(dq, dq_stride, wk, dt) || !rows_ok(dk, dk_stride, wk, dt) ||
          !rows_ok(dv, dv_stride, wv, dt) || !g || !aligned(g, 4)))
         return GDN_ERR_ARG;
-    const Plan p = plan_of(dims, batch);
+    const Plan p = plan_of(dims, batch, true);
     if (p.slots * H > kMaxGroups) return GDN_ERR_ARG;
     const Ws w = layout(dims, p.slots, batch->n_seqs, batch->n_rows, true);
     if (!workspace || !aligned(workspace, 256) || ws_bytes < w.all) return GDN_ERR_ARG;
@@ -342,13 +358,15 @@ GDN_EXPORT int32_t gdnl_attend_backward(const gdnl_dims* dims, const void* q, in
     A.q = rk; A.k = rq; A.v = ro;
     A.dk = dims->d_k; A.dv = dims->d_v;
     A.in = p.split ? dense(dims, after, gdnl::kBySlot) : ends;
-    A.out = dense(dims, d_state0, gdnl::kBySeq);
+    float* const first = dg && !d_state0 ? reinterpret_cast<float*>(ws + w.first) : d_state0;
+    A.out = dense(dims, first, gdnl::kBySeq);
     A.zero_uninit = 1;
     A.o = dv; A.o_stride = dv_stride; A.o_f32 = dt == GDN_F32;
     if ((e = gdnl::launch_attend(A, gdnl::kAttend, true, dt == GDN_BF16, s)) != hipSuccess) return from_hip(e);
     if (!dg) return GDN_OK;
-    gdnl::GateArgs T{G.segs, p.slots, batch->n_rows, H, size, g, g_stride, rows, cols, before, after, last, d_state, dg,
-                     one_decay ? reinterpret_cast<double*>(ws + w.gate) : nullptr};
+    gdnl::GateArgs T{G.segs, p.slots, batch->n_rows, H, size, g, g_stride, rows, cols, before, after, last, d_state,
+                     G.seqs, batch->page_idx, batch->has_init, batch->n_seqs, pages_of(dims, state_in), first,
+                     reinterpret_cast<double*>(ws + w.ends), dg, one_decay ? reinterpret_cast<double*>(ws + w.gate) : nullptr};
     if ((e = gdnl::launch_gate(T, s)) != hipSuccess || !one_decay) return from_hip(e);
     return from_hip(gdnl::launch_gate_sum(T.part, p.slots, H, dg, s));
 }

@@ -52,8 +52,8 @@ struct States {
 };
 
 // For every row and head, G the inclusive sum of g log2(e) within the row's
-// chunk of its segment: {G, what G's float leaves of it, e^G, e^{G_C - G}}, and
-// for every segment the sum over its rows.
+// chunk of its segment: {G, what G's float leaves of it, e^G, e^{G_C - G}},
+// e^{G_C} at a chunk's last row, and for every segment the sum over its rows.
 struct DecayArgs {
     const SegWord* segs; int64_t n_slots, n_rows;
     int32_t heads;
@@ -117,6 +117,10 @@ struct GateArgs {
     const float* rows; const float* cols;          // [heads][n_rows]
     const float* before; const float* after;       // [slot][heads][size], NULL: one segment to a sequence
     const float* last; const float* d_state;       // [seq][heads][size]; d_state NULL: X is 0 at a sequence's end
+    const SeqSlots* seqs; const int32_t* page_idx; const uint8_t* has_init;
+    int32_t n_seqs; States start;                  // the pages, and
+    const float* first;                            // [seq][heads][size]: their gradient
+    double* ends;                                  // [slot, then seq][heads]
     float* dg;                                     // [n_rows][heads], or with g_stride 0:
     double* part;                                  // [slot][heads]
 };

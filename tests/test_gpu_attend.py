@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from gpu_util import DEV, gdn, host
-from linear_util import Case
+from linear_util import HALF32, Case
 
 pytestmark = pytest.mark.gpu
 
@@ -77,6 +77,59 @@ def test_several_segments_with_padding_and_fresh_states():
     o, so = c.forward()
     c.check_forward(o, so)
     c.check_backward(c.backward())
+
+
+SHORT = [
+    dict(dk=128, dv=128, hk=1, hv=2, act="bf16"),
+    dict(dk=40, dv=72, hk=1, hv=3, act="bf16", state="bf16"),
+    dict(dk=31, dv=33, hk=1, hv=1, pad=3, offset=1),
+    dict(dk=48, dv=16, hk=1, hv=2, pad=5, offset=3, act="bf16"),
+    dict(dk=72, dv=24, hk=3, hv=3, decay="head"),
+    dict(fast=60.0, act="bf16"),
+    dict(skip=(2,), gap=5, tail=9, has_init=[1, 0, 1, 0], act="bf16", fast=0.02),
+]
+
+
+@pytest.mark.parametrize("shape", SHORT, ids=[",".join(f"{k}={v}" for k, v in s.items()) for s in SHORT])
+def test_short_segments(shape):
+    """Few sequences and heads: cut from 513 rows on."""
+    c = Case([513, 0, 128, 640], **{"fast": 0.3, **shape})
+    o, so = c.forward()
+    c.check_forward(o, so)
+    c.check_backward(c.backward())
+
+
+@pytest.mark.parametrize("rows", [1025, 17000])
+def test_many_segments(rows):
+    """More segments than a wave, and than a workgroup, joins in a round."""
+    c = Case([rows, 3], hk=1, hv=1, dk=8, dv=8, fast=0.01)
+    o, so = c.forward()
+    c.check_forward(o, so)
+    c.check_backward(c.backward())
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("lens", [[70, 300], [700, 1100]])
+def test_gate_gradients_end_at_the_initial_state(act, lens):
+    """The first decay's gradient is <S_0, d_state0>: its walk is held there.
+
+    Both are sums over d_k d_v products in 64 bits, so what is left is the
+    rounding of the result, and 2^-40 of the absolute sums for that of the
+    walk.  It is 0 where the sequence begins with zeros, and the same whether
+    d_state0 is asked for or not."""
+    g = gdn()
+    c = Case(lens, act=act, has_init=[1, 0], fast=0.1)
+    got = c.backward()
+    first = int(host(c.batch.cu_seqlens)[0]), int(host(c.batch.cu_seqlens)[1])
+    s0, d0 = c.s0.double().numpy()[c.pages[0]], host(got.d_state0)[0]
+    want, size = (s0 * d0).sum((1, 2)), np.abs(s0 * d0).sum((1, 2))
+    assert (np.abs(host(got.dg)[first[0]] - want) <= HALF32 * np.abs(want) + 2.0 ** -40 * (size + np.abs(host(got.dg)).max())).all()
+    assert (np.abs(host(got.dg)[first[1]]) <= 2.0 ** -40 * np.abs(host(got.dg)).max()).all()
+    bare = g.gdnl_attend_backward(c.dims, c.t["q"], c.t["k"], c.t["v"], c.g, c.batch, g.StatePool(c.s0.to(DEV)), c.t["d_o"],
+                                  d_state=torch.from_numpy(c.d_state).to(DEV),
+                                  out=g.LinearGrads(c.blank("q"), c.blank("k"), c.blank("v"), torch.zeros_like(got.dg), None))
+    torch.cuda.synchronize()
+    assert bare.d_state0 is None and torch.equal(bare.dg, got.dg)
 
 
 @pytest.mark.parametrize("rows", [1, 3, 8])
