@@ -388,9 +388,12 @@ template <typename T, int DK, int W, int NT, int MODE, bool BACK> struct Layout 
     static constexpr int oDot = oBad + (kGuard ? DV * 8 + 16 : 0);
     static constexpr int oSum = oDot + (kX ? W * 64 * 4 : 0);
     static constexpr int kBytes = oSum + (MODE == kDotRows ? 64 * 4 * 4 : 0);
-    // Waves on a SIMD that the registers are cut for: what LDS has room for, four at most.
+    // Waves on a SIMD that the registers are cut for: what LDS has room for, four at
+    // most; two for local sums of fp32 rows, which spill with four (16384 rows of 32
+    // heads of 128 x 128: 189 us against 317).
     static constexpr int kRoom = 160 * 1024 / kBytes * W / 4;
-    static constexpr int kWavesPerSimd = kRoom < 1 ? 1 : kRoom > 4 ? 4 : kRoom;
+    static constexpr int kMost = sizeof(T) == 4 && MODE == kLocal ? 2 : 4;
+    static constexpr int kWavesPerSimd = kRoom < 1 ? 1 : kRoom > kMost ? kMost : kRoom;
 };
 
 // The state's rows 16 m + 4 g + r of one column, `at` from each other by rs;
