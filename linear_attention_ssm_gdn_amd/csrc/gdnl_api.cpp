@@ -26,8 +26,10 @@ constexpr int64_t kSegGroups = 512;
 // Batches whose longest sequence has at most kSegNone rows are not cut, the states
 // between segments costing two more launches and another reading of k and v; where
 // sequences times heads are fewer than kSegFew, batches of at most kSegFewNone
-// (900 rows of 8 heads 87 us uncut and 42 cut, 4 x 1000 rows of 32 heads 104 and 132).
-constexpr int32_t kSegNone = 1024, kSegFewNone = 512;
+// (900 rows of 8 heads 87 us uncut and 42 cut, 4 x 1000 rows of 32 heads 104 and
+// 132), and fewer than twice as many for fp32 rows, whose chunks take longer (4 x
+// 1000 rows of 32 heads 240 uncut and 205 cut, 8 prompts of up to 656 172 and 211).
+constexpr int32_t kSegNone = 1024, kSegFewNone = 256;
 constexpr int64_t kSegFew = 128;
 // A backward pass takes no longer ones: the gradients of the decays are sums over
 // the rows to a segment's ends, whose rounding grows with them.
@@ -149,7 +151,7 @@ Plan plan_of(const gdnl_dims* d, const gdn_batch* b, bool backward) {
     Plan p;
     p.len = seg_rows(b->n_rows, d, backward);
     const int64_t most = b->max_seqlen > 0 && b->max_seqlen < b->n_rows ? b->max_seqlen : b->n_rows;  // rows of a sequence
-    const int64_t whole = (int64_t)b->n_seqs * d->h_v < kSegFew ? kSegFewNone : kSegNone;
+    const int64_t whole = (int64_t)b->n_seqs * d->h_v < (d->act_dtype == GDN_F32 ? 2 * kSegFew : kSegFew) ? kSegFewNone : kSegNone;
     p.split = most > p.len && most > whole;
     if (!p.split) p.len = kSegWhole;
     p.slots = slots_of(b->n_seqs, b->n_rows, p.len);
