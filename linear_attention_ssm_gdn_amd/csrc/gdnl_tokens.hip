@@ -6,7 +6,8 @@
 // all of a head's 64 KB are asked for before the first is used.  A row costs
 //   S <- e^g S + k v^T,  o = scale S^T q,
 // each lane its 16 rows, then a sum over the eight row groups through LDS.
-// Bound by the state's bytes, read and written once.
+// Bound by the state's bytes, read and written once: 64 sequences of 32 heads of
+// 128 x 128 in fp32 take 47 us, 268 MB at 5.7 TB/s.
 #include "gdn_device.hpp"
 #include "gdnl_kernels.h"
 #include "gdnt_device.hpp"
