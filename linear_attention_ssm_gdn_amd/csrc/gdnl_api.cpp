@@ -35,7 +35,7 @@ constexpr int64_t kSegFew = 128;
 // the rows to a segment's ends, whose rounding grows with them.
 constexpr int64_t kSegBack = 2048;
 constexpr int32_t kSegWhole = INT32_MAX;  // every sequence is one segment
-constexpr int64_t kMaxGroups = 1 << 24;  // 256 threads each: HIP launches fewer than 2^32 threads
+constexpr int64_t kMaxGroups = (1 << 23) - 1;  // of 512 threads: HIP launches fewer than 2^32 threads
 
 int64_t elem_size(int32_t dt) { return dt == GDN_BF16 ? 2 : 4; }
 bool dtype_ok(int32_t dt) { return dt == GDN_F32 || dt == GDN_BF16; }
@@ -95,6 +95,11 @@ int64_t most_slots(int64_t n_seqs, int64_t n_rows, int64_t heads, bool backward)
     int64_t most = by_rows < by_groups ? by_rows : by_groups;
     if (backward && most < (n_rows + kSegBack - 1) / kSegBack) most = (n_rows + kSegBack - 1) / kSegBack;
     return n_seqs + (most < 1 ? 1 : most) + 1;
+}
+
+// The chunked kernels' grid, rounded up to whole key heads on every XCD, is beyond a launch.
+bool too_many(int64_t slots, const gdnl_dims* d) {
+    return slots * d->h_v + 7 * (int64_t)(d->h_v / d->h_k) > kMaxGroups;
 }
 
 struct Ws {
@@ -168,7 +173,7 @@ GDN_EXPORT int32_t gdnl_attend_workspace_bytes(const gdnl_dims* dims, int32_t n_
     if (!out_bytes || n_seqs < 0 || n_seqs > (1 << 28) || (backward != 0 && backward != 1)) return GDN_ERR_ARG;
     if ((st = check_rows(n_rows)) != GDN_OK) return st;
     const int64_t slots = most_slots(n_seqs, n_rows, dims->h_v, backward != 0);
-    if (slots * dims->h_v > kMaxGroups) return GDN_ERR_ARG;
+    if (too_many(slots, dims)) return GDN_ERR_ARG;
     *out_bytes = layout(dims, slots, n_seqs, n_rows, backward != 0).all;
     return GDN_OK;
 }
@@ -208,7 +213,7 @@ GDN_EXPORT int32_t gdnl_attend_forward(const gdnl_dims* dims, const void* q, int
         return from_hip(gdnl::launch_tokens(A, s));
     }
     const Plan p = plan_of(dims, batch, false);
-    if (p.slots * H > kMaxGroups) return GDN_ERR_ARG;
+    if (too_many(p.slots, dims)) return GDN_ERR_ARG;
     const Ws w = layout(dims, p.slots, batch->n_seqs, batch->n_rows, false);
     if (!workspace || !aligned(workspace, 256) || ws_bytes < w.all) return GDN_ERR_ARG;
     char* const ws = static_cast<char*>(workspace);
@@ -274,7 +279,7 @@ GDN_EXPORT int32_t gdnl_attend_backward(const gdnl_dims* dims, const void* q, in
          !rows_ok(dv, dv_stride, wv, dt) || !g || !aligned(g, 4)))
         return GDN_ERR_ARG;
     const Plan p = plan_of(dims, batch, true);
-    if (p.slots * H > kMaxGroups) return GDN_ERR_ARG;
+    if (too_many(p.slots, dims)) return GDN_ERR_ARG;
     const Ws w = layout(dims, p.slots, batch->n_seqs, batch->n_rows, true);
     if (!workspace || !aligned(workspace, 256) || ws_bytes < w.all) return GDN_ERR_ARG;
     char* const ws = static_cast<char*>(workspace);

@@ -26,12 +26,13 @@
 //
 // What bounds it: issue.  Over 4 x 8192 rows of 32 heads of 128 x 128 in bf16 the
 // outputs take 290-320 us, some 660 vector and 98 matrix instructions a wave and
-// chunk, busy 62% and 37% of the time; the 0.93 GB would take 180 us at a copy's rate.  fp32 rows are bound by the matrix instructions (68% busy, 85
-// TFLOP/s over 16384 rows).  Why eight waves of 16 columns: two workgroups then
-// fit a compute unit's registers (128 a lane) and LDS, and one computes while the other
-// waits at a barrier; four waves of 32 columns were no faster.  Chunks of 64 rows:
-// with 32 the work on the state would come twice as often, with 128 two workgroups
-// would not fit LDS.
+// chunk, busy 62% and 37% of the time; the 0.93 GB would take 180 us at a copy's
+// rate.  fp32 rows are bound by the matrix instructions (68% busy, 85 TFLOP/s over
+// 16384 rows).  Why eight waves of 16 columns: two workgroups then fit a compute
+// unit's registers (128 a lane) and LDS, and one computes while the other waits at
+// a barrier; four waves of 32 columns were no faster.  Chunks of 64 rows: with 32
+// the work on the state would come twice as often, with 128 two workgroups would
+// not fit LDS.
 #pragma once
 
 #include "gdn_device.hpp"

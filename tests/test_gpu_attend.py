@@ -353,6 +353,24 @@ def test_rows_beyond_4_gb(max_len):
         assert torch.equal(o[r0:r0 + n], want) and torch.equal(pool.buf[p], small.buf[0])
 
 
+@pytest.mark.parametrize("hv", [1, 8, 48, 600])
+def test_a_larger_batchs_workspace_serves_smaller_ones(hv):
+    """Segments are cut by rows and heads: any batch of fewer rows needs no more, and gives the same bits."""
+    g = gdn()
+    dims = g.LinearDims(1, hv, 8, 8, act_dtype="f32")
+    most = 9000 if hv < 600 else 1200
+    spaces = [torch.empty(g.gdnl_attend_workspace_bytes(dims, 3, most, backward=b), dtype=torch.uint8, device=DEV) for b in (False, True)]
+    for rows in (1, 129, 257, 513, 1025, 2049, 4097, most):
+        if rows > most:
+            continue
+        c = Case([rows, 0, 0], hk=1, hv=hv, dk=8, dv=8, fast=0.1)
+        o, so = c.forward(workspace=spaces[0])
+        o2, so2 = c.forward()
+        assert torch.equal(o, o2) and torch.equal(so.buf.nan_to_num(1), so2.buf.nan_to_num(1))
+        for a, b in zip(c.backward(workspace=spaces[1]), c.backward()):
+            assert torch.equal(a, b)
+
+
 def test_many_sequences_and_an_empty_batch():
     g = gdn()
     c = Case([1, 0, 2] * 700, hk=1, hv=2, dk=8, dv=8)

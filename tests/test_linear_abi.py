@@ -131,6 +131,23 @@ def test_forward_refusals(so, L):
     assert _call(so, L, False, batch=B(None, None, None, 0, 0, 300), q=None, ws=None) == 0  # no sequence at all
 
 
+def test_more_workgroups_than_a_launch_has(so, L):
+    """2^32 threads are too many: 2^23 workgroups of 512, those counted that round a key head's values up to every XCD."""
+    B, out = L.GdnBatch, ctypes.c_size_t()
+    for hk, hv, n, status in ((1, 1 << 16, 127, 1), (1, 1 << 16, 200, 1), (1 << 16, 1 << 16, 127, 1), (1 << 16, 1 << 16, 120, 0)):
+        d = _dims(L, hk=hk, hv=hv, dk=1, dv=1)
+        for back in (0, 1):
+            assert so.gdnl_attend_workspace_bytes(ctypes.byref(d), n, 100, back, ctypes.byref(out)) == status
+        if status == 0:
+            continue
+        S = L.GdnStatePool
+        for back in (False, True):
+            assert _call(so, L, back, dims=d, qs=hk, ks=hk, vs=hv, os=hv, dqs=hk, dks=hk, dvs=hv, gs=hv, si=S(FAKE, hv, 4),
+                         sto=S(FAKE, hv, 4), batch=B(FAKE, FAKE, None, n, 0, 100)) == 1
+    d = _dims(L)
+    assert _call(so, L, False, batch=B(FAKE, FAKE, None, 1 << 21, 1, 300)) == 1  # row by row, a workgroup to a sequence and head
+
+
 def test_backward_refusals(so, L):
     B = L.GdnBatch
     for kw in _bad(L) + [dict(dq=None), dict(dk=None), dict(dv=None), dict(dqs=31), dict(dks=31), dict(dvs=127),
