@@ -206,7 +206,7 @@ def test_gradients_of_skipped_and_empty_sequences():
 
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
-@pytest.mark.parametrize("rows,max_len", [(100, 0), (8, 8)])
+@pytest.mark.parametrize("rows,max_len", [(100, 0), (8, 8), (700, 0)])
 def test_a_decay_of_zero_begins_anew(act, rows, max_len):
     for low in (-np.inf, -1e30, -200.0):
         c = Case([rows], act=act, max_len=max_len, fast=0.3)
@@ -223,7 +223,7 @@ def test_a_decay_of_zero_begins_anew(act, rows, max_len):
 
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), "max"])
-@pytest.mark.parametrize("rows,max_len", [(150, 0), (8, 8)])
+@pytest.mark.parametrize("rows,max_len", [(150, 0), (8, 8), (700, 0)])
 def test_what_is_not_finite_reaches_its_column_from_its_row_on(act, bad, rows, max_len):
     at = 100 if rows > 100 else 4
     clean = Case([rows, 20 if not max_len else 5], act=act, max_len=max_len)
