@@ -118,7 +118,7 @@ def _check_pool(name: str, pool: StatePool, dims: LinearDims) -> None:
     t = pool.buf
     shape = (dims.h_v, dims.d_k, dims.d_v)
     if t.dtype is not _TORCH_DT[dims.state_dtype] or t.dim() != 4 or t.shape[1:] != shape or \
-            (t.shape[0] > 0 and not t[0].is_contiguous()):
+            not (t.is_contiguous() or t.shape[0] == 0 or t[0].is_contiguous()):  # t[0] costs 2 us
         raise ValueError(f"{name} must be [pages]{list(shape)} of {_TORCH_DT[dims.state_dtype]}, a page contiguous")
 
 
@@ -141,6 +141,15 @@ def _space(ws: Optional[torch.Tensor], size: int, dev: torch.device) -> torch.Te
     return ws
 
 
+def _rows_out(name: str, t: Optional[torch.Tensor], like: torch.Tensor, rows: int, cols: int, dt: torch.dtype,
+              dev: torch.device) -> tuple:
+    """An output of [rows][cols] and its row stride: the caller's, checked, or a new one like `like`, checked before."""
+    if t is None:
+        return like.new_empty((rows, cols)), cols
+    _on(dev, **{name: t})
+    return t, _rows2(name, t, rows, cols, dt)
+
+
 def gdnl_attend_forward(dims: LinearDims, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor,
                         batch: Batch, state_in: StatePool, state_out: Optional[StatePool] = None,
                         o: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
@@ -154,15 +163,14 @@ def gdnl_attend_forward(dims: LinearDims, q: torch.Tensor, k: torch.Tensor, v: t
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or g.requires_grad or
                                     state_in.buf.requires_grad):
         _no_history("gdnl_attend_forward")
-    if o is None:
-        o = torch.empty((n, wv), dtype=dt, device=dev)
-    _on(dev, k=k, v=v, g=g, o=o, state_in=state_in.buf, state_out=state_out.buf, err=err)
+    _on(dev, k=k, v=v, g=g, state_in=state_in.buf, state_out=state_out.buf, err=err)
     _check_batch(batch, dev)
     _check_pool("state_in", state_in, dims)
     if state_out is not state_in:
         _check_pool("state_out", state_out, dims)
     qs, ks = _rows2("q", q, n, wk, dt), _rows2("k", k, n, wk, dt)
-    vs, os_ = _rows2("v", v, n, wv, dt), _rows2("o", o, n, wv, dt)
+    vs = _rows2("v", v, n, wv, dt)
+    o, os_ = _rows_out("o", o, v, n, wv, dt, dev)
     gs = _gates(g, n, dims.h_v)
     if workspace is None and 0 < batch.max_seqlen <= 8:
         ws, ws_bytes = None, 0  # row by row
@@ -191,21 +199,21 @@ def gdnl_attend_backward(dims: LinearDims, q: torch.Tensor, k: torch.Tensor, v: 
     state = (s, dims.h_v, dims.d_k, dims.d_v)
     if torch.is_grad_enabled() and (d_o.requires_grad or (d_state is not None and d_state.requires_grad)):
         _no_history("gdnl_attend_backward")
-    if out is None:
-        f32 = {"dtype": torch.float32, "device": dev}
-        out = LinearGrads(torch.empty((n, wk), dtype=dt, device=dev), torch.empty((n, wk), dtype=dt, device=dev),
-                          torch.empty((n, wv), dtype=dt, device=dev),
-                          torch.empty((dims.h_v,) if one else (n, dims.h_v), **f32) if with_dg else None,
-                          torch.empty(state, **f32))
-    _on(dev, k=k, v=v, g=g, d_o=d_o, d_state=d_state, state_in=state_in.buf, err=err, **out._asdict())
+    _on(dev, k=k, v=v, g=g, d_o=d_o, d_state=d_state, state_in=state_in.buf, err=err)
     _check_batch(batch, dev)
     _check_pool("state_in", state_in, dims)
     qs, ks, vs = _rows2("q", q, n, wk, dt), _rows2("k", k, n, wk, dt), _rows2("v", v, n, wv, dt)
     os_, gs = _rows2("d_o", d_o, n, wv, dt), _gates(g, n, dims.h_v)
-    dqs, dks, dvs = _rows2("dq", out.dq, n, wk, dt), _rows2("dk", out.dk, n, wk, dt), _rows2("dv", out.dv, n, wv, dt)
     _flat("d_state", d_state, state, torch.float32)
-    _flat("dg", out.dg, (dims.h_v,) if one else (n, dims.h_v), torch.float32)
-    _flat("d_state0", out.d_state0, state, torch.float32)
+    if out is None:
+        out = LinearGrads(q.new_empty((n, wk)), q.new_empty((n, wk)), q.new_empty((n, wv)),
+                          g.new_empty((dims.h_v,) if one else (n, dims.h_v)) if with_dg else None, g.new_empty(state))
+        dqs, dks, dvs = wk, wk, wv
+    else:
+        _on(dev, **out._asdict())
+        dqs, dks, dvs = _rows2("dq", out.dq, n, wk, dt), _rows2("dk", out.dk, n, wk, dt), _rows2("dv", out.dv, n, wv, dt)
+        _flat("dg", out.dg, (dims.h_v,) if one else (n, dims.h_v), torch.float32)
+        _flat("d_state0", out.d_state0, state, torch.float32)
     space = _space(workspace, 0 if workspace is not None else gdnl_attend_workspace_bytes(dims, s, n, True), dev)
     d, bt = dims.c(), batch.c()
     _call("gdnl_attend_backward", dev,
@@ -236,12 +244,8 @@ def gdnl_rotate_forward(dims: RotateDims, q: torch.Tensor, k: torch.Tensor, wq: 
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, wq, wk)):
         _no_history("gdnl_rotate_forward")
     n, dt, dev, qs, ks = _rotate_inputs(dims, q, k, wq, wk, pos, inv_freq)
-    if yq is None:
-        yq = torch.empty((n, dims.h_q * dims.d), dtype=dt, device=dev)
-    if yk is None:
-        yk = torch.empty((n, dims.h_k * dims.d), dtype=dt, device=dev)
-    _on(dev, yq=yq, yk=yk)
-    yqs, yks = _rows2("yq", yq, n, dims.h_q * dims.d, dt), _rows2("yk", yk, n, dims.h_k * dims.d, dt)
+    yq, yqs = _rows_out("yq", yq, q, n, dims.h_q * dims.d, dt, dev)
+    yk, yks = _rows_out("yk", yk, q, n, dims.h_k * dims.d, dt, dev)
     d = dims.c()
     _call("gdnl_rotate_forward", dev, ctypes.byref(d), q.data_ptr(), qs, k.data_ptr(), ks, _p(wq), _p(wk), _p(pos),
           _p(inv_freq), n, yq.data_ptr(), yqs, yk.data_ptr(), yks)
@@ -259,15 +263,17 @@ def gdnl_rotate_backward(dims: RotateDims, q: torch.Tensor, k: torch.Tensor, wq:
         _no_history("gdnl_rotate_backward")
     n, dt, dev, qs, ks = _rotate_inputs(dims, q, k, wq, wk, pos, inv_freq)
     nq, nk = dims.h_q * dims.d, dims.h_k * dims.d
-    if out is None:
-        w = lambda t: torch.empty(dims.d, dtype=torch.float32, device=dev) if t is not None else None  # noqa: E731
-        out = RotateGrads(torch.empty((n, nq), dtype=dt, device=dev), torch.empty((n, nk), dtype=dt, device=dev), w(wq),
-                          w(wk))
-    _on(dev, d_yq=d_yq, d_yk=d_yk, **out._asdict())
+    _on(dev, d_yq=d_yq, d_yk=d_yk)
     yqs, yks = _rows2("d_yq", d_yq, n, nq, dt), _rows2("d_yk", d_yk, n, nk, dt)
-    dqs, dks = _rows2("dq", out.dq, n, nq, dt), _rows2("dk", out.dk, n, nk, dt)
-    _flat("dwq", out.dwq, (dims.d,), torch.float32)
-    _flat("dwk", out.dwk, (dims.d,), torch.float32)
+    if out is None:
+        out = RotateGrads(q.new_empty((n, nq)), q.new_empty((n, nk)), None if wq is None else wq.new_empty(dims.d),
+                          None if wk is None else wk.new_empty(dims.d))
+        dqs, dks = nq, nk
+    else:
+        _on(dev, **out._asdict())
+        dqs, dks = _rows2("dq", out.dq, n, nq, dt), _rows2("dk", out.dk, n, nk, dt)
+        _flat("dwq", out.dwq, (dims.d,), torch.float32)
+        _flat("dwk", out.dwk, (dims.d,), torch.float32)
     space = _space(workspace, 0 if workspace is not None else gdnl_rotate_workspace_bytes(dims, n), dev)
     d = dims.c()
     _call("gdnl_rotate_backward", dev, ctypes.byref(d), q.data_ptr(), qs, k.data_ptr(), ks, _p(wq), _p(wk), _p(pos),
