@@ -223,8 +223,7 @@ GDN_EXPORT int32_t gdnl_attend_forward(const gdnl_dims* dims, const void* q, int
     G.segs = reinterpret_cast<gdnl::SegWord*>(ws + w.segs);
     G.seqs = reinterpret_cast<gdnl::SeqSlots*>(ws + w.seqs);
     G.err = err;
-    hipError_t e = gdnl::launch_segments(G, s);
-    if (e != hipSuccess || batch->n_rows == 0) return from_hip(e);
+    if (batch->n_rows == 0) return from_hip(gdnl::launch_segments(G, s));
     float* const before = reinterpret_cast<float*>(ws + w.before);
     double* const total = reinterpret_cast<double*>(ws + w.total);
 
@@ -240,7 +239,8 @@ GDN_EXPORT int32_t gdnl_attend_forward(const gdnl_dims* dims, const void* q, int
     A.f_p = A.f_i = dims->scale; A.f_u = 1.0f;
     A.gates = reinterpret_cast<const float4*>(ws + w.gates);
     gdnl::DecayArgs D{G.segs, p.slots, batch->n_rows, H, g, g_stride, reinterpret_cast<float4*>(ws + w.gates), total};
-    if ((e = gdnl::launch_decays(D, s)) != hipSuccess) return from_hip(e);
+    hipError_t e = gdnl::launch_segments_decays(G, D, s);
+    if (e != hipSuccess) return from_hip(e);
     if (p.split) {
         A.out = dense(dims, before, gdnl::kBySlot);
         if ((e = gdnl::launch_attend(A, gdnl::kLocal, false, dt == GDN_BF16, s)) != hipSuccess) return from_hip(e);
@@ -291,9 +291,11 @@ GDN_EXPORT int32_t gdnl_attend_backward(const gdnl_dims* dims, const void* q, in
     G.seqs = reinterpret_cast<gdnl::SeqSlots*>(ws + w.seqs);
     G.pass_src = d_state; G.pass_dst = d_state0; G.pass_width = (int64_t)H * size;
     G.err = err;
-    hipError_t e = gdnl::launch_segments(G, s);
-    if (e != hipSuccess) return from_hip(e);
-    if (batch->n_rows == 0) return dg && one_decay ? from_hip(gdnl::launch_gate_sum(nullptr, 0, H, dg, s)) : GDN_OK;
+    hipError_t e = hipSuccess;
+    if (batch->n_rows == 0) {
+        e = gdnl::launch_segments(G, s);
+        return e == hipSuccess && dg && one_decay ? from_hip(gdnl::launch_gate_sum(nullptr, 0, H, dg, s)) : from_hip(e);
+    }
     float* const before = reinterpret_cast<float*>(ws + w.before);
     float* const after = reinterpret_cast<float*>(ws + w.after);
     float* const rows = reinterpret_cast<float*>(ws + w.rows);
@@ -312,7 +314,7 @@ GDN_EXPORT int32_t gdnl_attend_backward(const gdnl_dims* dims, const void* q, in
     A.has_init = batch->has_init; A.heads = H; A.per = per;
     A.gates = reinterpret_cast<const float4*>(ws + w.gates);
     gdnl::DecayArgs D{G.segs, p.slots, batch->n_rows, H, g, g_stride, reinterpret_cast<float4*>(ws + w.gates), total};
-    if ((e = gdnl::launch_decays(D, s)) != hipSuccess) return from_hip(e);
+    if ((e = gdnl::launch_segments_decays(G, D, s)) != hipSuccess) return from_hip(e);
     const gdnl::States ends = dense(dims, d_state, gdnl::kBySeq);
     if (p.split) {
         // S in front of every segment, then its gradient behind every segment

@@ -15,7 +15,7 @@
 // the update.
 //
 // Decays.  G is summed within a chunk in 64 bits and kept as two floats
-// (k_decays, once for all passes), so e^{G_x - G_y} is good to the difference's
+// (decays_of, once for all passes), so e^{G_x - G_y} is good to the difference's
 // own digits; it is set, not multiplied, to zero where y lies ahead of x.
 //
 // Roundings with bf16 rows.  The products of q, k and v themselves are exact.

@@ -33,7 +33,6 @@ struct SegmentArgs {
     // a backward pass hands the gradient of empty sequences through and clears
     // that of skipped ones: `pass_width` values a sequence, NULL src: zeros
     const float* pass_src; float* pass_dst; int64_t pass_width;
-    float* zero; int64_t n_zero;   // floats to clear
     int32_t* err;
 };
 hipError_t launch_segments(const SegmentArgs& a, hipStream_t s);
@@ -61,7 +60,7 @@ struct DecayArgs {
     float4* gates;               // [heads][n_rows]
     double* total;               // [slot][heads]
 };
-hipError_t launch_decays(const DecayArgs& a, hipStream_t s);
+hipError_t launch_segments_decays(const SegmentArgs& s, const DecayArgs& a, hipStream_t stream);
 
 // One pass of linear attention over segments, forward or backward in time.
 // For output row x and source row y of a chunk, y <= x forward, y >= x backward:
@@ -72,7 +71,7 @@ hipError_t launch_decays(const DecayArgs& a, hipStream_t s);
 struct AttendArgs {
     const SegWord* segs; int64_t n_slots;
     Rows q, k, v, x;
-    const float4* gates;         // of launch_decays
+    const float4* gates;         // of launch_segments_decays
     const uint8_t* has_init;
     int32_t dk, dv, heads, per;  // widths of q, k and of v, out; value heads, those to a key head
     float f_p, f_i, f_u;
