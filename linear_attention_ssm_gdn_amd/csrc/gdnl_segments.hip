@@ -69,11 +69,13 @@ struct Batch {
             }
         }
         if (A.pass_dst) {  // gradients of sequences that no kernel behind this one writes
-            for (int s = blockIdx.x; s < A.n_seqs; s += gridDim.x) {
+            const int64_t parts = gridDim.x > A.n_seqs ? gridDim.x / A.n_seqs : 1;  // workgroups to a sequence
+            for (int64_t u = blockIdx.x; u < A.n_seqs * parts; u += gridDim.x) {
+                const int s = (int)(u / parts);
                 const bool ok = live(s);
                 if (ok && A.cu[s] != A.cu[s + 1]) continue;
                 const int64_t at = (int64_t)s * A.pass_width;
-                for (int64_t j = tid; j < A.pass_width; j += kThreads)
+                for (int64_t j = u % parts * kThreads + tid; j < A.pass_width; j += parts * kThreads)
                     A.pass_dst[at + j] = ok && A.pass_src ? A.pass_src[at + j] : 0.0f;
             }
         }
