@@ -19,10 +19,9 @@
 // own digits; it is set, not multiplied, to zero where y lies ahead of x.
 //
 // Roundings with bf16 rows.  The products of q, k and v themselves are exact.
-// What is not a bf16 number is split into terms of eight bits: P into two (2^-16
-// of its value is left, far below the output's 2^-9), S into two for o and three
-// where the gates' gradient needs fp32, and the decayed rows of the state's
-// update into three (nothing is left): a state is as good as its fp32 sum.
+// What is not a bf16 number (P, S, the decayed rows of the state's update) is
+// split into three terms of eight bits, which leave nothing: states are as good
+// as their fp32 sums, outputs as these rounded once.
 //
 // What bounds it: issue.  Over 4 x 8192 rows of 32 heads of 128 x 128 in bf16 the
 // outputs take 290-320 us, some 660 vector and 98 matrix instructions a wave and
@@ -55,12 +54,14 @@ constexpr int kTri = 10;  // tiles of 16 x 16 on or below the diagonal of 64 x 6
 __device__ __forceinline__ int tri(int lo, int hi) { return hi * (hi + 1) / 2 + lo; }
 // P in LDS: for an output tile x, the source tiles 2 ys and 2 ys + 1 side by
 // side, as one operand of a product takes them; six such pairs have a tile on
-// the right side of the diagonal.  In two of them the other half is zeros.
-constexpr int kPairs = 6;
+// the right side of the diagonal.  Two of them have one alone, which stands by
+// itself, the other half of the operand being zeros.
 template <bool BACK> __host__ __device__ constexpr bool is_pair(int x, int ys) { return BACK ? 2 * ys + 1 >= x : 2 * ys <= x; }
+template <bool BACK> __host__ __device__ constexpr bool is_alone(int x, int ys) { return x == 2 * ys + (BACK ? 1 : 0); }
+// In tiles, where a pair stands among the ten.
 template <bool BACK> __host__ __device__ constexpr int pair(int x, int ys) {
     // forward (0,0) (1,0) (2,0) (2,1) (3,0) (3,1), backward (0,0) (0,1) (1,0) (1,1) (2,1) (3,1)
-    return BACK ? (x < 2 ? 2 * x + ys : x + 2) : (x < 2 ? x : 2 * x - 2 + ys);
+    return BACK ? 0x975420 >> 4 * (x < 2 ? 2 * x + ys : x + 2) & 15 : 0x865310 >> 4 * (x < 2 ? x : 2 * x - 2 + ys) & 15;
 }
 
 __device__ __forceinline__ float exp2_hw(float v) { return __builtin_amdgcn_exp2f(v); }
@@ -213,10 +214,14 @@ template <typename T, int W> struct Tile {
             return by_row(t, base, b, ks);
         }
     }
+    // Where four bf16 columns from 4 q on stand in such a tile.
+    static __device__ __forceinline__ int quad(int row, int q) {
+        return row * kRow + (((q >> 3) * 4 + (q & 3)) ^ (row & (kPieces - 1))) * 16 + (q >> 2 & 1) * 8;
+    }
     static __device__ __forceinline__ void put_by_row(char* t, int row, int piece, u32x4 v) {
         if constexpr (sizeof(T) == 2) {
             // columns 8 piece..: quads 2 (piece & 1) and the next of the first or second 16 of 32
-            const int to = row * kRow + (((piece >> 2) * 4 + (piece & 1) * 2) ^ (row & (kPieces - 1))) * 16 + (piece >> 1 & 1) * 8;
+            const int to = quad(row, 2 * piece);
             *reinterpret_cast<u32x2*>(t + to) = u32x2{v.x, v.y};
             *reinterpret_cast<u32x2*>(t + (to ^ 16)) = u32x2{v.z, v.w};
         } else {
@@ -361,7 +366,8 @@ __device__ __forceinline__ void put_rows(const AttendArgs& A, const f32x4 (&o)[4
 }
 
 // A chunk's bf16 rows from LDS, by the threads that later put the same pieces.
-template <int W, int THREADS, bool VEC>
+// QUADS: from where rows are put by row.
+template <int W, int THREADS, bool VEC, bool QUADS>
 __device__ __forceinline__ void flush_rows(const AttendArgs& A, const char* stage, int64_t row0, int head, int n, int tid) {
     using L = Tile<bf16_t, W>;
     constexpr int kMine = kChunk * L::kPieces / THREADS;
@@ -369,7 +375,14 @@ __device__ __forceinline__ void flush_rows(const AttendArgs& A, const char* stag
 #pragma unroll
     for (int k = 0; k < kMine; ++k) {
         const int idx = tid + k * THREADS, row = idx / L::kPieces, c = idx % L::kPieces * L::kElems;
-        const u32x4 v = *reinterpret_cast<const u32x4*>(stage + L::place(row, idx % L::kPieces));
+        u32x4 v;
+        if constexpr (QUADS) {
+            const int to = L::quad(row, 2 * (idx % L::kPieces));
+            const u32x2 lo = *reinterpret_cast<const u32x2*>(stage + to), hi = *reinterpret_cast<const u32x2*>(stage + (to ^ 16));
+            v = u32x4{lo.x, lo.y, hi.x, hi.y};
+        } else {
+            v = *reinterpret_cast<const u32x4*>(stage + L::place(row, idx % L::kPieces));
+        }
         const uint32_t at = ((uint32_t)row * (uint32_t)A.o_stride + (uint32_t)c) * 2u;
         if constexpr (VEC) {
             __builtin_amdgcn_raw_buffer_store_b128(v, rs, c < A.dv ? at : kNowhere, 0, 0);
@@ -384,27 +397,34 @@ __device__ __forceinline__ void flush_rows(const AttendArgs& A, const char* stag
 
 template <typename T, int DK, int W, int NT, int MODE, bool BACK> struct Layout {
     static constexpr int DV = 16 * W * NT;
-    static constexpr int kTermsP = sizeof(T) == 2 ? 2 : 1;
-    static constexpr int kTermsV = sizeof(T) == 2 ? 3 : 1;
-    static constexpr int kTermsS = sizeof(T) == 4 ? 1 : MODE == kAttend ? 2 : 3;
-    static constexpr int kPPair = 64 * 8 * (int)sizeof(T);  // of one term
+    static constexpr int kTerms = sizeof(T) == 2 ? 3 : 1;     // of P, S and the decayed v: all 24 bits
+    static constexpr int kPTile = 64 * 4 * (int)sizeof(T);    // of one term
+    static constexpr int kPTerm = kTri * kPTile;
     static constexpr bool kX = MODE == kDot || MODE == kDotRows;
+    static constexpr bool kStage = sizeof(T) == 2 && MODE != kLocal;
     static constexpr int oK = 0;
     static constexpr int oV = oK + Tile<T, DK>::kBytes;
     static constexpr int oQ = oV + Tile<T, DV>::kBytes;
     static constexpr int oX = oQ + (MODE == kLocal ? 0 : Tile<T, DK>::kBytes);
-    static constexpr int oP = oX + (kX ? Tile<T, DV>::kBytes : 0);
-    static constexpr int oG = oP + (MODE == kLocal ? 0 : kPairs * kTermsP * kPPair);
-    // bf16 outputs leave through LDS as whole rows: where x's rows stood, which
-    // the second half of a chunk does not need, else in a place of their own.
-    static constexpr bool kStage = sizeof(T) == 2 && MODE != kLocal;
+    static constexpr int oFree = oX + (kX ? Tile<T, DV>::kBytes : 0);
+    // With four bf16 tiles of 128 columns P takes the place of q, behind a barrier
+    // of its own: two workgroups fit a compute unit only so.
+    static constexpr bool kPOnQ = kX && sizeof(T) == 2 && DK == 128 && DV == 128;
+    static constexpr int oP = kPOnQ ? oQ : oFree;
+    static constexpr int oG = oFree + (MODE == kLocal || kPOnQ ? 0 : kTerms * kPTerm);
+    // bf16 outputs leave through LDS as whole rows: where x's rows stood, or q's,
+    // which the second half of a chunk does not need, else in a place of their own.
+    static constexpr bool kStageOnQ = kStage && !kX && DK == DV;
     static constexpr int oOwn = oG + (int)sizeof(Gates);
-    static constexpr int oO = kX ? oX : oOwn;
-    static constexpr int oBad = oOwn + (kStage && !kX ? Tile<T, DV>::kBytes : 0);  // first row of a column that is not finite
+    static constexpr int oO = kX ? oX : kStageOnQ ? oQ : oOwn;
+    static constexpr int oBad = oOwn + (kStage && !kX && !kStageOnQ ? Tile<T, DV>::kBytes : 0);  // first row of a column that is not finite
     static constexpr bool kGuard = MODE == kAttend && !BACK;  // values that are not finite reach no row before theirs
     static constexpr int oDot = oBad + (kGuard ? DV * 8 + 16 : 0);
     static constexpr int oSum = oDot + (kX ? W * 64 * 4 : 0);
     static constexpr int kBytes = oSum + (MODE == kDotRows ? 64 * 4 * 4 : 0);
+    static __device__ __forceinline__ char* stage_at(char* lds, int row, int c) {  // c a multiple of 4
+        return lds + oO + (kStageOnQ ? Tile<T, DV>::quad(row, c / 4) : Tile<T, DV>::place(row, c / 8) + c % 8 * 2);
+    }
     // Waves on a SIMD that the registers are cut for: what LDS has room for, four at
     // most; two for local sums of fp32 rows, which spill with four (16384 rows of 32
     // heads of 128 x 128: 189 us against 317).
@@ -485,9 +505,6 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
             next_all = rows[n - 1].z;
         }
     };
-    if constexpr (MODE != kLocal)  // zeros, of which those that no tile overwrites stay
-        for (int c = threadIdx.x; c < kPairs * Y::kTermsP * Y::kPPair / 16; c += TH)
-            *reinterpret_cast<u32x4*>(tp + c * 16) = u32x4{0, 0, 0, 0};
     if constexpr (Y::kGuard) {
         if (threadIdx.x == 0) *s_bad = 0;
         for (int c = threadIdx.x; c < Y::DV; c += TH) poison[c] = 0.0f;
@@ -524,7 +541,7 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
         const int tid = MODE == kLocal ? (int)threadIdx.x : wave * 64 + lane, g = lane >> 4, i = lane & 15;
         if constexpr (Y::kStage) {
             if (step > 0 && !A.o_f32)
-                flush_rows<Y::DV, TH, VEC>(A, lds + Y::oO, row0 + (back ? kChunk : -kChunk), head,
+                flush_rows<Y::DV, TH, VEC, Y::kStageOnQ>(A, lds + Y::oO, row0 + (back ? kChunk : -kChunk), head,
                                            back ? min(kChunk, seg.rows - (c + 1) * kChunk) : kChunk, tid);
         }
         const float all = next_all;
@@ -575,7 +592,7 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) p[ks & 1] = mma(TK::by_row(tk, kr, o.ty, ks), TK::whole(tq, qr, o.tx, ks), p[ks & 1]);
             };
-            auto decayed = [&](int t, f32x4 (&p)[2]) {
+            auto decayed = [&](int t, f32x4 (&p)[2], float (&v)[4]) {
                 const Of o = tile_of(t);
                 settle(p);
                 f32x4 pm[2] = {f32x4{0, 0, 0, 0}, f32x4{0, 0, 0, 0}};
@@ -589,23 +606,11 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
                 const float xh = G.hi[x], xl = G.lo[x];
                 const f32x4 yh = *reinterpret_cast<const f32x4*>(G.hi + y0);
                 const f32x4 yl = *reinterpret_cast<const f32x4*>(G.lo + y0);
-                float v[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                     const float d = back ? (yh[r] - xh) + (yl[r] - xl) : (xh - yh[r]) + (xl - yl[r]);
                     const bool in = back ? y0 + r >= x : y0 + r <= x;
                     v[r] = in ? A.f_p * exp2_hw(d) * (p[0][r] + p[1][r]) : 0.0f;
-                }
-                char* const at = tp + pair<back>(o.tx, o.ty >> 1) * (Y::kTermsP * Y::kPPair) + lane * (8 * (int)sizeof(T)) +
-                                 (o.ty & 1) * (4 * (int)sizeof(T));
-                if constexpr (sizeof(T) == 2) {
-                    uint32_t a[2], b[2];
-                    split2<2>(v[0], v[1], a);
-                    split2<2>(v[2], v[3], b);
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) *reinterpret_cast<u32x2*>(at + j * Y::kPPair) = u32x2{a[j], b[j]};
-                } else {
-                    *reinterpret_cast<f32x4*>(at) = f32x4{v[0], v[1], v[2], v[3]};
                 }
                 if constexpr (MODE == kDotRows) {
                     // M without its diagonal: for a row x its sum over the tile's columns y, for a column y less its sum
@@ -624,6 +629,21 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
                     if (g == 0) s_sum[x * 4 + o.ty] = row;
                 }
             };
+            auto put = [&](int t, const float (&v)[4]) {
+                const Of o = tile_of(t);
+                const bool alone = is_alone<back>(o.tx, o.ty >> 1);
+                char* const at = tp + pair<back>(o.tx, o.ty >> 1) * Y::kPTile + lane * ((alone ? 4 : 8) * (int)sizeof(T)) +
+                                 (alone ? 0 : (o.ty & 1) * (4 * (int)sizeof(T)));
+                if constexpr (sizeof(T) == 2) {
+                    uint32_t a[3], b[3];
+                    split2<3>(v[0], v[1], a);
+                    split2<3>(v[2], v[3], b);
+#pragma unroll
+                    for (int j = 0; j < 3; ++j) *reinterpret_cast<u32x2*>(at + j * Y::kPTerm) = u32x2{a[j], b[j]};
+                } else {
+                    *reinterpret_cast<f32x4*>(at) = f32x4{v[0], v[1], v[2], v[3]};
+                }
+            };
             f32x4 p[2];
             if constexpr (MODE != kDotRows) products(wave, p);  // there, registers are short
             // the state's part, transposed: a lane holds four columns of row 16 b + i
@@ -631,7 +651,7 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
             for (int j = 0; j < 4 * NT; ++j) O[j] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                Frag<T> sf[NT][Y::kTermsS], qf[4];
+                Frag<T> sf[NT][Y::kTerms], qf[4];
 #pragma unroll
                 for (int b = 0; b < 4; ++b) qf[b] = TK::whole(tq, qr, b, ks);
 #pragma unroll
@@ -642,21 +662,37 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
                         f[r] = S[nn][2 * ks][r];
                         f[4 + r] = S[nn][2 * ks + 1][r];
                     }
-                    split<Y::kTermsS>(f, sf[nn]);
+                    split<Y::kTerms>(f, sf[nn]);
                 }
 #pragma unroll
-                for (int ts = 0; ts < Y::kTermsS; ++ts)
+                for (int ts = 0; ts < Y::kTerms; ++ts)
 #pragma unroll
                     for (int b = 0; b < 4; ++b)
 #pragma unroll
                         for (int nn = 0; nn < NT; ++nn) O[b * NT + nn] = mma(sf[nn][ts], qf[b], O[b * NT + nn]);
             }
             if constexpr (MODE == kDotRows) products(wave, p);
-            decayed(wave, p);
+            float own[4];
+            decayed(wave, p, own);
             // the tiles beyond W go to other waves, so to other SIMDs, in every chunk
-            for (int t = W + ((wave - 2 * step) & (W - 1)); t < kTri; t += W) {
-                products(t, p);
-                decayed(t, p);
+            const int more = W + ((wave - 2 * step) & (W - 1));
+            if constexpr (Y::kPOnQ) {
+                static_assert(kTri <= 2 * W, "two tiles to a wave");
+                float second[4];
+                if (more < kTri) {
+                    products(more, p);
+                    decayed(more, p, second);
+                }
+                lds_barrier();  // q has been read
+                put(wave, own);
+                if (more < kTri) put(more, second);
+            } else {
+                put(wave, own);
+                for (int t = more; t < kTri; t += W) {
+                    products(t, p);
+                    decayed(t, p, own);
+                    put(t, own);
+                }
             }
             settle(O);
 #pragma unroll
@@ -699,16 +735,24 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
 #pragma unroll
                 for (int nn = 0; nn < NT; ++nn) vf[nn] = TV::by_col(tv, vc, ys, wave * NT + nn);
 #pragma unroll
-                for (int j = 0; j < Y::kTermsP; ++j)
+                for (int j = 0; j < Y::kTerms; ++j)
 #pragma unroll
                     for (int b = 0; b < 4; ++b) {
                         if (!is_pair<back>(b, ys)) continue;
-                        const char* const p = tp + (pair<back>(b, ys) * Y::kTermsP + j) * Y::kPPair + lane * (8 * (int)sizeof(T));
+                        const bool alone = is_alone<back>(b, ys);
+                        const char* const p = tp + j * Y::kPTerm + pair<back>(b, ys) * Y::kPTile + lane * ((alone ? 4 : 8) * (int)sizeof(T));
                         Frag<T> pf;
                         if constexpr (sizeof(T) == 2) {
-                            pf.v = *reinterpret_cast<const u32x4*>(p);
+                            if (alone) {
+                                const u32x2 a = *reinterpret_cast<const u32x2*>(p);
+                                pf.v = back ? u32x4{0, 0, a.x, a.y} : u32x4{a.x, a.y, 0, 0};
+                            } else {
+                                pf.v = *reinterpret_cast<const u32x4*>(p);
+                            }
                         } else {
-                            const f32x4 a = *reinterpret_cast<const f32x4*>(p), c2 = *reinterpret_cast<const f32x4*>(p + 16);
+                            const f32x4 none = {0, 0, 0, 0}, one = *reinterpret_cast<const f32x4*>(p);
+                            const f32x4 a = alone && back ? none : one;
+                            const f32x4 c2 = alone ? (back ? one : none) : *reinterpret_cast<const f32x4*>(p + 16);
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 pf.v[e] = a[e];
@@ -727,7 +771,7 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
                 for (int nn = 0; nn < NT; ++nn)
 #pragma unroll
                     for (int b = 0; b < 4; ++b)
-                        *reinterpret_cast<u32x2*>(TV::at(lds + Y::oO, 16 * b + i, col0 + 16 * nn + 4 * g)) =
+                        *reinterpret_cast<u32x2*>(Y::stage_at(lds, 16 * b + i, col0 + 16 * nn + 4 * g)) =
                             u32x2{gdn::f32x2_to_bf16x2(O[b * NT + nn][0], O[b * NT + nn][1]),
                                   gdn::f32x2_to_bf16x2(O[b * NT + nn][2], O[b * NT + nn][3])};
             }
@@ -739,7 +783,7 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
                         for (int x = i; x < kChunk; x += 16) {
                             if (x < bad_row[c2]) continue;
                             if constexpr (Y::kStage) {
-                                *TV::at(lds + Y::oO, x, c2) = 0x7fc0;
+                                reinterpret_cast<bf16_t*>(Y::stage_at(lds, x, c2 - r))[r] = 0x7fc0;
                             } else {
                                 const uint32_t at = ((uint32_t)x * (uint32_t)A.o_stride + (uint32_t)c2) * (uint32_t)sizeof(T);
                                 __builtin_amdgcn_raw_buffer_store_b32(0x7fc00000u, rs, c2 < A.dv ? at : kNowhere, 0, 0);
@@ -751,7 +795,7 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
         // The next chunk's rows are asked for where the registers that held the output are free.
         fetch(back ? c - 1 : c + 1, tid, lane);
         const int kc = TK::col_base(g, i);
-        auto weighed = [&](int ys, Frag<T> (&vw)[NT][Y::kTermsV]) {  // v's rows with their decays
+        auto weighed = [&](int ys, Frag<T> (&vw)[NT][Y::kTerms]) {  // v's rows with their decays
             const f32x4 w0 = *reinterpret_cast<const f32x4*>(G.src + 32 * ys + 4 * g);
             const f32x4 w1 = *reinterpret_cast<const f32x4*>(G.src + 32 * ys + 16 + 4 * g);
 #pragma unroll
@@ -764,7 +808,7 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
                     f[4 + r] *= w1[r];
                 }
                 if constexpr (Y::kGuard) f[0] += poison[col0 + 16 * nn + i];
-                split<Y::kTermsV>(f, vw[nn]);
+                split<Y::kTerms>(f, vw[nn]);
             }
         };
         if constexpr (sizeof(T) == 4) {
@@ -803,7 +847,7 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
                 for (int m = 0; m < M; ++m) S[nn][m] *= all;
 #pragma unroll
             for (int ys = 0; ys < 2; ++ys) {
-                Frag<T> vw[NT][Y::kTermsV];
+                Frag<T> vw[NT][Y::kTerms];
                 weighed(ys, vw);
 #pragma unroll
                 for (int m = 0; m < M; m += KG) {  // sums in turn: none waits for itself
@@ -811,7 +855,7 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
 #pragma unroll
                     for (int j = 0; j < KG; ++j) kf[j] = TK::by_col(tk, kc, ys, m + j);
 #pragma unroll
-                    for (int tt = 0; tt < Y::kTermsV; ++tt)
+                    for (int tt = 0; tt < Y::kTerms; ++tt)
 #pragma unroll
                         for (int j = 0; j < KG; ++j)
 #pragma unroll
@@ -830,7 +874,7 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
     if constexpr (Y::kStage) {
         const int c = back ? 0 : n_chunks - 1;
         if (!A.o_f32)
-            flush_rows<Y::DV, TH, VEC>(A, lds + Y::oO, (int64_t)seg.row + (int64_t)c * kChunk, head,
+            flush_rows<Y::DV, TH, VEC, Y::kStageOnQ>(A, lds + Y::oO, (int64_t)seg.row + (int64_t)c * kChunk, head,
                                        min(kChunk, seg.rows - c * kChunk), threadIdx.x);
     }
     if (A.out.at != kNoState && (MODE == kLocal || (back ? seg.first : seg.last))) {
