@@ -776,16 +776,17 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
                                   gdn::f32x2_to_bf16x2(O[b * NT + nn][2], O[b * NT + nn][3])};
             }
             if (bad) {  // the same lanes wrote these places before
-                const __amdgpu_buffer_rsrc_t rs = rows_buffer<T>(A.o, A.o_stride, row0, (int64_t)head * A.dv, n, A.dv);
+                const bool staged = Y::kStage && !A.o_f32;
+                const __amdgpu_buffer_rsrc_t rs = rows_buffer<float>(A.o, A.o_stride, row0, (int64_t)head * A.dv, staged ? 0 : n, A.dv);
                 for (int nn = 0; nn < NT; ++nn)
                     for (int r = 0; r < 4; ++r) {
                         const int c2 = col0 + 16 * nn + 4 * g + r;
                         for (int x = i; x < kChunk; x += 16) {
                             if (x < bad_row[c2]) continue;
-                            if constexpr (Y::kStage) {
+                            if (staged) {
                                 reinterpret_cast<bf16_t*>(Y::stage_at(lds, x, c2 - r))[r] = 0x7fc0;
                             } else {
-                                const uint32_t at = ((uint32_t)x * (uint32_t)A.o_stride + (uint32_t)c2) * (uint32_t)sizeof(T);
+                                const uint32_t at = ((uint32_t)x * (uint32_t)A.o_stride + (uint32_t)c2) * (uint32_t)sizeof(float);
                                 __builtin_amdgcn_raw_buffer_store_b32(0x7fc00000u, rs, c2 < A.dv ? at : kNowhere, 0, 0);
                             }
                         }
