@@ -625,7 +625,11 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
                     }
                     row += __shfl_xor(row, 16, 64);
                     row += __shfl_xor(row, 32, 64);
-                    if (o.tx == o.ty) row += s_sum[x * 4 + o.tx];  // written above by this wave
+                    if (o.tx == o.ty) {  // written above by other lanes of this wave
+                        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+                        __builtin_amdgcn_wave_barrier();
+                        row += s_sum[x * 4 + o.tx];
+                    }
                     if (g == 0) s_sum[x * 4 + o.ty] = row;
                 }
             };
