@@ -149,7 +149,23 @@ __global__ __launch_bounds__(kThreads) void k_rotate(const RotateArgs A, int row
 #pragma unroll
                 for (int j = 0; j < N; ++j) ss = fmaf(a[k][j], a[k][j], fmaf(b[k][j], b[k][j], ss));
             ss = reduce16(ss);
-            const float root = 1.0f / sqrtf(ss * inv_over + A.eps);
+            float square = ss * inv_over + A.eps, unit = 1.0f;
+            // squares beyond fp32's range (|x| from some 2^60 on, or up to 2^-46 and eps no larger): the head, all
+            // sixteen lanes of it, is taken times a power of two, and its gradient once more in the end
+            if (!(square >= 0x1p-100f && square < __builtin_inff())) {
+                unit = square < 1.0f ? 0x1p100f : 0x1p-70f;
+                ss = 0.0f;
+#pragma unroll
+                for (int k = 0; k < NI; ++k)
+#pragma unroll
+                    for (int j = 0; j < N; ++j) {
+                        a[k][j] *= unit;
+                        b[k][j] *= unit;
+                        ss = fmaf(a[k][j], a[k][j], fmaf(b[k][j], b[k][j], ss));
+                    }
+                square = reduce16(ss) * inv_over + A.eps * unit * unit;
+            }
+            const float root = 1.0f / sqrtf(square);
             if constexpr (!BACK) {
 #pragma unroll
                 for (int k = 0; k < NI; ++k) {
@@ -204,8 +220,8 @@ __global__ __launch_bounds__(kThreads) void k_rotate(const RotateArgs A, int row
                     const int p0 = (k * kLanes + lane) * N;
 #pragma unroll
                     for (int j = 0; j < N; ++j) {
-                        da[k][j] = root * (da[k][j] - a[k][j] * along);
-                        db[k][j] = root * (db[k][j] - b[k][j] * along);
+                        da[k][j] = root * (da[k][j] - a[k][j] * along) * unit;
+                        db[k][j] = root * (db[k][j] - b[k][j] * along) * unit;
                     }
                     if (p0 < np) store_pairs<T, N>(y, p0, A.rot, neighbours, da[k], db[k]);
                 }

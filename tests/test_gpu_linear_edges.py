@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from gpu_util import DEV, gdn, host
+import test_gpu_rotate
 from linear_util import Case
 
 pytestmark = pytest.mark.gpu
@@ -28,3 +29,35 @@ def test_what_is_not_finite_shows_in_the_gradients(rows, act, hk, hv, with_dg):
         assert not torch.isfinite(getattr(got, out)[rest, 5]).any(), (name, out)
         for a, b in zip(got[:3], clean[:3]):
             assert torch.equal(a[rows:], b[rows:])
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-6])
+@pytest.mark.parametrize("shape", [dict(act="f32"), dict(), dict(act="f32", d=80, rot=36, pad=1), dict(d=250, rot=64, norm="l2"), dict(d=256, rot=256, norm="l2", act="f32")],
+                         ids=lambda s: ",".join(f"{k}={v}" for k, v in s.items()) or "plain")
+def test_heads_whose_squares_are_out_of_range(shape, eps):
+    """The norm of a head is a number wherever the head's values are: rows times
+    2^-100 to 2^120, gradients too, within the bounds of rows near 1."""
+    g = gdn()
+    c = test_gpu_rotate.Case(9, eps=eps, **shape)
+    times = torch.tensor([2.0 ** e for e in (120, 100, 64, 60, 0, -45, -52, -70, -100)], device=DEV)[:, None]
+    for t in ("q", "k"):
+        c.x[t].copy_((c.x[t].float() * times).to(c.x[t].dtype))
+    c.check(*g.gdnl_rotate_forward(*c.args()))
+    c.check_backward(g.gdnl_rotate_backward(*c.args(), c.dy["q"], c.dy["k"]))
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_heads_of_the_largest_and_the_smallest_numbers(act):
+    """A head of 64 values m and -m has the root mean square m: 1 and -1 come out."""
+    g = gdn()
+    dt = torch.float32 if act == "f32" else torch.bfloat16
+    dims = g.RotateDims(2, 0, 64, 0, act_dtype=act, eps=0.0)
+    sign = torch.where(torch.arange(128, device=DEV) % 3 == 0, -1.0, 1.0)
+    m = torch.tensor([torch.finfo(dt).max, torch.finfo(dt).tiny, 2.0 ** -133, 2.0 ** 61], device=DEV)[:, None]
+    q = (sign * m).to(dt)
+    y, _ = g.gdnl_rotate_forward(dims, q, q[:, :0], None, None, None, None)
+    # the squares' sum, the root and two products: within 32 half steps of fp32
+    assert (y.float() - sign).abs().max() <= (32 * 2.0 ** -24 if act == "f32" else 2.0 ** -8)
+    none = torch.zeros(1, 128, dtype=dt, device=DEV)
+    y, _ = g.gdnl_rotate_forward(g.RotateDims(2, 0, 64, 0, act_dtype=act, eps=1e-42), none, none[:, :0], None, None, None, None)
+    assert (y == 0).all()
