@@ -89,13 +89,14 @@ int64_t seg_rows(int64_t n_rows, const gdnl_dims* d, bool backward) {
     return len;
 }
 int64_t slots_of(int64_t n_seqs, int64_t n_rows, int64_t len) { return n_seqs + (n_rows + len - 1) / len + 1; }
-// The most slots that a batch of up to n_seqs sequences and n_rows rows has.
-int64_t most_slots(int64_t n_seqs, int64_t n_rows, int64_t heads, bool backward) {
+// The most borders between segments that a batch of up to n_rows rows has, and slots.
+int64_t most_borders(int64_t n_rows, int64_t heads, bool backward) {
     const int64_t by_rows = (n_rows + kSegMin - 1) / kSegMin, by_groups = kSegGroups / heads;
     int64_t most = by_rows < by_groups ? by_rows : by_groups;
     if (backward && most < (n_rows + kSegBack - 1) / kSegBack) most = (n_rows + kSegBack - 1) / kSegBack;
-    return n_seqs + (most < 1 ? 1 : most) + 1;
+    return most < 1 ? 1 : most;
 }
+int64_t most_slots(int64_t n_seqs, int64_t borders) { return n_seqs + borders + 1; }
 
 // The chunked kernels' grid, rounded up to whole key heads on every XCD, is beyond a launch.
 bool too_many(int64_t slots, const gdnl_dims* d) {
@@ -103,9 +104,9 @@ bool too_many(int64_t slots, const gdnl_dims* d) {
 }
 
 struct Ws {
-    size_t segs, seqs, total, gates, before, after, rows, cols, last, first, ends, gate, part, all;
+    size_t segs, seqs, total, gates, before, copy, after, rows, cols, last, first, ends, gate, part, all;
 };
-Ws layout(const gdnl_dims* d, int64_t slots, int64_t n_seqs, int64_t n_rows, bool backward) {
+Ws layout(const gdnl_dims* d, int64_t slots, int64_t borders, int64_t n_seqs, int64_t n_rows, bool backward) {
     Ws w{};
     const size_t H = (size_t)d->h_v, size = (size_t)d->d_k * d->d_v;
     size_t at = 0;
@@ -118,9 +119,10 @@ Ws layout(const gdnl_dims* d, int64_t slots, int64_t n_seqs, int64_t n_rows, boo
     w.seqs = take((size_t)n_seqs * sizeof(gdnl::SeqSlots));
     w.total = take((size_t)slots * H * sizeof(double));
     w.gates = take(H * (size_t)n_rows * sizeof(float4));
-    w.before = take((size_t)slots * H * size * sizeof(float));
+    w.before = take((size_t)borders * H * size * sizeof(float));
+    if (!backward) w.copy = take((size_t)borders * H * size * sizeof(float));
     if (backward) {
-        w.after = take((size_t)slots * H * size * sizeof(float));
+        w.after = take((size_t)borders * H * size * sizeof(float));
         w.rows = take(H * (size_t)n_rows * sizeof(float));
         w.cols = take(H * (size_t)n_rows * sizeof(float));
         w.last = take((size_t)n_seqs * H * size * sizeof(float));
@@ -150,6 +152,7 @@ gdnl::States turned(gdnl::States s) {
 
 struct Plan {
     int64_t len, slots, segments;  // rows of a segment; segments of the call and, at most, of a sequence
+    int64_t borders;               // between segments of a sequence
     bool split;  // sequences may have several segments
 };
 Plan plan_of(const gdnl_dims* d, const gdn_batch* b, bool backward) {
@@ -161,6 +164,7 @@ Plan plan_of(const gdnl_dims* d, const gdn_batch* b, bool backward) {
     if (!p.split) p.len = kSegWhole;
     p.slots = slots_of(b->n_seqs, b->n_rows, p.len);
     p.segments = (most + p.len - 1) / p.len;
+    p.borders = p.split ? (b->n_rows + p.len - 1) / p.len : 0;
     return p;
 }
 
@@ -172,9 +176,9 @@ GDN_EXPORT int32_t gdnl_attend_workspace_bytes(const gdnl_dims* dims, int32_t n_
     if ((st = check_dims(dims)) != GDN_OK) return st;
     if (!out_bytes || n_seqs < 0 || n_seqs > (1 << 28) || (backward != 0 && backward != 1)) return GDN_ERR_ARG;
     if ((st = check_rows(n_rows)) != GDN_OK) return st;
-    const int64_t slots = most_slots(n_seqs, n_rows, dims->h_v, backward != 0);
+    const int64_t borders = most_borders(n_rows, dims->h_v, backward != 0), slots = most_slots(n_seqs, borders);
     if (too_many(slots, dims)) return GDN_ERR_ARG;
-    *out_bytes = layout(dims, slots, n_seqs, n_rows, backward != 0).all;
+    *out_bytes = layout(dims, slots, borders, n_seqs, n_rows, backward != 0).all;
     return GDN_OK;
 }
 
@@ -214,7 +218,7 @@ GDN_EXPORT int32_t gdnl_attend_forward(const gdnl_dims* dims, const void* q, int
     }
     const Plan p = plan_of(dims, batch, false);
     if (too_many(p.slots, dims)) return GDN_ERR_ARG;
-    const Ws w = layout(dims, p.slots, batch->n_seqs, batch->n_rows, false);
+    const Ws w = layout(dims, p.slots, p.borders, batch->n_seqs, batch->n_rows, false);
     if (!workspace || !aligned(workspace, 256) || ws_bytes < w.all) return GDN_ERR_ARG;
     char* const ws = static_cast<char*>(workspace);
     gdnl::SegmentArgs G{};
@@ -234,7 +238,7 @@ GDN_EXPORT int32_t gdnl_attend_forward(const gdnl_dims* dims, const void* q, int
     A.v = {v, v_stride, 1};
     A.vec = rows_on(q, q_stride, dims->d_k, dt, 16) && rows_on(k, k_stride, dims->d_k, dt, 16) &&
             rows_on(v, v_stride, dims->d_v, dt, 16) && rows_on(o, o_stride, dims->d_v, dt, 16);
-    A.has_init = batch->has_init;
+    A.has_init = batch->has_init; A.len = (int32_t)p.len;
     A.dk = dims->d_k; A.dv = dims->d_v; A.heads = H; A.per = per;
     A.f_p = A.f_i = dims->scale; A.f_u = 1.0f;
     A.gates = reinterpret_cast<const float4*>(ws + w.gates);
@@ -242,13 +246,15 @@ GDN_EXPORT int32_t gdnl_attend_forward(const gdnl_dims* dims, const void* q, int
     hipError_t e = gdnl::launch_segments_decays(G, D, s);
     if (e != hipSuccess) return from_hip(e);
     if (p.split) {
-        A.out = dense(dims, before, gdnl::kBySlot);
+        A.out = A.mid = dense(dims, before, gdnl::kByBorder);
         if ((e = gdnl::launch_attend(A, gdnl::kLocal, false, dt == GDN_BF16, s)) != hipSuccess) return from_hip(e);
+        float* const copy = reinterpret_cast<float*>(ws + w.copy);
         gdnl::ScanArgs C{G.seqs, batch->page_idx, batch->has_init, batch->n_seqs, H, dims->d_k * dims->d_v, 0,
-                         pages_of(dims, state_in), before, total};
+                         pages_of(dims, state_in), before, total, copy};
+        A.copy = dense(dims, copy, gdnl::kByBorder);
         if ((e = gdnl::launch_state_scan(C, p.segments, s)) != hipSuccess) return from_hip(e);
     }
-    A.in = p.split ? dense(dims, before, gdnl::kBySlot) : pages_of(dims, state_in);
+    A.in = pages_of(dims, state_in);
     A.out = pages_of(dims, state_out);
     A.o = o; A.o_stride = o_stride;
     A.o_f32 = dt == GDN_F32;
@@ -280,7 +286,7 @@ GDN_EXPORT int32_t gdnl_attend_backward(const gdnl_dims* dims, const void* q, in
         return GDN_ERR_ARG;
     const Plan p = plan_of(dims, batch, true);
     if (too_many(p.slots, dims)) return GDN_ERR_ARG;
-    const Ws w = layout(dims, p.slots, batch->n_seqs, batch->n_rows, true);
+    const Ws w = layout(dims, p.slots, p.borders, batch->n_seqs, batch->n_rows, true);
     if (!workspace || !aligned(workspace, 256) || ws_bytes < w.all) return GDN_ERR_ARG;
     char* const ws = static_cast<char*>(workspace);
     const int32_t size = dims->d_k * dims->d_v;
@@ -311,21 +317,22 @@ GDN_EXPORT int32_t gdnl_attend_backward(const gdnl_dims* dims, const void* q, in
             rows_on(dq, dq_stride, dims->d_k, dt, 16) && rows_on(dk, dk_stride, dims->d_k, dt, 16) &&
             rows_on(dv, dv_stride, dims->d_v, dt, 16);
     A.segs = G.segs; A.n_slots = p.slots; A.n_rows = batch->n_rows;
-    A.has_init = batch->has_init; A.heads = H; A.per = per;
+    A.has_init = batch->has_init; A.heads = H; A.per = per; A.len = (int32_t)p.len;
     A.gates = reinterpret_cast<const float4*>(ws + w.gates);
     gdnl::DecayArgs D{G.segs, p.slots, batch->n_rows, H, g, g_stride, reinterpret_cast<float4*>(ws + w.gates), total};
     if ((e = gdnl::launch_segments_decays(G, D, s)) != hipSuccess) return from_hip(e);
     const gdnl::States ends = dense(dims, d_state, gdnl::kBySeq);
+    const gdnl::States at_borders = dense(dims, before, gdnl::kByBorder), grad_borders = dense(dims, after, gdnl::kByBorder);
     if (p.split) {
-        // S in front of every segment, then its gradient behind every segment
+        // S at every border, then its gradient there
         A.k = rk; A.v = rv; A.dk = dims->d_k; A.dv = dims->d_v; A.f_u = 1.0f;
-        A.out = dense(dims, before, gdnl::kBySlot);
+        A.out = at_borders;
         if ((e = gdnl::launch_attend(A, gdnl::kLocal, false, dt == GDN_BF16, s)) != hipSuccess) return from_hip(e);
         gdnl::ScanArgs C{G.seqs, batch->page_idx, batch->has_init, batch->n_seqs, H, size, 0, pages_of(dims, state_in),
-                         before, total};
+                         before, total, nullptr};
         if ((e = gdnl::launch_state_scan(C, p.segments, s)) != hipSuccess) return from_hip(e);
         A.k = rq; A.v = ro; A.f_u = dims->scale;
-        A.out = dense(dims, after, gdnl::kBySlot);
+        A.out = grad_borders;
         if ((e = gdnl::launch_attend(A, gdnl::kLocal, true, dt == GDN_BF16, s)) != hipSuccess) return from_hip(e);
         C.in = ends; C.back = 1; C.local = after;
         if ((e = gdnl::launch_state_scan(C, p.segments, s)) != hipSuccess) return from_hip(e);
@@ -348,7 +355,8 @@ GDN_EXPORT int32_t gdnl_attend_backward(const gdnl_dims* dims, const void* q, in
     A.q = ro; A.k = rv; A.v = rk; A.x = rq;
     A.dk = dims->d_v; A.dv = dims->d_k;
     A.f_p = A.f_i = dims->scale; A.f_u = 1.0f;
-    A.in = turned(p.split ? dense(dims, before, gdnl::kBySlot) : pages_of(dims, state_in));
+    A.in = turned(pages_of(dims, state_in));
+    A.mid = turned(at_borders);
     A.out = turned(dense(dims, dg && d_state ? last : nullptr, gdnl::kBySeq));
     A.dot = rows;
     to_keys(dq, dq_stride);
@@ -357,7 +365,8 @@ GDN_EXPORT int32_t gdnl_attend_backward(const gdnl_dims* dims, const void* q, in
     // dk: of v over d_o and q, backward in time
     A.q = rv; A.k = ro; A.v = rq; A.x = rk;
     A.f_i = 1.0f; A.f_u = dims->scale;
-    A.in = turned(p.split ? dense(dims, after, gdnl::kBySlot) : ends);
+    A.in = turned(ends);
+    A.mid = turned(grad_borders);
     A.out = gdnl::States{};
     A.dot = cols;
     to_keys(dk, dk_stride);
@@ -366,14 +375,15 @@ GDN_EXPORT int32_t gdnl_attend_backward(const gdnl_dims* dims, const void* q, in
     // dv: of k over q and d_o, backward in time, and the initial state's gradient
     A.q = rk; A.k = rq; A.v = ro;
     A.dk = dims->d_k; A.dv = dims->d_v;
-    A.in = p.split ? dense(dims, after, gdnl::kBySlot) : ends;
+    A.in = ends;
+    A.mid = grad_borders;
     float* const first = dg && !d_state0 ? reinterpret_cast<float*>(ws + w.first) : d_state0;
     A.out = dense(dims, first, gdnl::kBySeq);
     A.zero_uninit = 1;
     A.o = dv; A.o_stride = dv_stride; A.o_f32 = dt == GDN_F32;
     if ((e = gdnl::launch_attend(A, gdnl::kAttend, true, dt == GDN_BF16, s)) != hipSuccess) return from_hip(e);
     if (!dg) return GDN_OK;
-    gdnl::GateArgs T{G.segs, p.slots, batch->n_rows, H, size, g, g_stride, rows, cols, before, after, last, d_state,
+    gdnl::GateArgs T{G.segs, p.slots, batch->n_rows, H, size, (int32_t)p.len, g, g_stride, rows, cols, before, after, last, d_state,
                      G.seqs, batch->page_idx, batch->has_init, batch->n_seqs, pages_of(dims, state_in), first,
                      reinterpret_cast<double*>(ws + w.ends), dg, one_decay ? reinterpret_cast<double*>(ws + w.gate) : nullptr};
     if ((e = gdnl::launch_gate(T, s)) != hipSuccess || !one_decay) return from_hip(e);

@@ -315,8 +315,9 @@ __device__ __forceinline__ Segment segment_of(const SegWord* segs, int64_t slot)
     const int4 w = *reinterpret_cast<const int4*>(segs + slot);
     return Segment{w.x, w.y, w.z, w.w >> 2, (w.w & 1) != 0, (w.w & 2) != 0};
 }
-__device__ __forceinline__ int64_t state_base(const States& s, const Segment& seg, int64_t slot, int head) {
-    const int64_t unit = s.at == kByPage ? seg.page : s.at == kBySeq ? seg.seq : slot;
+// kByBorder: the border that the segment begins at or, `behind`, ends at.
+__device__ __forceinline__ int64_t state_base(const States& s, const Segment& seg, int len, bool behind, int head) {
+    const int64_t unit = s.at == kByPage ? seg.page : s.at == kBySeq ? seg.seq : seg.row / len + (behind ? 1 : 0);
     return unit * s.unit + head * s.head;
 }
 
@@ -513,18 +514,21 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
     f32x4 S[NT][M];
     {
         const int g = lane0 >> 4, i = lane0 & 15;
-        const bool zero = MODE == kLocal || A.in.at == kNoState ||
-                          (A.in.at == kByPage && A.has_init && A.has_init[seg.seq] == 0);
-        const int64_t base = zero ? 0 : state_base(A.in, seg, slot, head);
+        const States& in = !(back ? seg.last : seg.first)              ? A.mid
+                           : !back && !seg.last && A.copy.at != kNoState ? A.copy
+                                                                         : A.in;
+        const bool zero = MODE == kLocal || in.at == kNoState ||
+                          (in.at == kByPage && A.has_init && A.has_init[seg.seq] == 0);
+        const int64_t base = zero ? 0 : state_base(in, seg, A.len, back, head);
 #pragma unroll
         for (int nn = 0; nn < NT; ++nn) {
             const int col = col0 + 16 * nn + i;
 #pragma unroll
             for (int m = 0; m < M; ++m) S[nn][m] = f32x4{0, 0, 0, 0};
             if (!zero && col < A.dv) {
-                const int64_t at = base + (int64_t)col * A.in.cs;
-                if (A.in.bf16) load_state(S[nn], static_cast<const bf16_t*>(A.in.p) + at, A.in.rs, A.dk, g);
-                else load_state(S[nn], static_cast<const float*>(A.in.p) + at, A.in.rs, A.dk, g);
+                const int64_t at = base + (int64_t)col * in.cs;
+                if (in.bf16) load_state(S[nn], static_cast<const bf16_t*>(in.p) + at, in.rs, A.dk, g);
+                else load_state(S[nn], static_cast<const float*>(in.p) + at, in.rs, A.dk, g);
             }
         }
     }
@@ -884,7 +888,7 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
     }
     if (A.out.at != kNoState && (MODE == kLocal || (back ? seg.first : seg.last))) {
         const bool zero = A.zero_uninit && A.has_init && A.has_init[seg.seq] == 0;
-        const int64_t base = state_base(A.out, seg, slot, head);
+        const int64_t base = state_base(A.out, seg, A.len, !back, head);
         const int g = lane0 >> 4, i = lane0 & 15;
 #pragma unroll
         for (int nn = 0; nn < NT; ++nn) {

@@ -25,6 +25,11 @@ struct SeqSlots { int32_t slot, n; };
 // Segments of `len` rows (a multiple of 64) of every valid sequence: segment i
 // of sequence s has slot s + cu[s] / len + i.  Valid sequences do not overlap,
 // so their slots do not either, and all are below n_seqs + ceil(n_rows / len).
+// Where row r begins a sequence's second or later segment stands border r / len:
+// rows of one sequence's borders are len from each other, and those of another
+// more, its own first segment lying between.  There are ceil(n_rows / len) borders
+// however many sequences a batch has, and only cut ones have states at them.  By
+// the same division of their first rows cut sequences differ from each other too.
 struct SegmentArgs {
     const int32_t* cu; const int32_t* page_idx; int32_t n_seqs;
     int64_t n_rows, n_slots;
@@ -43,10 +48,10 @@ struct Rows {                    // packed rows of heads
 };
 
 // Where a segment's state comes from or goes to.
-enum StateAt { kNoState = 0, kByPage, kBySeq, kBySlot };
+enum StateAt { kNoState = 0, kByPage, kBySeq, kByBorder };
 struct States {
     void* p; int32_t at, bf16;
-    int64_t unit, head;          // elements from page (sequence, slot) to the next, from head to head
+    int64_t unit, head;          // elements from page (sequence, border) to the next, from head to head
     int32_t rs, cs;              // from row to row and column to column of the matrix the kernel holds
 };
 
@@ -75,7 +80,11 @@ struct AttendArgs {
     const uint8_t* has_init;
     int32_t dk, dv, heads, per;  // widths of q, k and of v, out; value heads, those to a key head
     float f_p, f_i, f_u;
-    States in, out;              // out: at the end of the sequence (local sums: of the segment)
+    // in, out: at the ends of a sequence (out of local sums: at the border that the segment ends at);
+    // mid: in of segments that begin at a border; copy: of the first segment of a cut sequence, whose page another
+    // segment's workgroup may write (kNoState: no such page is written)
+    States in, mid, copy, out;
+    int32_t len;                 // rows of a segment
     int32_t zero_uninit;         // out is zero where has_init is 0
     void* o; int64_t o_stride; int32_t o_f32;
     int32_t vec;                 // all rows and heads on 16 bytes, those of o on four values
@@ -98,12 +107,15 @@ inline hipError_t launch_attend(const AttendArgs& a, int mode, bool back, bool b
     return bf16 ? launch_attend_bf16(a, mode, s) : launch_attend_f32(a, mode, s);
 }
 
-// S in front of (back: behind) every segment in the place of its local sum.
+// At every border the state there in the place of the local sum of the segment
+// in front of it (back: behind it).
 struct ScanArgs {
     const SeqSlots* seqs; const int32_t* page_idx; const uint8_t* has_init;
     int32_t n_seqs, heads, size, back;   // size: dk * dv
     States in;
-    float* local; const double* total;
+    float* local;                // [border][heads][size]
+    const double* total;
+    float* copy;                 // [first row / len][heads][size]: receives cut sequences' `in`, or NULL
 };
 hipError_t launch_state_scan(const ScanArgs& a, int64_t segments, hipStream_t s);  // of a sequence, at most
 
@@ -111,10 +123,10 @@ hipError_t launch_state_scan(const ScanArgs& a, int64_t segments, hipStream_t s)
 // gradient> at the segment's end.
 struct GateArgs {
     const SegWord* segs; int64_t n_slots, n_rows;
-    int32_t heads, size;
+    int32_t heads, size, len;
     const float* g; int64_t g_stride;
     const float* rows; const float* cols;          // [heads][n_rows]
-    const float* before; const float* after;       // [slot][heads][size], NULL: one segment to a sequence
+    const float* before; const float* after;       // [border][heads][size]: the state and its gradient there
     const float* last; const float* d_state;       // [seq][heads][size]; d_state NULL: X is 0 at a sequence's end
     const SeqSlots* seqs; const int32_t* page_idx; const uint8_t* has_init;
     int32_t n_seqs; States start;                  // the pages, and

@@ -197,11 +197,11 @@ hipError_t launch_segments_decays(const SegmentArgs& s, const DecayArgs& a, hipS
     return hipGetLastError();
 }
 
-// The states between segments.  A lane holds a value of the state, and a wave eight
-// segments of the round, whose local sums it asks for together; with more segments
+// The states at borders.  A lane holds a value of the state, and a wave eight
+// borders of the round, whose local sums it asks for together; with more borders
 // than that, waves of a workgroup take eight each, fold them to (decay, sum), and
 // each takes its state from the folds before it.  One round of loads and one of
-// stores for 128 segments: 36 us -> 8 us for 118 segments of four heads of 64 x 64,
+// stores for 128 borders: 36 us -> 8 us for 118 segments of four heads of 64 x 64,
 // where waiting is all of it; 28 us for 16 segments of 4 x 32 heads of 128 x 128.
 constexpr int kScanMine = 8, kScanWaves = 16;
 __global__ __launch_bounds__(kScanWaves * 64) void k_state_scan(const ScanArgs A, int blocks, int waves, int width) {
@@ -212,7 +212,8 @@ __global__ __launch_bounds__(kScanWaves * 64) void k_state_scan(const ScanArgs A
         const int part = (int)(b % blocks), head = (int)(b / blocks % A.heads), seq = (int)(b / blocks / A.heads);
         const SeqSlots at = A.seqs[seq];
         const int e = part * width + team / waves * 64 + lane;
-        if (at.n <= 0) continue;
+        const int n = at.n - 1;  // borders
+        if (n <= 0) continue;
         const bool in = e < A.size;
         const bool zero = A.in.at == kNoState || (A.in.at == kByPage && A.has_init && A.has_init[seq] == 0);
         float carry = 0.0f;
@@ -220,19 +221,20 @@ __global__ __launch_bounds__(kScanWaves * 64) void k_state_scan(const ScanArgs A
             const int64_t from = (A.in.at == kByPage ? (int64_t)A.page_idx[seq] : (int64_t)seq) * A.in.unit + head * A.in.head + e;
             carry = A.in.bf16 ? gdn::to_f32(static_cast<const gdn::bf16_t*>(A.in.p)[from]) : static_cast<const float*>(A.in.p)[from];
         }
+        if (A.copy && in && mine == 0) A.copy[((int64_t)(at.slot - seq) * A.heads + head) * A.size + e] = carry;
         const int64_t step = A.back ? -A.heads : A.heads;
-        for (int k0 = 0; k0 < at.n; k0 += kScanMine * waves) {
+        for (int k0 = 0; k0 < n; k0 += kScanMine * waves) {
             const int first = k0 + mine * kScanMine;
-            const int64_t item = (int64_t)(at.slot + (A.back ? at.n - 1 : 0)) * A.heads + head + step * first;
+            // the segment whose local sum is at the border, and the border: slot - seq is that of the first row
+            const int64_t item = (int64_t)(at.slot + (A.back ? n : 0)) * A.heads + head + step * first;
+            const int64_t border = (int64_t)(at.slot - seq + (A.back ? n : 1)) * A.heads + head + step * first;
             float own[kScanMine], factor[kScanMine];
 #pragma unroll
-            for (int j = 0; j < kScanMine; ++j) {
-                const bool more = first + j + 1 < at.n;  // the last one's local sum was not made
-                own[j] = more && in ? A.local[(item + step * j) * A.size + e] : 0.0f;
-            }
+            for (int j = 0; j < kScanMine; ++j)
+                own[j] = first + j < n && in ? A.local[(border + step * j) * A.size + e] : 0.0f;
             // the factors, each made by a lane, take up what rounding left of those before, as in decays_of
             const int j8 = lane % kScanMine;
-            const double exact = exp2_of<double>(first + j8 + 1 < at.n ? A.total[item + step * j8] : 0.0);
+            const double exact = exp2_of<double>(first + j8 < n ? A.total[item + step * j8] : 0.0);
             const float exact_hi = (float)exact, exact_lo = fabsf(exact_hi) < __builtin_inff() ? (float)(exact - (double)exact_hi) : 0.0f;
             float left = 0.0f;
 #pragma unroll
@@ -260,8 +262,8 @@ __global__ __launch_bounds__(kScanWaves * 64) void k_state_scan(const ScanArgs A
             }
 #pragma unroll
             for (int j = 0; j < kScanMine; ++j) {
-                if (in && first + j < at.n) A.local[(item + step * j) * A.size + e] = cur;
                 cur = fmaf(factor[j], cur, own[j]);
+                if (in && first + j < n) A.local[(border + step * j) * A.size + e] = cur;
             }
             if (waves == 1) carry = cur;
         }
@@ -311,8 +313,8 @@ __global__ __launch_bounds__(kEndThreads) void k_gate_ends(const GateArgs A) {
                 e = A.d_state + at;
             } else if (w.z > 0 && (w.w & 2) == 0) {
                 p.p = const_cast<float*>(A.before);
-                at = ((unit + 1) * A.heads + head) * A.size;
-                e = A.after + (unit * A.heads + head) * A.size;
+                at = ((int64_t)(w.y / A.len + 1) * A.heads + head) * A.size;
+                e = A.after + at;
             }
         } else {
             const int seq = (int)(unit - A.n_slots);
