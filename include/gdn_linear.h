@@ -68,9 +68,18 @@ typedef struct gdnl_dims {
 
 /* ------------------------------------------------- linear attention */
 
+/* What a backward call is asked for and given: dg, d_state, d_state0. */
+#define GDNL_ASKS 16
+#define GDNL_ASKS_DG 1
+#define GDNL_ASKS_D_STATE 2
+#define GDNL_ASKS_D_STATE0 4
+
 /* Bytes of workspace gdnl_attend_forward (backward = 0) or
  * gdnl_attend_backward (1) needs for a batch of up to n_seqs sequences and
- * n_rows rows (host-only). */
+ * n_rows rows (host-only).  backward = GDNL_ASKS, or-ed with GDNL_ASKS_* for
+ * those of the three arguments that are not NULL: for such calls alone, a state
+ * for every sequence less where no dg is wanted, where there is no d_state, or
+ * where d_state0 is given. */
 int32_t gdnl_attend_workspace_bytes(const gdnl_dims* dims, int32_t n_seqs, int64_t n_rows, int32_t backward,
                                     size_t* out_bytes);
 

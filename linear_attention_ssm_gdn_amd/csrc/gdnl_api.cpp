@@ -106,7 +106,8 @@ bool too_many(int64_t slots, const gdnl_dims* d) {
 struct Ws {
     size_t segs, seqs, total, gates, before, copy, after, rows, cols, last, first, ends, gate, part, all;
 };
-Ws layout(const gdnl_dims* d, int64_t slots, int64_t borders, int64_t n_seqs, int64_t n_rows, bool backward) {
+// asked: GDNL_ASKS_* of a backward call, 0 of a forward one.
+Ws layout(const gdnl_dims* d, int64_t slots, int64_t borders, int64_t n_seqs, int64_t n_rows, bool backward, int32_t asked) {
     Ws w{};
     const size_t H = (size_t)d->h_v, size = (size_t)d->d_k * d->d_v;
     size_t at = 0;
@@ -125,8 +126,10 @@ Ws layout(const gdnl_dims* d, int64_t slots, int64_t borders, int64_t n_seqs, in
         w.after = take((size_t)borders * H * size * sizeof(float));
         w.rows = take(H * (size_t)n_rows * sizeof(float));
         w.cols = take(H * (size_t)n_rows * sizeof(float));
-        w.last = take((size_t)n_seqs * H * size * sizeof(float));
-        w.first = take((size_t)n_seqs * H * size * sizeof(float));
+        // a state for every sequence only where the decays' gradient reads what is not an argument
+        const size_t whole = (size_t)n_seqs * H * size * sizeof(float);
+        w.last = take((asked & GDNL_ASKS_DG) && (asked & GDNL_ASKS_D_STATE) ? whole : 0);
+        w.first = take((asked & GDNL_ASKS_DG) && !(asked & GDNL_ASKS_D_STATE0) ? whole : 0);
         w.ends = take((size_t)(slots + n_seqs) * H * sizeof(double));
         w.gate = take((size_t)slots * H * sizeof(double));
         if (d->h_k != d->h_v) w.part = take((size_t)n_rows * H * (size_t)d->d_k * sizeof(float));
@@ -174,11 +177,14 @@ GDN_EXPORT int32_t gdnl_attend_workspace_bytes(const gdnl_dims* dims, int32_t n_
                                                size_t* out_bytes) {
     int32_t st;
     if ((st = check_dims(dims)) != GDN_OK) return st;
-    if (!out_bytes || n_seqs < 0 || n_seqs > (1 << 28) || (backward != 0 && backward != 1)) return GDN_ERR_ARG;
+    constexpr int32_t all = GDNL_ASKS | GDNL_ASKS_DG | GDNL_ASKS_D_STATE | GDNL_ASKS_D_STATE0;
+    if (!out_bytes || n_seqs < 0 || n_seqs > (1 << 28)) return GDN_ERR_ARG;
+    if (backward != 0 && backward != 1 && (!(backward & GDNL_ASKS) || (backward & ~all))) return GDN_ERR_ARG;
     if ((st = check_rows(n_rows)) != GDN_OK) return st;
+    const int32_t asked = backward == 1 ? GDNL_ASKS_DG | GDNL_ASKS_D_STATE : backward;  // 1: the most
     const int64_t borders = most_borders(n_rows, dims->h_v, backward != 0), slots = most_slots(n_seqs, borders);
     if (too_many(slots, dims)) return GDN_ERR_ARG;
-    *out_bytes = layout(dims, slots, borders, n_seqs, n_rows, backward != 0).all;
+    *out_bytes = layout(dims, slots, borders, n_seqs, n_rows, backward != 0, asked).all;
     return GDN_OK;
 }
 
@@ -218,7 +224,7 @@ GDN_EXPORT int32_t gdnl_attend_forward(const gdnl_dims* dims, const void* q, int
     }
     const Plan p = plan_of(dims, batch, false);
     if (too_many(p.slots, dims)) return GDN_ERR_ARG;
-    const Ws w = layout(dims, p.slots, p.borders, batch->n_seqs, batch->n_rows, false);
+    const Ws w = layout(dims, p.slots, p.borders, batch->n_seqs, batch->n_rows, false, 0);
     if (!workspace || !aligned(workspace, 256) || ws_bytes < w.all) return GDN_ERR_ARG;
     char* const ws = static_cast<char*>(workspace);
     gdnl::SegmentArgs G{};
@@ -286,7 +292,8 @@ GDN_EXPORT int32_t gdnl_attend_backward(const gdnl_dims* dims, const void* q, in
         return GDN_ERR_ARG;
     const Plan p = plan_of(dims, batch, true);
     if (too_many(p.slots, dims)) return GDN_ERR_ARG;
-    const Ws w = layout(dims, p.slots, p.borders, batch->n_seqs, batch->n_rows, true);
+    const int32_t asked = (dg ? GDNL_ASKS_DG : 0) | (d_state ? GDNL_ASKS_D_STATE : 0) | (d_state0 ? GDNL_ASKS_D_STATE0 : 0);
+    const Ws w = layout(dims, p.slots, p.borders, batch->n_seqs, batch->n_rows, true, asked);
     if (!workspace || !aligned(workspace, 256) || ws_bytes < w.all) return GDN_ERR_ARG;
     char* const ws = static_cast<char*>(workspace);
     const int32_t size = dims->d_k * dims->d_v;

@@ -93,10 +93,14 @@ class RotateGrads(NamedTuple):
     dwk: Optional[torch.Tensor]
 
 
-def gdnl_attend_workspace_bytes(dims: LinearDims, n_seqs: int, n_rows: int, backward: bool = False) -> int:
-    out, d = ctypes.c_size_t(0), dims.c()
+def gdnl_attend_workspace_bytes(dims: LinearDims, n_seqs: int, n_rows: int, backward: bool = False,
+                                asks: Optional[tuple] = None) -> int:
+    """asks: for backward calls alone that are given (dg, d_state, d_state0), three truth values."""
+    out, d, what = ctypes.c_size_t(0), dims.c(), 1 if backward else 0
+    if backward and asks is not None:
+        what = L.GDNL_ASKS | sum(f for f, given in zip((L.GDNL_ASKS_DG, L.GDNL_ASKS_D_STATE, L.GDNL_ASKS_D_STATE0), asks) if given)
     _check("gdnl_attend_workspace_bytes",
-           L.load().gdnl_attend_workspace_bytes(ctypes.byref(d), n_seqs, n_rows, 1 if backward else 0, ctypes.byref(out)))
+           L.load().gdnl_attend_workspace_bytes(ctypes.byref(d), n_seqs, n_rows, what, ctypes.byref(out)))
     return int(out.value)
 
 
@@ -214,7 +218,8 @@ def gdnl_attend_backward(dims: LinearDims, q: torch.Tensor, k: torch.Tensor, v: 
         dqs, dks, dvs = _rows2("dq", out.dq, n, wk, dt), _rows2("dk", out.dk, n, wk, dt), _rows2("dv", out.dv, n, wv, dt)
         _flat("dg", out.dg, (dims.h_v,) if one else (n, dims.h_v), torch.float32)
         _flat("d_state0", out.d_state0, state, torch.float32)
-    space = _space(workspace, 0 if workspace is not None else gdnl_attend_workspace_bytes(dims, s, n, True), dev)
+    asks = out.dg is not None, d_state is not None, out.d_state0 is not None
+    space = _space(workspace, 0 if workspace is not None else gdnl_attend_workspace_bytes(dims, s, n, True, asks), dev)
     d, bt = dims.c(), batch.c()
     _call("gdnl_attend_backward", dev,
           ctypes.byref(d), q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, g.data_ptr(), gs, ctypes.byref(bt),

@@ -61,3 +61,32 @@ def test_heads_of_the_largest_and_the_smallest_numbers(act):
     none = torch.zeros(1, 128, dtype=dt, device=DEV)
     y, _ = g.gdnl_rotate_forward(g.RotateDims(2, 0, 64, 0, act_dtype=act, eps=1e-42), none, none[:, :0], None, None, None, None)
     assert (y == 0).all()
+
+
+@pytest.mark.parametrize("d_state", [True, False])
+@pytest.mark.parametrize("with_dg", [True, False])
+@pytest.mark.parametrize("with_d_state0", [True, False])
+def test_workspace_of_exactly_what_a_call_asks_for(d_state, with_dg, with_d_state0):
+    """Each combination within its own size, filled with NaN, gives the bits of a
+    call with room for any; half of what 128 rows need is refused."""
+    g = gdn()
+    c = Case([700, 0, 300, 70], hk=1, hv=2, dk=16, dv=24, act="bf16", fast=0.1)
+    size = g.gdnl_attend_workspace_bytes(c.dims, c.n, c.rows, True, (with_dg, d_state, with_d_state0))
+    most = g.gdnl_attend_workspace_bytes(c.dims, c.n, c.rows, True)
+    assert size <= most
+
+    def run(n_bytes):
+        ws = torch.full((n_bytes + 256,), 255, dtype=torch.uint8, device=DEV)
+        out = g.LinearGrads(*(torch.zeros_like(c.t[t]) for t in "qkv"), torch.zeros(c.rows, c.hv, device=DEV) if with_dg else None,
+                            torch.zeros(c.n, c.hv, c.dk, c.dv, device=DEV) if with_d_state0 else None)
+        g.gdnl_attend_backward(c.dims, c.t["q"], c.t["k"], c.t["v"], c.g, c.batch, g.StatePool(c.s0.to(DEV)), c.t["d_o"],
+                               d_state=torch.from_numpy(c.d_state).to(DEV) if d_state else None, out=out, workspace=ws[:n_bytes])
+        torch.cuda.synchronize()
+        assert (ws[n_bytes:] == 255).all()
+        return out
+
+    for a, b in zip(run(size), run(most)):
+        assert (a is None and b is None) or torch.equal(a, b)
+    small = g.gdnl_attend_workspace_bytes(c.dims, c.n, 128, True, (with_dg, d_state, with_d_state0))
+    with pytest.raises(g.GdnError):
+        run(small // 2)

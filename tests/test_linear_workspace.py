@@ -1,6 +1,7 @@
 """What the attend calls ask for as scratch (host only)."""
 import ctypes
 import os
+import re
 
 import pytest
 
@@ -26,3 +27,29 @@ def test_many_short_documents_need_no_states_for_each(L):
     need = size(L, (16, 32, 128, 128, 1, 0), 1024, rows, 0)
     assert need <= 2 * 16 * state + 32 * rows * 16 + (1024 + 17) * (16 + 8 + 32 * 8) + 6 * 256
     assert size(L, (16, 32, 128, 128, 1, 0), 1, rows, 0) >= 2 * 16 * state  # one document is cut, and in place
+
+
+def test_a_backward_call_asks_for_states_of_sequences_that_it_reads(L):
+    """`last`, the final states, beside a dg and a d_state, and `first`, the
+    gradient of the initial ones, beside a dg and no d_state0: nothing else
+    grows with the sequences but for their 16 + 8 + 32 * 8 bytes a slot."""
+    dims, state = (16, 32, 128, 128, 1, 0), 32 * 128 * 128 * 4
+    extra = lambda what: size(L, dims, 1024, 65536, what) - size(L, dims, 24, 65536, what)  # noqa: E731
+    for dg in (0, L.GDNL_ASKS_DG):
+        for ds in (0, L.GDNL_ASKS_D_STATE):
+            for d0 in (0, L.GDNL_ASKS_D_STATE0):
+                states = ((1 if ds else 0) + (0 if d0 else 1)) * 1000 * state if dg else 0
+                assert states <= extra(L.GDNL_ASKS | dg | ds | d0) <= states + 1000 * 2048
+    assert size(L, dims, 1024, 65536, 1) == size(L, dims, 1024, 65536, L.GDNL_ASKS | L.GDNL_ASKS_DG | L.GDNL_ASKS_D_STATE)
+    out = ctypes.c_size_t()
+    for what in (3, 8, 24, 32, -1, 16 + 8):
+        assert L.load().gdnl_attend_workspace_bytes(ctypes.byref(L.GdnlDims(*dims, 1.0)), 4, 64, what, ctypes.byref(out)) == 1
+
+
+def test_the_binding_has_the_headers_constants(L):
+    header = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "gdn_linear.h")
+    with open(header) as f:
+        defined = dict(re.findall(r"^#define (GDNL_\w+) (\d+)", f.read(), re.M))
+    assert {"GDNL_ASKS", "GDNL_ASKS_DG", "GDNL_ASKS_D_STATE", "GDNL_ASKS_D_STATE0"} <= set(defined)
+    for name, value in defined.items():
+        assert getattr(L, name) == int(value)
