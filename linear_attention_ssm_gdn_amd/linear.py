@@ -208,6 +208,8 @@ def gdnl_attend_backward(dims: LinearDims, q: torch.Tensor, k: torch.Tensor, v: 
     _check_pool("state_in", state_in, dims)
     qs, ks, vs = _rows2("q", q, n, wk, dt), _rows2("k", k, n, wk, dt), _rows2("v", v, n, wv, dt)
     os_, gs = _rows2("d_o", d_o, n, wv, dt), _gates(g, n, dims.h_v)
+    if gs == 0 and not one:  # one row expanded over all: its gradient is each row's
+        g, gs = g.contiguous(), dims.h_v
     _flat("d_state", d_state, state, torch.float32)
     if out is None:
         out = LinearGrads(q.new_empty((n, wk)), q.new_empty((n, wk)), q.new_empty((n, wv)),

@@ -90,3 +90,20 @@ def test_workspace_of_exactly_what_a_call_asks_for(d_state, with_dg, with_d_stat
     small = g.gdnl_attend_workspace_bytes(c.dims, c.n, 128, True, (with_dg, d_state, with_d_state0))
     with pytest.raises(g.GdnError):
         run(small // 2)
+
+
+def test_decays_of_one_row_expanded_over_all():
+    """A g [rows][heads] whose rows are one and the same memory has a gradient for every row."""
+    g = gdn()
+    c = Case([70, 3], decay="head", act="bf16", fast=0.1)
+    one, rows = c.g, c.g.expand(c.rows, c.hv)
+    want = {}
+    for gates in (rows.contiguous(), rows):
+        o = g.gdnl_attend_forward(c.dims, c.t["q"], c.t["k"], c.t["v"], gates, c.batch, g.StatePool(c.s0.to(DEV)))
+        d = g.gdnl_attend_backward(c.dims, c.t["q"], c.t["k"], c.t["v"], gates, c.batch, g.StatePool(c.s0.to(DEV)), c.t["d_o"])
+        assert d.dg.shape == (c.rows, c.hv)
+        for n, t in {"o": o, **d._asdict()}.items():
+            assert torch.equal(want.setdefault(n, t), t), n
+    summed = g.gdnl_attend_backward(c.dims, c.t["q"], c.t["k"], c.t["v"], one, c.batch, g.StatePool(c.s0.to(DEV)), c.t["d_o"]).dg
+    # the sum of rows rounded one by one: half a step each
+    assert ((want["dg"].double().sum(0) - summed.double()).abs() <= 2.0 ** -24 * (want["dg"].double().abs().sum(0) + summed.double().abs())).all()
