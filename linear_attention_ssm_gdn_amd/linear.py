@@ -6,8 +6,11 @@ As in train.py every function checks its tensors, turns them into device
 pointers, strides and sizes, calls the C entry point on the current HIP stream
 of the tensors' device and raises on a non-OK status.  Outputs and workspaces
 that are not given are allocated.  Autograd records nothing here: a call whose
-history would be lost in silence is refused (call it under torch.no_grad(), with
-detached tensors, or from a torch.autograd.Function).
+history would be lost in silence, forward or backward, is refused, be it that
+gradients are enabled and an input requires one (the backward calls' inputs
+too: they have no second derivative) or that an input has a forward-mode
+tangent.  Call it under torch.no_grad(), with detached tensors, or from a
+torch.autograd.Function.
 """
 from __future__ import annotations
 
@@ -17,6 +20,7 @@ import functools
 from typing import NamedTuple, Optional
 
 import torch
+from torch.autograd import forward_ad
 
 from . import _lib as L
 from .ops import _DT, _TORCH_DT, Batch, StatePool, _check
@@ -118,6 +122,13 @@ def gdnl_cache_bytes(dims: LinearDims, n_entries: int) -> tuple:
     return int(q.value), int(s.value)
 
 
+def _no_tangents(fn: str, *tensors: Optional[torch.Tensor]) -> None:
+    """Within torch.autograd.forward_ad.dual_level() alone, which _current_level tells for less than a tensor's check."""
+    for t in tensors:
+        if t is not None and forward_ad.unpack_dual(t).tangent is not None:
+            _no_history(fn)
+
+
 def _check_pool(name: str, pool: StatePool, dims: LinearDims) -> None:
     t = pool.buf
     shape = (dims.h_v, dims.d_k, dims.d_v)
@@ -167,6 +178,8 @@ def gdnl_attend_forward(dims: LinearDims, q: torch.Tensor, k: torch.Tensor, v: t
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or g.requires_grad or
                                     state_in.buf.requires_grad):
         _no_history("gdnl_attend_forward")
+    if forward_ad._current_level >= 0:
+        _no_tangents("gdnl_attend_forward", q, k, v, g, state_in.buf)
     _on(dev, k=k, v=v, g=g, state_in=state_in.buf, state_out=state_out.buf, err=err)
     _check_batch(batch, dev)
     _check_pool("state_in", state_in, dims)
@@ -201,8 +214,12 @@ def gdnl_attend_backward(dims: LinearDims, q: torch.Tensor, k: torch.Tensor, v: 
     dev, n, dt, s = q.device, batch.n_rows, _TORCH_DT[dims.act_dtype], batch.n_seqs
     wk, wv, one = dims.h_k * dims.d_k, dims.h_v * dims.d_v, g.dim() == 1
     state = (s, dims.h_v, dims.d_k, dims.d_v)
-    if torch.is_grad_enabled() and (d_o.requires_grad or (d_state is not None and d_state.requires_grad)):
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad or g.requires_grad or
+                                    state_in.buf.requires_grad or d_o.requires_grad or
+                                    (d_state is not None and d_state.requires_grad)):
         _no_history("gdnl_attend_backward")
+    if forward_ad._current_level >= 0:
+        _no_tangents("gdnl_attend_backward", q, k, v, g, state_in.buf, d_o, d_state)
     _on(dev, k=k, v=v, g=g, d_o=d_o, d_state=d_state, state_in=state_in.buf, err=err)
     _check_batch(batch, dev)
     _check_pool("state_in", state_in, dims)
@@ -250,6 +267,8 @@ def gdnl_rotate_forward(dims: RotateDims, q: torch.Tensor, k: torch.Tensor, wq: 
     [n_rows]) times inv_freq (fp32 [rot/2]).  yq may be q, and yk k."""
     if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, wq, wk)):
         _no_history("gdnl_rotate_forward")
+    if forward_ad._current_level >= 0:
+        _no_tangents("gdnl_rotate_forward", q, k, wq, wk)
     n, dt, dev, qs, ks = _rotate_inputs(dims, q, k, wq, wk, pos, inv_freq)
     yq, yqs = _rows_out("yq", yq, q, n, dims.h_q * dims.d, dt, dev)
     yk, yks = _rows_out("yk", yk, q, n, dims.h_k * dims.d, dt, dev)
@@ -266,8 +285,10 @@ def gdnl_rotate_backward(dims: RotateDims, q: torch.Tensor, k: torch.Tensor, wq:
     """The gradients of gdnl_rotate_forward at its inputs q and k.  out.dq may
     be d_yq and out.dk d_yk; an `out` whose dwq or dwk is None leaves it out, as
     does a weight of None."""
-    if torch.is_grad_enabled() and (d_yq.requires_grad or d_yk.requires_grad):
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (q, k, wq, wk, d_yq, d_yk)):
         _no_history("gdnl_rotate_backward")
+    if forward_ad._current_level >= 0:
+        _no_tangents("gdnl_rotate_backward", q, k, wq, wk, d_yq, d_yk)
     n, dt, dev, qs, ks = _rotate_inputs(dims, q, k, wq, wk, pos, inv_freq)
     nq, nk = dims.h_q * dims.d, dims.h_k * dims.d
     _on(dev, d_yq=d_yq, d_yk=d_yk)
@@ -292,6 +313,10 @@ def gdnl_rotate_backward(dims: RotateDims, q: torch.Tensor, k: torch.Tensor, wq:
 def _cache_call(fn: str, dims: LinearDims, first: tuple, second: tuple, pool: StatePool, cache: StateCache, err,
                 store: bool) -> None:
     dev, n = pool.buf.device, first[1].numel()
+    if torch.is_grad_enabled() and pool.buf.requires_grad:
+        _no_history(fn)
+    if forward_ad._current_level >= 0:
+        _no_tangents(fn, pool.buf)
     _on(dev, **{first[0]: first[1], second[0]: second[1]}, q=cache.q, scale=cache.scale, err=err)
     for name, t in (first, second):
         _flat(name, t, (n,), torch.int32)
