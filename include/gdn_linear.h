@@ -38,6 +38,15 @@
  * - Sums, states and softly decayed weights are held in fp32 or more; results
  *   do not depend on timing.
  * - Every call can be captured in a HIP graph and replayed.
+ * - Limits, beyond which a call is refused with GDN_ERR_ARG before anything is
+ *   launched: n_rows up to 2^31 - 1025, n_seqs up to 2^28, a pool of up to
+ *   2^29 - 1 pages, h_v d_k and h_v d_v up to 2^24, a state of up to 2^31 values.
+ *   A launch has 2^23 - 1 workgroups: row by row one for a sequence and value
+ *   head; in chunks one for a segment and value head, of which a batch has up to
+ *   n_seqs + n_rows / 128 + 2, at most n_seqs + 512 / h_v + 2 (backward: or
+ *   n_seqs + n_rows / 2048 + 2, where that is more), and 7 more for each head of
+ *   a key head's; in a call on 8-bit entries one for a pair and 64 blocks of
+ *   GDNL_CACHE_COLS columns.  262,000 sequences of 32 heads are within them.
  */
 #ifndef GDN_LINEAR_H
 #define GDN_LINEAR_H
@@ -68,6 +77,9 @@ typedef struct gdnl_dims {
 
 /* ------------------------------------------------- linear attention */
 
+/* Batches with 0 < max_seqlen <= this are computed row by row. */
+#define GDNL_TOKEN_ROWS 8
+
 /* What a backward call is asked for and given: dg, d_state, d_state0. */
 #define GDNL_ASKS 16
 #define GDNL_ASKS_DG 1
@@ -91,8 +103,9 @@ int32_t gdnl_attend_workspace_bytes(const gdnl_dims* dims, int32_t n_seqs, int64
  * A g below -128 counts as a decay of exactly 0 (so an infinite one begins a
  * sequence anew); NaN stays NaN.  A value that is not finite reaches its own
  * column of o and of the state from its row on and nothing before that.
- * Batches with 0 < max_seqlen <= 8 are computed row by row in one launch,
- * others in chunks of 64 rows on matrix cores. */
+ * Batches with 0 < max_seqlen <= GDNL_TOKEN_ROWS are computed row by row in one
+ * launch without a workspace, others, whatever the lengths of their shorter
+ * sequences, in chunks of 64 rows on matrix cores. */
 int32_t gdnl_attend_forward(const gdnl_dims* dims, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                             const void* v, int64_t v_stride, const float* g, int64_t g_stride,
                             const gdn_batch* batch, gdn_state_pool state_in, gdn_state_pool state_out,

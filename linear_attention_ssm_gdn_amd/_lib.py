@@ -24,7 +24,7 @@ GDN_MIXED_AUTO, GDN_MIXED_ONE_LAUNCH, GDN_MIXED_TWO_LAUNCHES = 0, 1, 2
 GDN_NOALLOC_SYNC_WORDS = 65536
 GDNT_SCAN_BLOCK, GDNT_CKPT_ROWS, GDNT_CKPT_CHANNELS = 256, 16, 4
 GDNT_DEVERR_TIMEOUT = 32
-GDNL_CACHE_COLS = 64
+GDNL_CACHE_COLS, GDNL_TOKEN_ROWS = 64, 8
 GDNL_ASKS, GDNL_ASKS_DG, GDNL_ASKS_D_STATE, GDNL_ASKS_D_STATE0 = 16, 1, 2, 4
 GDNL_NORM_RMS, GDNL_NORM_L2 = 0, 1
 GDNL_PAIRS_HALVES, GDNL_PAIRS_NEIGHBOURS = 0, 1

@@ -13,8 +13,6 @@
 
 namespace {
 
-// Batches whose longest sequence has at most this many rows go row by row.
-constexpr int32_t kTokensMax = 8;
 // Rows of a segment, at least, and workgroups (segments times value heads)
 // from which on segments grow longer instead of more: two to a compute unit
 // (512, 1024, 2048 take 425, 460, 526 us forward and 2165, 2340, 2610 with the
@@ -206,7 +204,7 @@ GDN_EXPORT int32_t gdnl_attend_forward(const gdnl_dims* dims, const void* q, int
         return GDN_ERR_ARG;
     const hipStream_t s = (hipStream_t)stream;
     const int32_t limit = state_in.n_pages < state_out.n_pages ? state_in.n_pages : state_out.n_pages;
-    if (batch->max_seqlen > 0 && batch->max_seqlen <= kTokensMax) {
+    if (batch->max_seqlen > 0 && batch->max_seqlen <= GDNL_TOKEN_ROWS) {
         if ((int64_t)batch->n_seqs * H > kMaxGroups) return GDN_ERR_ARG;
         gdnl::TokenArgs A{};
         A.cu = batch->cu_seqlens; A.page_idx = batch->page_idx; A.has_init = batch->has_init;

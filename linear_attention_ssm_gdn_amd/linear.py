@@ -189,7 +189,7 @@ def gdnl_attend_forward(dims: LinearDims, q: torch.Tensor, k: torch.Tensor, v: t
     vs = _rows2("v", v, n, wv, dt)
     o, os_ = _rows_out("o", o, v, n, wv, dt, dev)
     gs = _gates(g, n, dims.h_v)
-    if workspace is None and 0 < batch.max_seqlen <= 8:
+    if workspace is None and 0 < batch.max_seqlen <= L.GDNL_TOKEN_ROWS:
         ws, ws_bytes = None, 0  # row by row
     else:
         space = _space(workspace, 0 if workspace is not None else gdnl_attend_workspace_bytes(dims, batch.n_seqs, n), dev)
@@ -208,9 +208,9 @@ def gdnl_attend_backward(dims: LinearDims, q: torch.Tensor, k: torch.Tensor, v: 
     """The gradients of gdnl_attend_forward.  state_in: the pages as they were
     before the forward call; d_state [n_seqs][h_v][d_k][d_v] fp32: the gradient
     of the final states.  Rows of no sequence and of padding are left as they are
-    in every output: give zeroed ones where something reads them.  with_dg
-    False, or an `out` whose dg is None: no gradient of the decays, which saves
-    time."""
+    in every output: give zeroed ones where something reads them.  An `out` whose
+    dg is None, or with_dg False where there is no `out`: no gradient of the
+    decays, which saves time."""
     dev, n, dt, s = q.device, batch.n_rows, _TORCH_DT[dims.act_dtype], batch.n_seqs
     wk, wv, one = dims.h_k * dims.d_k, dims.h_v * dims.d_v, g.dim() == 1
     state = (s, dims.h_v, dims.d_k, dims.d_v)

@@ -50,6 +50,29 @@ def test_the_binding_has_the_headers_constants(L):
     header = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "gdn_linear.h")
     with open(header) as f:
         defined = dict(re.findall(r"^#define (GDNL_\w+) (\d+)", f.read(), re.M))
-    assert {"GDNL_ASKS", "GDNL_ASKS_DG", "GDNL_ASKS_D_STATE", "GDNL_ASKS_D_STATE0"} <= set(defined)
+    assert {"GDNL_TOKEN_ROWS", "GDNL_ASKS", "GDNL_ASKS_DG", "GDNL_ASKS_D_STATE", "GDNL_ASKS_D_STATE0"} <= set(defined)
     for name, value in defined.items():
         assert getattr(L, name) == int(value)
+
+
+def test_the_limits_that_the_header_states(L):
+    """At a limit a size is given, beyond it refused; row by row the call itself is."""
+    so, out = L.load(), ctypes.c_size_t()
+    ask = lambda dims, seqs, rows, back: so.gdnl_attend_workspace_bytes(ctypes.byref(L.GdnlDims(*dims, 1.0)), seqs, rows, back, ctypes.byref(out))  # noqa: E731
+    narrow = (1, 1, 1, 1, 0, 0)
+    assert ask(narrow, 1, (1 << 31) - 1025, 0) == 0 and ask(narrow, 1, (1 << 31) - 1024, 0) == 1
+    assert ask((16, 32, 128, 128, 1, 0), 262000, 1 << 20, 0) == 0
+    assert ask((1, 32, 4, 4, 1, 0), 262144, 0, 0) == 1
+    for hv, d, status in ((1 << 24, 1, 1), (1 << 17, 128, 0), ((1 << 17) + 1, 128, 1)):  # h_v d_k at most 2^24
+        assert ask((1, hv, d, 1, 0, 0), 1, 1, 0) == status
+    fake, pool = 0x10000, L.GdnStatePool
+
+    def forward(seqs, pages, max_len=8):
+        d = L.GdnlDims(1, 32, 4, 4, 0, 0, 1.0)
+        b = L.GdnBatch(fake, fake, None, seqs, max_len, 1)
+        return so.gdnl_attend_forward(ctypes.byref(d), fake, 4, fake, 4, fake, 128, fake, 32, ctypes.byref(b), pool(fake, 512, pages),
+                                      pool(fake, 512, pages), fake, 128, None, 0, None, None)
+
+    assert forward(262144, 4) == 1      # 2^23 workgroups
+    assert forward(1, 1 << 29) == 1     # pages
+    assert forward(1, 4, 9) == 1        # in chunks: no workspace
