@@ -107,3 +107,87 @@ def test_decays_of_one_row_expanded_over_all():
     summed = g.gdnl_attend_backward(c.dims, c.t["q"], c.t["k"], c.t["v"], one, c.batch, g.StatePool(c.s0.to(DEV)), c.t["d_o"]).dg
     # the sum of rows rounded one by one: half a step each
     assert ((want["dg"].double().sum(0) - summed.double()).abs() <= 2.0 ** -24 * (want["dg"].double().abs().sum(0) + summed.double().abs())).all()
+
+
+def bad_batch(c, cu, pages=None, max_len=0):
+    g = gdn()
+    return g.Batch(torch.tensor(cu, dtype=torch.int32, device=DEV), c.batch.page_idx if pages is None else pages, None, max_len, c.rows)
+
+
+def check_skipped(c, batch, bit, live, act_rows):
+    """Sequences `live` as in the whole batch, bit for bit, and nothing of others
+    written but zeros into d_state0; act_rows: rows that a live sequence owns."""
+    good_o, good_s = c.forward()
+    good = c.backward()
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    o, so = c.forward(batch=batch, err=err)
+    assert int(err.item()) == bit
+    err.zero_()
+    d = c.backward(batch=batch, err=err)
+    assert int(err.item()) == bit
+    mine = torch.zeros(c.rows, dtype=torch.bool)
+    for r in act_rows:
+        mine[r] = True
+    mine = mine.to(DEV)
+    for a, b in ((o, good_o), (d.dq, good.dq), (d.dk, good.dk), (d.dv, good.dv), (d.dg, good.dg)):
+        assert torch.equal(a[mine], b[mine]) and torch.isnan(a[~mine]).all()
+    pages = host(batch.page_idx).astype(int)
+    for s in range(c.n):
+        if s in live:
+            assert torch.equal(so.buf[pages[s]].nan_to_num(3.0), good_s.buf[c.pages[s]].nan_to_num(3.0))
+            assert torch.equal(d.d_state0[s], good.d_state0[s])
+        else:
+            assert (d.d_state0[s] == 0).all()
+            if pages[s] < len(so.buf) and pages[s] >= 0:
+                assert torch.isnan(so.buf[pages[s]]).all()
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+def test_bad_bounds_beside_sequences_of_several_segments(act):
+    """Sequences of three and more segments stay whole beside one whose bounds
+    decrease, one that begins before an earlier one's end, one beyond the rows,
+    and one whose page is beyond the pools."""
+    g = gdn()
+    lens = [400, 300, 500, 350]
+    c = Case(lens, hk=1, hv=2, dk=16, dv=8, act=act, fast=0.1)
+    rows = [slice(0, 400), slice(400, 700), slice(700, 1200), slice(1200, 1550)]
+    for cu, live in (([0, 400, -2, 1200, 1550], (0, 3)),   # 1: negative end; 2: from -2 on
+                     ([0, 400, 300, 1200, 1550], (0, 3)),  # 1: decreasing; 2: begins within 0
+                     ([0, 400, 700, 1200, 1551], (0, 1, 2))):
+        check_skipped(c, bad_batch(c, cu), g.GDN_DEVERR_BATCH, live, [rows[s] for s in live])
+    pages = c.batch.page_idx.clone()
+    pages[2] = 6  # the pools have 6
+    check_skipped(c, bad_batch(c, [0, 400, 700, 1200, 1550], pages), g.GDN_DEVERR_PAGE, (0, 1, 3), [rows[s] for s in (0, 1, 3)])
+    # longer than max_seqlen: the cut is that of sequences of up to 400 rows, as in a batch told so
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    o, _ = c.forward(batch=bad_batch(c, [0, 400, 700, 1200, 1550], max_len=400), err=err)
+    assert int(err.item()) == g.GDN_DEVERR_BATCH and torch.isnan(o[rows[2]]).all()
+    d = c.backward(batch=bad_batch(c, [0, 400, 700, 1200, 1550], max_len=400), err=err)
+    assert torch.isnan(d.dq[rows[2]]).all() and (d.d_state0[2] == 0).all() and torch.isfinite(d.dq[rows[3]]).all()
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [3, 300])
+def test_bad_bounds_among_more_sequences_than_one_launch_places(act, rows):
+    """More than 256 sequences: segments and decays are two launches, a thread finds a slot's segment."""
+    g = gdn()
+    n = 300
+    lens = [2] * n
+    lens[40], lens[299] = rows, rows
+    c = Case(lens, hk=1, hv=2, dk=8, dv=8, act=act, fast=0.1)
+    cu = [int(v) for v in host(c.batch.cu_seqlens)]
+    starts = list(cu)
+    cu[101] = 0  # 100 decreases, 101 begins before the end of 99
+    live = [s for s in range(n) if s not in (100, 101)]
+    check_skipped(c, bad_batch(c, cu), g.GDN_DEVERR_BATCH, live, [slice(starts[s], starts[s + 1]) for s in live])
+
+
+def test_states_in_place_of_cut_sequences():
+    """A cut sequence's first segment takes the page as it was, whatever the last one has written by then."""
+    c = Case([1300, 70, 900, 257], hk=1, hv=2, dk=32, dv=32, act="bf16", fast=0.01)
+    want_o, want_s = c.forward()
+    for _ in range(5):
+        o, so = c.forward(in_place=True)
+        assert torch.equal(o, want_o)
+        for s in range(c.n):
+            assert torch.equal(so.buf[c.pages[s]], want_s.buf[c.pages[s]])
