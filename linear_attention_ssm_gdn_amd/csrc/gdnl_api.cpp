@@ -441,7 +441,7 @@ GDN_EXPORT int32_t gdnl_rotate_workspace_bytes(const gdnl_rotate_dims* dims, int
     const int32_t st = check_rotate(dims);
     if (st != GDN_OK) return st;
     if (!out_bytes || check_rows(n_rows) != GDN_OK) return GDN_ERR_ARG;
-    *out_bytes = round_up((size_t)gdnl::rotate_groups(n_rows) * 2 * (size_t)dims->d * sizeof(float));
+    *out_bytes = round_up((size_t)gdnl::rotate_groups(n_rows) * 2 * (size_t)dims->d * sizeof(double));
     return GDN_OK;
 }
 
@@ -487,7 +487,7 @@ GDN_EXPORT int32_t gdnl_rotate_backward(const gdnl_rotate_dims* dims, const void
         n_rows = 0;
         if (!sums) return GDN_OK;
     }
-    const size_t need = round_up((size_t)gdnl::rotate_groups(n_rows) * 2 * (size_t)dims->d * sizeof(float));
+    const size_t need = round_up((size_t)gdnl::rotate_groups(n_rows) * 2 * (size_t)dims->d * sizeof(double));
     if (sums && n_rows > 0 && (!workspace || !aligned(workspace, 256) || ws_bytes < need)) return GDN_ERR_ARG;
     gdnl::RotateArgs A = rotate_args(dims, q, q_stride, k, k_stride, wq, wk, pos, inv_freq, n_rows);
     A.dy[0] = d_yq; A.dy[1] = d_yk; A.dy_stride[0] = d_yq_stride; A.dy_stride[1] = d_yk_stride;
@@ -495,7 +495,7 @@ GDN_EXPORT int32_t gdnl_rotate_backward(const gdnl_rotate_dims* dims, const void
     A.vec = A.vec && fours(dims, dims->h_q, d_yq, d_yq_stride) && fours(dims, dims->h_k, d_yk, d_yk_stride) &&
             fours(dims, dims->h_q, dq, dq_stride) && fours(dims, dims->h_k, dk, dk_stride);
     A.dw[0] = dwq; A.dw[1] = dwk;
-    A.part = sums ? static_cast<float*>(workspace) : nullptr;
+    A.part = sums ? static_cast<double*>(workspace) : nullptr;
     return from_hip(gdnl::launch_rotate(A, true, (hipStream_t)stream));
 }
 

@@ -168,7 +168,7 @@ struct RotateArgs {
     int64_t n_rows;
     int32_t heads[2], d, rot, neighbours, bf16, vec;
     float over, eps;             // the sum of squares is divided by `over`
-    float* part; float* dw[2];   // backward: [groups][2][d]
+    double* part; float* dw[2];  // backward: [groups][2][d]
 };
 int64_t rotate_groups(int64_t n_rows);
 hipError_t launch_rotate(const RotateArgs& a, bool back, hipStream_t s);

@@ -8,6 +8,7 @@ import torch
 from gpu_util import DEV, gdn, host
 import test_gpu_rotate
 from linear_util import Case
+from oracle import linear as ol
 
 pytestmark = pytest.mark.gpu
 
@@ -107,6 +108,26 @@ def test_decays_of_one_row_expanded_over_all():
     summed = g.gdnl_attend_backward(c.dims, c.t["q"], c.t["k"], c.t["v"], one, c.batch, g.StatePool(c.s0.to(DEV)), c.t["d_o"]).dg
     # the sum of rows rounded one by one: half a step each
     assert ((want["dg"].double().sum(0) - summed.double()).abs() <= 2.0 ** -24 * (want["dg"].double().abs().sum(0) + summed.double().abs())).all()
+
+
+@pytest.mark.parametrize("act", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,shape", [(1 << 20, dict(hq=8, hk=0, d=4)), (20000, dict(hq=3, hk=9, d=80, pairs="neighbours")), (20000, dict(hq=2, hk=2, d=256))])
+def test_weights_gradients_over_many_rows(rows, act, shape):
+    """The error of a weight's gradient does not grow with the rows beyond its
+    terms' root sum of squares r.  A term dy x / |x| is off by four half steps of
+    2^-24 at random, 4 / 3^(1/2); a sum of 32 of them in fp32 by a half step of
+    each of its partial sums, of i^(1/2) terms: (32 / 2 / 3)^(1/2); together 3.3
+    half steps of r in the norm, below 4.  Summed in fp32 throughout, 512 terms to
+    a lane are off by (512 / 2 / 3)^(1/2) = 9."""
+    c = test_gpu_rotate.Case(rows, act=act, rot=0, **shape)
+    got = gdn().gdnl_rotate_backward(*c.args(), c.dy["q"], c.dy["k"])
+    for t, dw in (("q", got.dwq), ("k", got.dwk)):
+        x, dy = c.heads(c.x[t]), c.heads(c.dy[t])
+        if x.shape[1] == 0:
+            continue
+        terms = dy * x / ol._size(x, c.norm, c.eps)
+        off, r2 = host(dw) - terms.sum((0, 1)), (terms ** 2).sum((0, 1))
+        assert np.sqrt((off ** 2).sum() / r2.sum()) <= 4 * 2.0 ** -24
 
 
 def bad_batch(c, cu, pages=None, max_len=0):
