@@ -8,7 +8,8 @@
 //
 // The angle pos * inv_freq is an fp64 product, reduced to a fraction of a turn
 // in fp64 (for a position of 10^6 its last digits in fp32 are half a radian),
-// and its sine and cosine are made once for a row, for all its heads, in LDS.
+// and its sine and cosine are made once for a row, for all its heads, in LDS:
+// those of the fraction in fp32, and to first order what that rounding left.
 //
 // Bound by the bytes of x and y: 32768 rows of 48 heads of 128 in bf16 take 146-169
 // us forward (5.1 TB/s at the middle) and 270-330 us backward.
@@ -145,8 +146,10 @@ __global__ __launch_bounds__(kThreads) void k_rotate(const RotateArgs A, int row
             const int r = j / nr, p = j - r * nr;
             const double turns = (double)A.pos[r0 + r] * (double)A.inv_freq[p] * 0.15915494309189535;
             float sn, cs;
-            sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cs);
-            s_turn[r][p] = make_float2(cs, sn);
+            const double part = turns - rint(turns);
+            const float near = (float)part, off = (float)(part - (double)near) * 6.2831853f;
+            sincospif(2.0f * near, &sn, &cs);
+            s_turn[r][p] = make_float2(fmaf(-off, sn, cs), fmaf(off, cs, sn));
         }
         __syncthreads();
         for (int u = grp; u < rows * heads; u += kHeadsAtOnce) {

@@ -110,6 +110,27 @@ def test_decays_of_one_row_expanded_over_all():
     assert ((want["dg"].double().sum(0) - summed.double()).abs() <= 2.0 ** -24 * (want["dg"].double().abs().sum(0) + summed.double().abs())).all()
 
 
+def test_angles_near_half_a_turn():
+    """Values of 1 turned against 0 are cosine and sine of the angle, off by the
+    library's two ulps and two roundings, six half steps of 2^-24 of themselves,
+    where a sine is near 0 too: a fraction of a turn rounded to fp32 alone would
+    be off by up to 2 pi 2^-26 whatever its size.  2^-45 is for the angle's own
+    rounding in 64 bits, of up to 2^19 radians."""
+    rows = 5000
+    rng = np.random.default_rng(3)
+    g = gdn()
+    inv = np.array([np.pi, 1.0], np.float32)
+    pos = rng.integers(-100000, 100000, rows).astype(np.int32)
+    q = torch.zeros(rows, 4, device=DEV)
+    q[:, :2] = 1.0  # pairs (0, 2) and (1, 3)
+    y, _ = g.gdnl_rotate_forward(g.RotateDims(1, 0, 4, 4, act_dtype="f32", norm="l2", eps=0.0), q, q[:, :0], None, None,
+                                 torch.from_numpy(pos).to(DEV), torch.from_numpy(inv).to(DEV))
+    y = host(y) / float(np.float32(1.0) / np.sqrt(np.float32(2.0)))
+    angle = pos[:, None].astype(np.float64) * inv.astype(np.float64)
+    for got, want in ((y[:, :2], np.cos(angle)), (y[:, 2:], np.sin(angle))):
+        assert (np.abs(got - want) <= 6 * 2.0 ** -24 * np.abs(want) + 2.0 ** -45).all(), np.abs(got - want).max() * 2 ** 24
+
+
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,shape", [(1 << 20, dict(hq=8, hk=0, d=4)), (20000, dict(hq=3, hk=9, d=80, pairs="neighbours")), (20000, dict(hq=2, hk=2, d=256))])
 def test_weights_gradients_over_many_rows(rows, act, shape):
