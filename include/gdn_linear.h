@@ -152,7 +152,8 @@ int32_t gdnl_rotate_workspace_bytes(const gdnl_rotate_dims* dims, int64_t n_rows
 /* For every head x of a row: n = x / sqrt(mean or sum of x^2 + eps) * w, then
  * the first `rot` values turned in pairs by the angle pos * inv_freq[i]:
  *   (a, b) -> (a cos - b sin, b cos + a sin),
- * the angle taken in 64 bits, the rest in fp32, one rounding at the end.
+ * the angle taken in 64 bits, the rest in fp32, one rounding at the end; the
+ * norm is a number for every head of numbers, the largest and smallest too.
  *   q, yq: [n_rows][stride >= h_q*d]; k, yk: [n_rows][stride >= h_k*d] act
  *   dtype; wq, wk: fp32 [d] or NULL (ones); pos: int32 [n_rows]; inv_freq:
  *   fp32 [rot/2].

@@ -15,18 +15,18 @@ namespace {
 
 // Rows of a segment, at least, and workgroups (segments times value heads)
 // from which on segments grow longer instead of more: two to a compute unit
-// (512, 1024, 2048 take 425, 460, 526 us forward and 2165, 2340, 2610 with the
+// (512, 1024, 2048 take 467, 490, 545 us forward and 2175, 2320, 2605 with the
 // backward pass over 4 x 8192 rows of 32 heads), and one where segments are short
-// and states wide, whose reading and writing then counts (256 and 512 take 75 and
-// 90 us over 2000 rows of 32 heads of 128 x 128, 96 and 110 us over 4000).
+// and states wide, whose reading and writing then counts (256 and 512 take 71 and
+// 80 us over 2000 rows of 32 heads of 128 x 128, 93 and 100 us over 4000).
 constexpr int32_t kSegMin = 128, kSegShort = 512;
 constexpr int64_t kSegGroups = 512;
 // Batches whose longest sequence has at most kSegNone rows are not cut, the states
 // between segments costing two more launches and another reading of k and v; where
 // sequences times heads are fewer than kSegFew, batches of at most kSegFewNone
-// (900 rows of 8 heads 87 us uncut and 42 cut, 4 x 1000 rows of 32 heads 104 and
-// 132), and fewer than twice as many for fp32 rows, whose chunks take longer (4 x
-// 1000 rows of 32 heads 240 uncut and 205 cut, 8 prompts of up to 656 172 and 211).
+// (900 rows of 8 heads 93 us uncut and 40 cut, 4 x 1000 rows of 32 heads 107 and
+// 139), and fewer than twice as many for fp32 rows, whose chunks take longer (4 x
+// 1000 rows of 32 heads 240 uncut and 205 cut, 8 prompts of up to 656 167 and 189).
 constexpr int32_t kSegNone = 1024, kSegFewNone = 256;
 constexpr int64_t kSegFew = 128;
 // A backward pass takes no longer ones: the gradients of the decays are sums over

@@ -23,10 +23,10 @@
 // split into three terms of eight bits, which leave nothing: states are as good
 // as their fp32 sums, outputs as these rounded once.
 //
-// What bounds it: issue.  Over 4 x 8192 rows of 32 heads of 128 x 128 in bf16 the
-// outputs take 290-320 us, some 660 vector and 98 matrix instructions a wave and
-// chunk, busy 62% and 37% of the time; the 0.93 GB would take 180 us at a copy's
-// rate.  fp32 rows are bound by the matrix instructions (68% busy, 85 TFLOP/s over
+// What bounds it: vector and matrix instructions, on units of their own, and waits
+// between them.  Over 4 x 8192 rows of 32 heads of 128 x 128 in bf16 the outputs take
+// 320-345 us, some 650 vector and 119 matrix instructions a wave and chunk, busy 66%
+// and 41% of the time; the 0.9 GB would take 175 us at a copy's rate.  fp32 rows are bound by the matrix instructions (68% busy, 85 TFLOP/s over
 // 16384 rows).  Why eight waves of 16 columns: two workgroups then fit a compute
 // unit's registers (128 a lane) and LDS, and one computes while the other waits at
 // a barrier; four waves of 32 columns were no faster.  Chunks of 64 rows: with 32
@@ -461,8 +461,8 @@ __global__ __launch_bounds__(64 * W, (Layout<T, DK, W, NT, MODE, back>::kWavesPe
     using Y = Layout<T, DK, W, NT, MODE, back>;
     using TK = Tile<T, DK>;
     using TV = Tile<T, Y::DV>;
-    // KG sums of the state's update in turn; fewer where a fourth tile's rows are in registers (a spill there waits for
-    // memory: 485 us with four, 400 with two, kDotRows over 32768 rows of 32 heads)
+    // KG sums of the state's update in turn; fewer where a fourth tile's rows are in registers (with four kDotRows takes
+    // 17 us more over 32768 rows of 32 heads, of 430)
     constexpr int KG = Y::kX ? 2 : 4, M = DK / 16, KS = DK / 32, TH = 64 * W;
     __shared__ __attribute__((aligned(16))) char lds[Y::kBytes];
     char* const tk = lds + Y::oK;

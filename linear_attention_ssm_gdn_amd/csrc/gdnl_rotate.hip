@@ -11,8 +11,8 @@
 // and its sine and cosine are made once for a row, for all its heads, in LDS:
 // those of the fraction in fp32, and to first order what that rounding left.
 //
-// Bound by the bytes of x and y: 32768 rows of 48 heads of 128 in bf16 take 146-169
-// us forward (5.1 TB/s at the middle) and 270-330 us backward.
+// Bound by the bytes of x and y: 32768 rows of 48 heads of 128 in bf16 take 146-172
+// us forward (5.1 TB/s at the middle) and 280-349 us backward.
 #include "gdn_device.hpp"
 #include "gdnl_kernels.h"
 
